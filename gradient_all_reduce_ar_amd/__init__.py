@@ -1,6 +1,8 @@
 """MI355X-native gradient all-reduce schedules (ring, hierarchical, Rabenseifner,
 recursive doubling, binary and double binary trees; fp32, bf16 and blockwise
-INT8 with error feedback).
+INT8 with error feedback), and what stands around them in a training step: the
+products of a mixture of experts (whose weight gradients fill the arenas) and
+the Muon update of the reduced gradients.
 
 The compute path is the HIP library libar.so (csrc/), reached through the
 C ABI declared in include/ar.h; this package only marshals arguments.
@@ -17,4 +19,7 @@ from ._binding import (  # noqa: F401
     ar_plan_launch_scratch, ar_plan_launch_times, ar_plan_num_launches, ar_plan_owned_range, ar_plan_prepare,
     ar_plan_set_cache_bytes, ar_plan_set_exec, ar_plan_set_graph, ar_plan_set_profiling,
     ar_plan_set_profiling_period, ar_plan_stats, ar_plan_transfers, ar_reduce_scatter, ar_select_schedule,
+    ar_experts_create, ar_experts_destroy, ar_experts_forward, ar_experts_input_grad, ar_experts_prepare,
+    ar_experts_stats, ar_experts_weight_grad, ar_muon_plan_create, ar_muon_plan_destroy, ar_muon_plan_prepare,
+    ar_muon_plan_set_iterations, ar_muon_plan_set_scales, ar_muon_plan_stats, ar_muon_step, ar_orthogonalize,
 )

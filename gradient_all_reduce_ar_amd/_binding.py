@@ -52,6 +52,23 @@ class ar_cost_params_t(ctypes.Structure):
                 ("bw_group_egress_Bps", ctypes.c_double), ("egress_share", ctypes.c_double)]
 
 
+class ar_experts_stats_t(ctypes.Structure):
+    _fields_ = [("nexperts", ctypes.c_int32), ("device", ctypes.c_int32), ("in_features", ctypes.c_uint64),
+                ("out_features", ctypes.c_uint64), ("elem_bytes", ctypes.c_uint64), ("grad_bytes", ctypes.c_uint64),
+                ("arena_count", ctypes.c_uint64)]
+
+
+class ar_muon_stats_t(ctypes.Structure):
+    _fields_ = [("nmatrices", ctypes.c_int32), ("device", ctypes.c_int32), ("iterations", ctypes.c_int32),
+                ("launches", ctypes.c_int32), ("grad_bytes", ctypes.c_uint64), ("weight_bytes", ctypes.c_uint64),
+                ("arena_count", ctypes.c_uint64), ("workspace_bytes", ctypes.c_uint64)]
+
+
+class ar_muon_params_t(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("momentum", ctypes.c_double), ("weight_decay", ctypes.c_double),
+                ("grad_scale", ctypes.c_double), ("nesterov", ctypes.c_int32)]
+
+
 class ar_stats_t(ctypes.Structure):
     _fields_ = [
         ("nranks", ctypes.c_int32), ("group_size", ctypes.c_int32),
@@ -142,6 +159,21 @@ def _declare(L):
                                   ctypes.POINTER(dbl)], dbl),
         "ar_bucket_stats": ([P], ar_stats_t),
         "ar_bucket_plan_destroy": ([P], None),
+        "ar_experts_create": ([ctypes.c_int, sz, sz, ctypes.c_int, ctypes.c_int, psz], P),
+        "ar_experts_prepare": ([P], ctypes.c_int),
+        "ar_experts_stats": ([P], ar_experts_stats_t),
+        "ar_experts_forward": ([P, P, sz, P, P, sz, P, sz, P], ctypes.c_int),
+        "ar_experts_input_grad": ([P, P, sz, P, P, sz, P, sz, P], ctypes.c_int),
+        "ar_experts_weight_grad": ([P, P, sz, P, sz, P, ctypes.c_int, P, sz, P], ctypes.c_int),
+        "ar_experts_destroy": ([P], None),
+        "ar_muon_plan_create": ([ctypes.c_int, psz, psz, psz, ctypes.c_int, ctypes.c_int], P),
+        "ar_muon_plan_set_iterations": ([P, ctypes.c_int, ctypes.POINTER(dbl)], ctypes.c_int),
+        "ar_muon_plan_set_scales": ([P, ctypes.POINTER(dbl)], ctypes.c_int),
+        "ar_muon_plan_prepare": ([P], ctypes.c_int),
+        "ar_muon_plan_stats": ([P], ar_muon_stats_t),
+        "ar_orthogonalize": ([P, P, P, P], ctypes.c_int),
+        "ar_muon_step": ([P, P, P, P, P, P, ctypes.POINTER(ar_muon_params_t), P], ctypes.c_int),
+        "ar_muon_plan_destroy": ([P], None),
     }
     for name, (args, res) in sig.items():
         f = getattr(L, name)
@@ -638,3 +670,209 @@ def ar_bucket_stats(bp):
 
 def ar_bucket_plan_destroy(bp):
     lib().ar_bucket_plan_destroy(bp)
+
+
+# ------------------------------------------- products grouped by expert
+
+def _check_device(t, device, what):
+    """A tensor's device has to be the plan's (device: -1 before it is known)."""
+    if device >= 0 and hasattr(t, "device") and t.device.index not in (None, device):
+        raise ValueError(f"{what} is on device {t.device.index}; the plan is on device {device}")
+
+
+def _rows(t, stride, rows, features, elem, device, what):
+    """(pointer, row stride in elements) of a [rows, features] argument: a
+    device tensor whose rows are contiguous, or an address with its stride."""
+    if not hasattr(t, "data_ptr"):
+        return _ptr(t), features if stride is None else int(stride)
+    if stride is not None:
+        raise ValueError(f"{what}: a tensor brings its own stride")
+    if not getattr(t, "is_cuda", False):
+        raise ValueError(f"{what} is not a device tensor")
+    _check_device(t, device, what)
+    if t.dim() != 2 or t.element_size() != elem or tuple(t.shape) != (rows, features):
+        raise ValueError(f"{what} is {tuple(t.shape)} of {t.element_size()} bytes; wanted ({rows}, {features}) of {elem}")
+    if features > 1 and rows > 0 and t.stride(1) != 1:
+        raise ValueError(f"{what}: rows are not contiguous")
+    return t.data_ptr(), t.stride(0) if rows > 1 else features
+
+
+def _arena(t, count, elem, device, what):
+    """Pointer of an arena of at least count elements: a contiguous device
+    tensor, or an address."""
+    if not hasattr(t, "data_ptr"):
+        return _ptr(t)
+    if not getattr(t, "is_cuda", False):
+        raise ValueError(f"{what} is not a device tensor")
+    _check_device(t, device, what)
+    if not t.is_contiguous():
+        raise ValueError(f"{what} is not contiguous")
+    if t.element_size() != elem or t.numel() < count:
+        raise ValueError(f"{what} holds {t.numel()} elements of {t.element_size()} bytes; wanted {count} of {elem}")
+    return t.data_ptr()
+
+
+def _tokens(rows, ntokens, what):
+    if ntokens is not None:
+        return int(ntokens)
+    if not hasattr(rows, "shape"):
+        raise ValueError(f"{what} is an address: ntokens is needed")
+    return int(rows.shape[0])
+
+
+def _ends(ends, nexperts, device):
+    if not hasattr(ends, "data_ptr"):
+        return _ptr(ends)
+    if not getattr(ends, "is_cuda", False):
+        raise ValueError("ends is not a device tensor")
+    _check_device(ends, device, "ends")
+    if ends.element_size() != 4 or ends.is_floating_point() or not ends.is_contiguous() or ends.numel() < nexperts:
+        raise ValueError(f"ends: wanted {nexperts} contiguous int32")
+    return ends.data_ptr()
+
+
+def ar_experts_create(nexperts, in_features, out_features, dtype, grad_dtype=None, weight_offsets=None):
+    """dtype, grad_dtype: "fp32" or "bf16" (grad_dtype None: dtype); weight_offsets: first element of each
+    expert's [out_features, in_features] matrix in its arena (None: back to back)."""
+    if weight_offsets is not None and len(weight_offsets) != nexperts:
+        raise ValueError(f"{len(weight_offsets)} weight offsets for {nexperts} experts")
+    offs = None if weight_offsets is None else (ctypes.c_size_t * max(nexperts, 1))(*[int(o) for o in weight_offsets])
+    d = _code(DTYPES, dtype)
+    p = lib().ar_experts_create(nexperts, in_features, out_features, d,
+                                d if grad_dtype is None else _code(DTYPES, grad_dtype), offs)
+    if not p:
+        _raise()
+    return p
+
+
+def ar_experts_prepare(plan):
+    _check(lib().ar_experts_prepare(plan))
+
+
+def ar_experts_stats(plan):
+    s = lib().ar_experts_stats(plan)
+    return {k: getattr(s, k) for k, _ in s._fields_}
+
+
+def _experts_rows_call(fn, plan, rows, weights, out, ends, stream, ntokens, stride, out_stride, names, features):
+    s = lib().ar_experts_stats(plan)
+    n = _tokens(rows, ntokens, names[0])
+    fi, fo = (s.in_features, s.out_features) if features == "in" else (s.out_features, s.in_features)
+    p, ps = _rows(rows, stride, n, fi, s.elem_bytes, s.device, names[0])
+    o, os_ = _rows(out, out_stride, n, fo, s.elem_bytes, s.device, names[1])
+    w = _arena(weights, s.arena_count, s.elem_bytes, s.device, "weights")
+    _check(fn(plan, p, ps, w, o, os_, _ends(ends, s.nexperts, s.device), n, _stream(stream)))
+
+
+def ar_experts_forward(plan, x, weights, y, ends, stream=None, ntokens=None, x_stride=None, y_stride=None):
+    """y[t] = W_e x[t] for the rows t of expert e.  x [tokens, in], y [tokens, out]: tensors with contiguous
+    rows, or addresses (then ntokens, and the strides if rows are not dense); ends: int32 on the device."""
+    if not plan:
+        _check(lib().ar_experts_forward(plan, None, 0, None, None, 0, None, 0, None))
+    _experts_rows_call(lib().ar_experts_forward, plan, x, weights, y, ends, stream, ntokens, x_stride, y_stride,
+                       ("x", "y"), "in")
+
+
+def ar_experts_input_grad(plan, dy, weights, dx, ends, stream=None, ntokens=None, dy_stride=None, dx_stride=None):
+    """dx[t] = W_e^T dy[t] for the rows t of expert e (arguments as ar_experts_forward's)."""
+    if not plan:
+        _check(lib().ar_experts_input_grad(plan, None, 0, None, None, 0, None, 0, None))
+    _experts_rows_call(lib().ar_experts_input_grad, plan, dy, weights, dx, ends, stream, ntokens, dy_stride,
+                       dx_stride, ("dy", "dx"), "out")
+
+
+def ar_experts_weight_grad(plan, x, dy, grads, ends, accumulate=False, stream=None, ntokens=None, x_stride=None,
+                           dy_stride=None):
+    """dW_e = (old dW_e +) the sum over e's rows t of dy[t] x[t]^T, into the gradient arena."""
+    L = lib()
+    if not plan:
+        _check(L.ar_experts_weight_grad(plan, None, 0, None, 0, None, 0, None, 0, None))
+    s = L.ar_experts_stats(plan)
+    n = _tokens(x, ntokens, "x")
+    xp, xs = _rows(x, x_stride, n, s.in_features, s.elem_bytes, s.device, "x")
+    dp, ds = _rows(dy, dy_stride, n, s.out_features, s.elem_bytes, s.device, "dy")
+    g = _arena(grads, s.arena_count, s.grad_bytes, s.device, "grads")
+    _check(L.ar_experts_weight_grad(plan, xp, xs, dp, ds, g, 1 if accumulate else 0,
+                                    _ends(ends, s.nexperts, s.device), n, _stream(stream)))
+
+
+def ar_experts_destroy(plan):
+    lib().ar_experts_destroy(plan)
+
+
+# ------------------------------------------------- Newton-Schulz and Muon
+
+def ar_muon_plan_create(shapes, grad_dtype, weight_dtype, offsets=None):
+    """shapes: (rows, cols) of each matrix; offsets: first element of each in every arena (None: back to back)."""
+    n = len(shapes)
+    if offsets is not None and len(offsets) != n:
+        raise ValueError(f"{len(offsets)} offsets for {n} matrices")
+    arr = ctypes.c_size_t * max(n, 1)
+    rows, cols = arr(*[int(r) for r, _ in shapes]), arr(*[int(c) for _, c in shapes])
+    offs = None if offsets is None else arr(*[int(o) for o in offsets])
+    p = lib().ar_muon_plan_create(n, rows, cols, offs, _code(DTYPES, grad_dtype), _code(DTYPES, weight_dtype))
+    if not p:
+        _raise()
+    return p
+
+
+def ar_muon_plan_set_iterations(plan, n, coefficients=None):
+    """coefficients: n triples (a, b, c), or None for the default ones in each of the n steps."""
+    abc = None
+    if coefficients is not None:
+        flat = [float(v) for t in coefficients for v in t]
+        if len(flat) != 3 * n:
+            raise ValueError(f"{len(flat)} coefficients for {n} steps of three")
+        abc = (ctypes.c_double * max(len(flat), 1))(*flat)
+    _check(lib().ar_muon_plan_set_iterations(plan, n, abc))
+
+
+def ar_muon_plan_set_scales(plan, scales=None):
+    """scales: one factor per matrix, or None for sqrt(max(1, rows / cols))."""
+    arr = None
+    if scales is not None:
+        n = lib().ar_muon_plan_stats(plan).nmatrices if plan else 0
+        if len(scales) != n:
+            raise ValueError(f"{len(scales)} scales for {n} matrices")
+        arr = (ctypes.c_double * max(n, 1))(*[float(v) for v in scales])
+    _check(lib().ar_muon_plan_set_scales(plan, arr))
+
+
+def ar_muon_plan_prepare(plan):
+    _check(lib().ar_muon_plan_prepare(plan))
+
+
+def ar_muon_plan_stats(plan):
+    s = lib().ar_muon_plan_stats(plan)
+    return {k: getattr(s, k) for k, _ in s._fields_}
+
+
+def ar_orthogonalize(plan, grads, out, stream=None):
+    """out = Newton-Schulz of every matrix of the gradient arena (out in the plan's weight type)."""
+    L = lib()
+    if not plan:
+        _check(L.ar_orthogonalize(plan, None, None, None))
+    s = L.ar_muon_plan_stats(plan)
+    g = _arena(grads, s.arena_count, s.grad_bytes, s.device, "grads")
+    o = _arena(out, s.arena_count, s.weight_bytes, s.device, "out")
+    _check(L.ar_orthogonalize(plan, g, o, _stream(stream)))
+
+
+def ar_muon_step(plan, grads, momentum, weights, lr, mu=0.95, weight_decay=0.0, grad_scale=1.0, nesterov=True,
+                 momentum_out=None, weights_out=None, stream=None):
+    """One Muon step on the arenas; momentum (fp32) and weights are updated in place unless the outputs are given."""
+    L = lib()
+    prm = ar_muon_params_t(lr, mu, weight_decay, grad_scale, 1 if nesterov else 0)
+    if not plan:
+        _check(L.ar_muon_step(plan, None, None, None, None, None, ctypes.byref(prm), None))
+    s = L.ar_muon_plan_stats(plan)
+    g = _arena(grads, s.arena_count, s.grad_bytes, s.device, "grads")
+    m = _arena(momentum, s.arena_count, 4, s.device, "momentum")
+    w = _arena(weights, s.arena_count, s.weight_bytes, s.device, "weights")
+    mo = None if momentum_out is None else _arena(momentum_out, s.arena_count, 4, s.device, "momentum_out")
+    wo = None if weights_out is None else _arena(weights_out, s.arena_count, s.weight_bytes, s.device, "weights_out")
+    _check(L.ar_muon_step(plan, g, m, w, mo, wo, ctypes.byref(prm), _stream(stream)))
+
+
+def ar_muon_plan_destroy(plan):
+    lib().ar_muon_plan_destroy(plan)

@@ -12,7 +12,7 @@ LIB = os.path.join(HERE, "libar.so")
 LIB_SANITIZED = os.path.join(HERE, "libar_sanitized.so")
 SANITIZE_FLAGS = "-Xarch_host -fsanitize=address -Xarch_host -fsanitize=undefined " \
                  "-Xarch_host -fno-sanitize-recover=undefined -Xarch_host -fno-omit-frame-pointer".split()
-SOURCES = ["plan.cpp", "kernels.hip", "qkernels.hip", "capi.hip"]
+SOURCES = ["plan.cpp", "kernels.hip", "qkernels.hip", "capi.hip", "experts.hip", "muon.hip", "oapi.hip"]
 
 # -ffp-contract=off and no fast-math: every add is one IEEE binary32 add.
 # -fno-gpu-flush-denormals-to-zero: fp32 denormals are kept on the device.

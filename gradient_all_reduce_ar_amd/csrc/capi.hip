@@ -22,24 +22,18 @@
 #include <vector>
 
 #include "../../include/ar.h"
+#include "host.hpp"
 #include "kernels.hpp"
 #include "plan.hpp"
 
 namespace {
 
-// The value of a C enum argument as an integer, read from its bytes: a
-// caller may pass any int, and loading a value outside the enumerators as
-// the C++ enum type is undefined behaviour.  The planner validates it.
-template <class E>
-int32_t raw_enum(const E &v) {
-  static_assert(sizeof(E) == sizeof(int32_t), "C enums are int-sized");
-  int32_t r;
-  std::memcpy(&r, &v, sizeof r);
-  return r;
-}
-
 thread_local std::string g_err;
 thread_local ar_status_t g_status = AR_OK;
+
+}  // namespace
+
+namespace ar_host {
 
 ar_status_t fail(ar_status_t st, const std::string &msg) {
   g_status = st;
@@ -51,7 +45,11 @@ ar_status_t hip_fail(hipError_t e, const char *what) {
   return fail(AR_ERR_HIP, std::string(what) + ": " + hipGetErrorString(e));
 }
 
-}  // namespace
+}  // namespace ar_host
+
+using ar_host::fail;
+using ar_host::hip_fail;
+using ar_host::raw_enum;
 
 struct ar_plan {
   ar::Plan p;

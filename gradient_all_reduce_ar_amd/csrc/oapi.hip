@@ -1,0 +1,750 @@
+// oapi.hip -- C ABI (include/ar.h) of the expert products and of the Muon
+// update: argument checks, the plans' device tables, and the launches.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <new>
+#include <string>
+#include <vector>
+
+#include "../../include/ar.h"
+#include "host.hpp"
+#include "kernels.hpp"
+#include "operators.hpp"
+
+using ar_host::fail;
+using ar_host::hip_fail;
+using ar_host::raw_enum;
+
+namespace ar_host {
+
+ar_status_t CallMarks::of(hipStream_t s, hipEvent_t *ev) {
+  *ev = nullptr;
+  hipStreamCaptureStatus cs = hipStreamCaptureStatusNone;
+  hipError_t e = hipStreamIsCapturing(s, &cs);
+  if (e != hipSuccess) return hip_fail(e, "hipStreamIsCapturing");
+  if (cs != hipStreamCaptureStatusNone) return AR_OK;
+  for (const Mark &m : marks_)
+    if (m.stream == s) {
+      *ev = m.event;
+      return AR_OK;
+    }
+  if (marks_.size() >= kMax) {  // retire the oldest stream's mark
+    (void)hipEventSynchronize(marks_.front().event);
+    (void)hipEventDestroy(marks_.front().event);
+    marks_.erase(marks_.begin());
+  }
+  marks_.reserve(kMax);
+  e = hipEventCreate(ev);  // with timing: a dispatch can record it
+  if (e != hipSuccess) {
+    *ev = nullptr;
+    return hip_fail(e, "hipEventCreate");
+  }
+  marks_.push_back({s, *ev});
+  return AR_OK;
+}
+
+void CallMarks::wait() const {
+  for (const Mark &m : marks_) (void)hipEventSynchronize(m.event);
+}
+
+void CallMarks::release() {
+  wait();
+  for (const Mark &m : marks_) (void)hipEventDestroy(m.event);
+  marks_.clear();
+}
+
+hipError_t device_table(void **dst, const void *src, size_t bytes) {
+  hipError_t e = hipMalloc(dst, bytes);
+  if (e != hipSuccess) {
+    (void)hipGetLastError();  // clear the sticky allocation error
+    *dst = nullptr;
+    return e;
+  }
+  if (!src) return hipSuccess;
+  // a non-blocking stream and an event: a synchronous copy would go through
+  // the default stream, which ends a capture that another thread has open
+  hipStream_t s = nullptr;
+  hipEvent_t done = nullptr;
+  e = hipStreamCreateWithFlags(&s, hipStreamNonBlocking);
+  if (e == hipSuccess) e = hipEventCreateWithFlags(&done, hipEventDisableTiming);
+  if (e == hipSuccess) e = hipMemcpyAsync(*dst, src, bytes, hipMemcpyHostToDevice, s);
+  if (e == hipSuccess) e = hipEventRecord(done, s);
+  if (e == hipSuccess) e = hipEventSynchronize(done);
+  if (done) (void)hipEventDestroy(done);
+  if (s) (void)hipStreamDestroy(s);
+  if (e != hipSuccess) {
+    (void)hipFree(*dst);
+    *dst = nullptr;
+  }
+  return e;
+}
+
+}  // namespace ar_host
+
+struct ar_experts {
+  int32_t nexperts = 0;
+  int64_t in = 0, out = 0;
+  bool bf16 = false, grad_bf16 = false;
+  std::vector<int64_t> offsets;
+  int64_t arena = 0;         // elements an arena holds at least
+  bool offsets_by_8 = true;  // every matrix starts on a multiple of 8 elements
+  int device = -1;
+  void *d_offsets = nullptr;
+  ar_host::CallMarks marks;
+
+  void release() {
+    marks.release();
+    if (d_offsets) (void)hipFree(d_offsets);
+    d_offsets = nullptr;
+    device = -1;
+  }
+};
+
+namespace {
+
+constexpr int64_t kMaxFeatures = 1 << 22, kMaxStride = 1 << 22;
+
+// [p, p + n) and [q, q + m) share a byte.
+bool overlap(const void *p, int64_t n, const void *q, int64_t m) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return n > 0 && m > 0 && a < b + static_cast<uint64_t>(m) && b < a + static_cast<uint64_t>(n);
+}
+
+bool on(const void *p, uintptr_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
+
+ar_status_t prepare(ar_experts *ex) {
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return hip_fail(e, "hipGetDevice");
+  if (ex->d_offsets) {
+    if (dev != ex->device) return fail(AR_ERR_INVALID_ARG, "expert plan was prepared on another device");
+    return AR_OK;
+  }
+  e = ar_host::device_table(&ex->d_offsets, ex->offsets.data(), ex->offsets.size() * sizeof(int64_t));
+  if (e == hipErrorOutOfMemory) return fail(AR_ERR_OOM, "expert offset table allocation");
+  if (e != hipSuccess) return hip_fail(e, "expert offset table");
+  ex->device = dev;
+  return AR_OK;
+}
+
+// A matrix of `rows` rows of `features` elements, `stride` apart.
+struct RowsArg {
+  const void *p;
+  size_t stride;
+  int64_t features;
+  const char *name;
+};
+
+ar_status_t check_rows(const RowsArg &r, int64_t rows, int64_t elem, int64_t *bytes) {
+  *bytes = 0;
+  if (r.stride < static_cast<size_t>(r.features) || r.stride > static_cast<size_t>(kMaxStride))
+    return fail(AR_ERR_INVALID_ARG, std::string(r.name) + ": row stride must be from its features to 2^22");
+  if (rows == 0) return AR_OK;
+  if (!r.p) return fail(AR_ERR_INVALID_ARG, std::string(r.name) + " is NULL");
+  if (!on(r.p, elem)) return fail(AR_ERR_INVALID_ARG, std::string(r.name) + " is not aligned to its elements");
+  *bytes = ((rows - 1) * static_cast<int64_t>(r.stride) + r.features) * elem;
+  return AR_OK;
+}
+
+enum Which { kForward, kInputGrad, kWeightGrad };
+
+ar_status_t run(ar_experts *ex, Which which, const RowsArg &r1, const RowsArg &r2, const void *arena, bool out_is_rows,
+                bool accumulate, const int32_t *ends, size_t ntokens, void *stream) {
+  if (ntokens > static_cast<size_t>(INT32_MAX)) return fail(AR_ERR_INVALID_ARG, "more than 2^31 - 1 tokens");
+  const int64_t t = static_cast<int64_t>(ntokens), elem = ex->bf16 ? 2 : 4;
+  int64_t b1 = 0, b2 = 0;
+  ar_status_t st = check_rows(r1, t, elem, &b1);
+  if (st == AR_OK) st = check_rows(r2, t, elem, &b2);
+  if (st != AR_OK) return st;
+  const int64_t aelem = which == kWeightGrad ? (ex->grad_bf16 ? 2 : 4) : elem;
+  if (t > 0 || which == kWeightGrad) {
+    if (!ends) return fail(AR_ERR_INVALID_ARG, "ends is NULL");
+    if (!on(ends, 4)) return fail(AR_ERR_INVALID_ARG, "ends is not aligned to its elements");
+    if (!arena) return fail(AR_ERR_INVALID_ARG, "the weight arena is NULL");
+    if (!on(arena, aelem)) return fail(AR_ERR_INVALID_ARG, "the weight arena is not aligned to its elements");
+  }
+  const int64_t ab = ex->arena * aelem, eb = 4 * static_cast<int64_t>(ex->nexperts);
+  if (out_is_rows ? overlap(r2.p, b2, r1.p, b1) || overlap(r2.p, b2, arena, ab) || overlap(r2.p, b2, ends, eb)
+                  : overlap(arena, ab, r1.p, b1) || overlap(arena, ab, r2.p, b2) || overlap(arena, ab, ends, eb))
+    return fail(AR_ERR_INVALID_ARG, "the output overlaps an input");
+  st = prepare(ex);
+  if (st != AR_OK) return st;
+  if (t == 0 && which != kWeightGrad) return AR_OK;
+  ar_dev::ExpertArgs a{};
+  a.offsets = static_cast<const int64_t *>(ex->d_offsets);
+  a.ends = ends;
+  a.tokens = t;
+  a.in = ex->in;
+  a.outf = ex->out;
+  a.experts = ex->nexperts;
+  a.bf16 = ex->bf16;
+  a.grad_bf16 = ex->grad_bf16;
+  a.accumulate = accumulate;
+  const bool rows16 = on(r1.p, 16) && r1.stride % 8 == 0;
+  if (which == kWeightGrad) {
+    a.x = r1.p;
+    a.xs = static_cast<int64_t>(r1.stride);
+    a.dy = r2.p;
+    a.dys = static_cast<int64_t>(r2.stride);
+    a.out = const_cast<void *>(arena);
+    a.aligned = rows16 && on(r2.p, 16) && r2.stride % 8 == 0 && ex->in % 8 == 0 && ex->out % 8 == 0;
+    a.vec_out = on(arena, 4 * aelem) && ex->in % 4 == 0 && ex->offsets_by_8;
+  } else {
+    a.w = arena;
+    a.out = const_cast<void *>(r2.p);
+    a.outs = static_cast<int64_t>(r2.stride);
+    (which == kForward ? a.x : a.dy) = r1.p;
+    (which == kForward ? a.xs : a.dys) = static_cast<int64_t>(r1.stride);
+    a.aligned = rows16 && on(arena, 16) && ex->offsets_by_8 && ex->in % 8 == 0 && ex->out % 8 == 0;
+    a.vec_out = on(r2.p, 4 * elem) && r2.stride % 4 == 0;
+  }
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  hipEvent_t mark = nullptr;
+  st = ex->marks.of(s, &mark);
+  if (st != AR_OK) return st;
+  ar_dev::t_launch_events = ar_dev::LaunchEvents{nullptr, mark};
+  const hipError_t e = which == kForward     ? ar_dev::experts_forward(a, s)
+                       : which == kInputGrad ? ar_dev::experts_input_grad(a, s)
+                                             : ar_dev::experts_weight_grad(a, s);
+  ar_dev::t_launch_events = ar_dev::LaunchEvents{};
+  if (e == hipErrorInvalidConfiguration)
+    return fail(AR_ERR_UNSUPPORTED, "expert product larger than one launch grid");
+  return e == hipSuccess ? AR_OK : hip_fail(e, "kernel launch");
+}
+
+// Runs f, turning a failed host allocation into a status.
+template <class F>
+ar_status_t guarded(F f) {
+  try {
+    return f();
+  } catch (const std::bad_alloc &) {
+    return fail(AR_ERR_OOM, "host allocation failed");
+  }
+}
+
+bool float_type(int32_t d) { return d == AR_FLOAT32 || d == AR_BFLOAT16; }
+
+}  // namespace
+
+struct ar_muon_plan {
+  bool g_bf16 = false, w_bf16 = false;
+  int32_t nmatrices = 0;
+  std::vector<ar_dev::MuonMat> mats;  // those with elements; scale from scales
+  std::vector<int32_t> index;         // their numbers
+  int64_t arena = 0;                  // elements an arena holds at least
+  std::vector<ar_dev::MuonStep> steps;
+  int32_t ex0 = 0;
+  // work lists, one after another, and the sizes of the workspace
+  std::vector<ar_dev::MuonTile> tiles;
+  int32_t nparts = 0, nblocks = 0, nsym = 0, nfull = 0, shape_sym = 0, shape_full = 0;
+  size_t mats_bytes = 0, tiles_bytes = 0, partial_bytes = 0, ws_bytes = 0;
+  int device = -1;
+  void *d_mats = nullptr, *d_tiles = nullptr, *d_work = nullptr;  // d_work: partials, then X, A and B
+  ar_host::CallMarks marks;
+
+  void release() {
+    marks.release();
+    for (void **p : {&d_mats, &d_tiles, &d_work}) {
+      if (*p) (void)hipFree(*p);
+      *p = nullptr;
+    }
+    device = -1;
+  }
+};
+
+namespace {
+
+using ar_dev::MuonMat;
+using ar_dev::MuonStep;
+using ar_dev::MuonTile;
+
+constexpr double kNsA = 3.4445, kNsB = -4.7750, kNsC = 2.0315;
+constexpr int kNsSteps = 5;
+
+// The largest |f| of f(t) = a + b t + c t^2 over [0, s].
+double quad_bound(double a, double b, double c, double s) {
+  double m = std::max(std::fabs(a), std::fabs(a + b * s + c * s * s));
+  if (c != 0) {
+    const double t = -b / (2 * c);
+    if (t > 0 && t < s) m = std::max(m, std::fabs(a + b * t + c * t * t));
+  }
+  return m;
+}
+
+// The largest |sigma f(sigma^2)| over [0, s].
+double step_bound(double a, double b, double c, double s) {
+  auto p = [&](double x) { return std::fabs(x * (a + x * x * (b + x * x * c))); };
+  double m = p(s);
+  // extremes: a + 3 b t + 5 c t^2 = 0 in t = sigma^2
+  double roots[2];
+  int n = 0;
+  if (c == 0) {
+    if (b != 0) roots[n++] = -a / (3 * b);
+  } else {
+    const double d = 9 * b * b - 20 * a * c;
+    if (d >= 0) {
+      roots[n++] = (-3 * b + std::sqrt(d)) / (10 * c);
+      roots[n++] = (-3 * b - std::sqrt(d)) / (10 * c);
+    }
+  }
+  for (int i = 0; i < n; ++i)
+    if (roots[i] > 0 && roots[i] < s * s) m = std::max(m, p(std::sqrt(roots[i])));
+  return m;
+}
+
+// The power of two that takes a number of at most `bound` (and 1/16 more, for
+// what rounding adds) to at most 2^15.
+int32_t scale_exp(double bound) { return 15 - static_cast<int32_t>(std::ceil(std::log2(std::max(bound, 1e-6) * 1.0625))); }
+
+// The steps' factors; false where a bound is passed.
+bool make_steps(int n, const double *abc, bool pair_ab, std::vector<MuonStep> &steps, int32_t &ex0) {
+  steps.clear();
+  double s = 1;  // largest singular value; X_0's Frobenius norm is at most 1
+  ex0 = scale_exp(s);
+  for (int i = 0; i < n; ++i) {
+    const double a = abc ? abc[3 * i] : kNsA, b = abc ? abc[3 * i + 1] : kNsB, c = abc ? abc[3 * i + 2] : kNsC;
+    if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c)) return false;
+    MuonStep k{};
+    k.coef_a = static_cast<float>(a);
+    k.coef_b = static_cast<float>(b);
+    k.coef_c = static_cast<float>(c);
+    k.ex = scale_exp(s);
+    k.ea = scale_exp(s * s);
+    const double q = quad_bound(a, b, c, s * s);
+    const double next = step_bound(a, b, c, s);
+    // the terms of B are formed before they are added
+    const double terms = std::fabs(a) + std::fabs(b) * s * s + std::fabs(c) * s * s * s * s;
+    if (!(terms <= 1 << 14) || !(next <= 1 << 10)) return false;
+    k.eb = scale_exp(q);
+    s = next;
+    k.ex_next = scale_exp(s);
+    k.last = i + 1 == n;
+    // the last step's X may be one fp16 where the others are: nothing
+    // amplifies its rounding any more
+    k.pair_ab = pair_ab;
+    k.pair_x = pair_ab || !k.last;
+    k.pair_next = pair_ab || i + 2 < n;
+    k.from = i & 1;
+    steps.push_back(k);
+  }
+  return true;
+}
+
+int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
+
+// Work lists and workspace layout.
+void lay_out(ar_muon_plan *p) {
+  p->tiles.clear();
+  const bool pair_ab = !p->w_bf16;
+  int64_t ws = 0, part0 = 0;
+  auto take = [&](int64_t n) {
+    const int64_t at = ws;
+    ws += n;
+    return at;
+  };
+  int64_t sym0 = 0, full0 = 0;  // tiles of the largest shape
+  const int64_t t0 = ar_dev::muon_tile(0);
+  for (MuonMat &m : p->mats) {
+    const int64_t size = static_cast<int64_t>(m.rows) * m.cols, x = static_cast<int64_t>(m.mp) * m.np;
+    const int64_t sq = static_cast<int64_t>(m.mp) * m.mp * (pair_ab ? 2 : 1);
+    for (int i = 0; i < 2; ++i) m.x[i] = take(2 * x);
+    m.a = take(sq);
+    m.b = take(sq);
+    // parts: of 4096 elements, larger where a matrix would have more than 1024
+    m.chunk = static_cast<int32_t>(up(std::max<int64_t>(4096, (size + 1023) / 1024), 1024));
+    m.parts = static_cast<int32_t>((size + m.chunk - 1) / m.chunk);
+    m.part0 = static_cast<int32_t>(part0);
+    part0 += m.parts;
+    const int64_t r = up(m.mp, t0) / t0, c = up(m.np, t0) / t0;
+    sym0 += r * (r + 1) / 2;
+    full0 += r * c;
+  }
+  p->shape_sym = sym0 >= 256 ? 0 : 1;
+  p->shape_full = full0 >= 256 ? 0 : 1;
+  const int32_t nm = static_cast<int32_t>(p->mats.size());
+  for (int32_t i = 0; i < nm; ++i)
+    for (int32_t k = 0; k < p->mats[i].parts; ++k) p->tiles.push_back({i, k, 0});
+  p->nparts = static_cast<int32_t>(p->tiles.size());
+  for (int32_t i = 0; i < nm; ++i)
+    for (int32_t r = 0; r < p->mats[i].mp / 64; ++r)
+      for (int32_t c = 0; c < p->mats[i].np / 64; ++c) p->tiles.push_back({i, r, c});
+  p->nblocks = static_cast<int32_t>(p->tiles.size()) - p->nparts;
+  // product tiles: the matrices of the longest contraction first, so that
+  // what is left at a launch's end is short
+  std::vector<int32_t> order(nm);
+  for (int32_t i = 0; i < nm; ++i) order[i] = i;
+  auto longest = [&](auto key) {
+    std::stable_sort(order.begin(), order.end(), [&](int32_t a, int32_t b) { return key(p->mats[a]) > key(p->mats[b]); });
+  };
+  constexpr int32_t kBand = 8;  // row tiles that are swept together
+  longest([](const MuonMat &m) { return m.np; });
+  int64_t bt = ar_dev::muon_tile(p->shape_sym);
+  for (int32_t i : order) {
+    const int32_t r = static_cast<int32_t>(up(p->mats[i].mp, bt) / bt);
+    for (int32_t m0 = 0; m0 < r; m0 += kBand)
+      for (int32_t n = m0; n < r; ++n)
+        for (int32_t m = m0; m < std::min(r, m0 + kBand); ++m)
+          if (n >= m) p->tiles.push_back({i, m, n});
+  }
+  p->nsym = static_cast<int32_t>(p->tiles.size()) - p->nparts - p->nblocks;
+  longest([](const MuonMat &m) { return m.mp; });
+  bt = ar_dev::muon_tile(p->shape_full);
+  for (int32_t i : order) {
+    const int32_t r = static_cast<int32_t>(up(p->mats[i].mp, bt) / bt), c = static_cast<int32_t>(up(p->mats[i].np, bt) / bt);
+    for (int32_t m0 = 0; m0 < r; m0 += kBand)
+      for (int32_t n = 0; n < c; ++n)
+        for (int32_t m = m0; m < std::min(r, m0 + kBand); ++m) p->tiles.push_back({i, m, n});
+  }
+  p->nfull = static_cast<int32_t>(p->tiles.size()) - p->nparts - p->nblocks - p->nsym;
+  p->mats_bytes = p->mats.size() * sizeof(MuonMat);
+  p->tiles_bytes = p->tiles.size() * sizeof(MuonTile);
+  p->partial_bytes = static_cast<size_t>(up(part0 * 8, 256));
+  p->ws_bytes = static_cast<size_t>(ws) * 2;
+}
+
+void default_scales(ar_muon_plan *p) {
+  for (MuonMat &m : p->mats)
+    m.scale = static_cast<float>(std::sqrt(std::max(1.0, static_cast<double>(m.rows) / m.cols)));
+}
+
+ar_status_t prepare(ar_muon_plan *p) {
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return hip_fail(e, "hipGetDevice");
+  if (p->device >= 0) {
+    if (dev != p->device) return fail(AR_ERR_INVALID_ARG, "Muon plan was prepared on another device");
+    return AR_OK;
+  }
+  if (!p->mats.empty()) {
+    e = ar_host::device_table(&p->d_mats, p->mats.data(), p->mats_bytes);
+    if (e == hipSuccess) e = ar_host::device_table(&p->d_tiles, p->tiles.data(), p->tiles_bytes);
+    if (e == hipSuccess) e = ar_host::device_table(&p->d_work, nullptr, p->partial_bytes + p->ws_bytes);
+    if (e != hipSuccess) {
+      p->release();
+      return e == hipErrorOutOfMemory ? fail(AR_ERR_OOM, "Muon workspace allocation") : hip_fail(e, "Muon tables");
+    }
+  }
+  p->device = dev;
+  return AR_OK;
+}
+
+struct MuonCall {
+  const void *g;
+  const float *mom;
+  float *mom_out;
+  const void *w;
+  void *w_out;
+  const ar_muon_params_t *params;  // NULL: orthogonalisation only
+};
+
+ar_status_t run(ar_muon_plan *p, const MuonCall &c, void *stream) {
+  const int64_t gb = p->arena * (p->g_bf16 ? 2 : 4), wb = p->arena * (p->w_bf16 ? 2 : 4), mb = p->arena * 4;
+  struct Arena {
+    const void *p;
+    int64_t bytes;
+    uintptr_t elem;
+    const char *name;
+    bool out;
+  };
+  const Arena all[5] = {{c.g, gb, p->g_bf16 ? 2u : 4u, "grads", false},
+                        {c.w_out, wb, p->w_bf16 ? 2u : 4u, c.params ? "weights_out" : "out", true},
+                        {c.mom, mb, 4, "momentum", false},
+                        {c.mom_out, mb, 4, "momentum_out", true},
+                        {c.w, wb, p->w_bf16 ? 2u : 4u, "weights", false}};
+  const int n = c.params ? 5 : 2;
+  if (p->arena > 0)
+    for (int i = 0; i < n; ++i) {
+      if (!all[i].p) return fail(AR_ERR_INVALID_ARG, std::string(all[i].name) + " is NULL");
+      if (!on(all[i].p, all[i].elem))
+        return fail(AR_ERR_INVALID_ARG, std::string(all[i].name) + " is not aligned to its elements");
+      for (int j = 0; j < i; ++j) {
+        if ((!all[i].out && !all[j].out) || !overlap(all[i].p, all[i].bytes, all[j].p, all[j].bytes)) continue;
+        // an output may be its own input: weights_out and weights (1, 4),
+        // momentum_out and momentum (3, 2), out and grads of one type (1, 0)
+        const bool own = (i == 4 && j == 1) || (i == 3 && j == 2) || (!c.params && p->g_bf16 == p->w_bf16);
+        if (!own || all[i].p != all[j].p)
+          return fail(AR_ERR_INVALID_ARG, std::string(all[i].name) + " and " + all[j].name + " overlap");
+      }
+    }
+  ar_dev::MuonArgs a{};
+  if (c.params) {
+    const ar_muon_params_t &q = *c.params;
+    const float f[4] = {static_cast<float>(q.momentum), static_cast<float>(q.grad_scale),
+                        static_cast<float>(1.0 - q.lr * q.weight_decay), static_cast<float>(q.lr)};
+    for (float v : f)
+      if (!std::isfinite(v)) return fail(AR_ERR_INVALID_ARG, "a Muon parameter is not a finite fp32 number");
+    a.step = true;
+    a.nesterov = q.nesterov != 0;
+    a.mu = f[0];
+    a.gscale = f[1];
+    a.keep = f[2];
+    a.lr = f[3];
+  }
+  ar_status_t st = prepare(p);
+  if (st != AR_OK || p->mats.empty()) return st;
+  const MuonTile *t = static_cast<const MuonTile *>(p->d_tiles);
+  a.mats = static_cast<const MuonMat *>(p->d_mats);
+  a.parts = t;
+  a.blocks = a.parts + p->nparts;
+  a.sym = a.blocks + p->nblocks;
+  a.full = a.sym + p->nsym;
+  a.nparts = p->nparts;
+  a.nblocks = p->nblocks;
+  a.nsym = p->nsym;
+  a.nfull = p->nfull;
+  a.shape_sym = p->shape_sym;
+  a.shape_full = p->shape_full;
+  a.partials = static_cast<double *>(p->d_work);
+  a.ws = reinterpret_cast<uint16_t *>(static_cast<char *>(p->d_work) + p->partial_bytes);
+  a.g = c.g;
+  a.mom = c.mom;
+  a.mom_out = c.mom_out;
+  a.w = c.w;
+  a.w_out = c.w_out;
+  a.g_bf16 = p->g_bf16;
+  a.w_bf16 = p->w_bf16;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  hipEvent_t mark = nullptr;
+  st = p->marks.of(s, &mark);
+  if (st != AR_OK) return st;
+  hipError_t e = ar_dev::muon_begin(a, p->ex0, p->steps[0].pair_x, s);
+  for (const MuonStep &k : p->steps) {
+    if (e == hipSuccess) e = ar_dev::muon_gram(a, k, s);
+    if (e == hipSuccess) e = ar_dev::muon_poly(a, k, s);
+    if (k.last) ar_dev::t_launch_events = ar_dev::LaunchEvents{nullptr, mark};
+    if (e == hipSuccess) e = ar_dev::muon_apply(a, k, s);
+  }
+  ar_dev::t_launch_events = ar_dev::LaunchEvents{};
+  return e == hipSuccess ? AR_OK : hip_fail(e, "kernel launch");
+}
+
+}  // namespace
+
+extern "C" {
+
+ar_experts_t *ar_experts_create(int nexperts, size_t in_features, size_t out_features, ar_dtype_t dtype,
+                                ar_dtype_t grad_dtype, const size_t *weight_offsets) {
+  ar_experts *ex = nullptr;
+  const ar_status_t st = guarded([&]() -> ar_status_t {
+    const int32_t d = raw_enum(dtype), g = raw_enum(grad_dtype);
+    if (nexperts < 1 || nexperts > 65536) return fail(AR_ERR_INVALID_ARG, "nexperts must be from 1 to 65536");
+    if (in_features < 1 || out_features < 1 || in_features > kMaxFeatures || out_features > kMaxFeatures)
+      return fail(AR_ERR_INVALID_ARG, "features must be from 1 to 2^22");
+    if (!float_type(d) || !float_type(g))
+      return fail(AR_ERR_INVALID_ARG, "expert products take AR_FLOAT32 or AR_BFLOAT16");
+    if (d == AR_FLOAT32 && g != AR_FLOAT32)
+      return fail(AR_ERR_UNSUPPORTED, "AR_FLOAT32 expert products give AR_FLOAT32 weight gradients");
+    ex = new ar_experts;
+    ex->nexperts = nexperts;
+    ex->in = static_cast<int64_t>(in_features);
+    ex->out = static_cast<int64_t>(out_features);
+    ex->bf16 = d == AR_BFLOAT16;
+    ex->grad_bf16 = g == AR_BFLOAT16;
+    const int64_t size = ex->in * ex->out;
+    for (int e = 0; e < nexperts; ++e) {
+      if (weight_offsets && weight_offsets[e] > static_cast<size_t>(INT64_MAX / 16))
+        return fail(AR_ERR_INVALID_ARG, "weight offset of expert " + std::to_string(e) + " is too large");
+      const int64_t at = weight_offsets ? static_cast<int64_t>(weight_offsets[e]) : e * size;
+      ex->offsets.push_back(at);
+      ex->arena = std::max(ex->arena, at + size);
+      ex->offsets_by_8 = ex->offsets_by_8 && at % 8 == 0;
+    }
+    std::vector<int64_t> sorted = ex->offsets;
+    std::sort(sorted.begin(), sorted.end());
+    for (int e = 1; e < nexperts; ++e)
+      if (sorted[e] - sorted[e - 1] < size) return fail(AR_ERR_INVALID_ARG, "the experts' matrices overlap");
+    return AR_OK;
+  });
+  if (st != AR_OK) {
+    delete ex;
+    return nullptr;
+  }
+  return ex;
+}
+
+ar_status_t ar_experts_prepare(ar_experts_t *ex) {
+  if (!ex) return fail(AR_ERR_INVALID_ARG, "expert plan is NULL");
+  return prepare(ex);
+}
+
+ar_experts_stats_t ar_experts_stats(const ar_experts_t *ex) {
+  ar_experts_stats_t s{};
+  if (!ex) {
+    fail(AR_ERR_INVALID_ARG, "expert plan is NULL");
+    return s;
+  }
+  s.nexperts = ex->nexperts;
+  s.device = ex->device;
+  s.in_features = static_cast<uint64_t>(ex->in);
+  s.out_features = static_cast<uint64_t>(ex->out);
+  s.elem_bytes = ex->bf16 ? 2 : 4;
+  s.grad_bytes = ex->grad_bf16 ? 2 : 4;
+  s.arena_count = static_cast<uint64_t>(ex->arena);
+  return s;
+}
+
+ar_status_t ar_experts_forward(ar_experts_t *ex, const void *x, size_t x_stride, const void *weights, void *y,
+                               size_t y_stride, const int32_t *ends, size_t ntokens, void *stream) {
+  if (!ex) return fail(AR_ERR_INVALID_ARG, "expert plan is NULL");
+  return guarded([&] {
+    return run(ex, kForward, {x, x_stride, ex->in, "x"}, {y, y_stride, ex->out, "y"}, weights, true, false, ends,
+               ntokens, stream);
+  });
+}
+
+ar_status_t ar_experts_input_grad(ar_experts_t *ex, const void *dy, size_t dy_stride, const void *weights, void *dx,
+                                  size_t dx_stride, const int32_t *ends, size_t ntokens, void *stream) {
+  if (!ex) return fail(AR_ERR_INVALID_ARG, "expert plan is NULL");
+  return guarded([&] {
+    return run(ex, kInputGrad, {dy, dy_stride, ex->out, "dy"}, {dx, dx_stride, ex->in, "dx"}, weights, true, false,
+               ends, ntokens, stream);
+  });
+}
+
+ar_status_t ar_experts_weight_grad(ar_experts_t *ex, const void *x, size_t x_stride, const void *dy, size_t dy_stride,
+                                   void *grads, int accumulate, const int32_t *ends, size_t ntokens, void *stream) {
+  if (!ex) return fail(AR_ERR_INVALID_ARG, "expert plan is NULL");
+  return guarded([&] {
+    return run(ex, kWeightGrad, {x, x_stride, ex->in, "x"}, {dy, dy_stride, ex->out, "dy"}, grads, false,
+               accumulate != 0, ends, ntokens, stream);
+  });
+}
+
+void ar_experts_destroy(ar_experts_t *ex) {
+  if (!ex) return;
+  ex->release();
+  delete ex;
+}
+
+ar_muon_plan_t *ar_muon_plan_create(int nmatrices, const size_t *rows, const size_t *cols, const size_t *offsets,
+                                    ar_dtype_t grad_dtype, ar_dtype_t weight_dtype) {
+  ar_muon_plan *p = nullptr;
+  const ar_status_t st = guarded([&]() -> ar_status_t {
+    const int32_t g = raw_enum(grad_dtype), w = raw_enum(weight_dtype);
+    if (nmatrices < 0 || nmatrices > 65536) return fail(AR_ERR_INVALID_ARG, "nmatrices must be from 0 to 65536");
+    if (nmatrices > 0 && (!rows || !cols)) return fail(AR_ERR_INVALID_ARG, "rows or cols is NULL");
+    if (!float_type(g) || !float_type(w))
+      return fail(AR_ERR_INVALID_ARG, "Muon plans take AR_FLOAT32 or AR_BFLOAT16");
+    p = new ar_muon_plan;
+    p->nmatrices = nmatrices;
+    p->g_bf16 = g == AR_BFLOAT16;
+    p->w_bf16 = w == AR_BFLOAT16;
+    int64_t next = 0;
+    double work = 0;
+    std::vector<std::pair<int64_t, int64_t>> ranges;
+    for (int i = 0; i < nmatrices; ++i) {
+      const std::string name = "matrix " + std::to_string(i);
+      if (rows[i] > 1u << 20 || cols[i] > 1u << 20) return fail(AR_ERR_INVALID_ARG, name + " has a side over 2^20");
+      if (offsets && offsets[i] > static_cast<size_t>(INT64_MAX / 16))
+        return fail(AR_ERR_INVALID_ARG, name + ": offset too large");
+      const int64_t at = offsets ? static_cast<int64_t>(offsets[i]) : next;
+      const int64_t size = static_cast<int64_t>(rows[i]) * static_cast<int64_t>(cols[i]);
+      next = at + size;
+      if (size == 0) continue;
+      MuonMat m{};
+      m.at = at;
+      m.rows = static_cast<int32_t>(rows[i]);
+      m.cols = static_cast<int32_t>(cols[i]);
+      m.tall = m.rows > m.cols;
+      m.m = std::min(m.rows, m.cols);
+      m.n = std::max(m.rows, m.cols);
+      m.mp = static_cast<int32_t>(up(m.m, ar_dev::kMuonPad));
+      m.np = static_cast<int32_t>(up(m.n, ar_dev::kMuonPad));
+      work += static_cast<double>(m.mp) * (4.0 * m.np + 4.0 * m.mp);
+      p->mats.push_back(m);
+      p->index.push_back(i);
+      ranges.push_back({at, next});
+      p->arena = std::max(p->arena, next);
+    }
+    // tiles are counted in int32 and the workspace in bytes
+    if (work > 2e11) return fail(AR_ERR_INVALID_ARG, "the matrices are too large for one plan");
+    std::sort(ranges.begin(), ranges.end());
+    for (size_t i = 1; i < ranges.size(); ++i)
+      if (ranges[i].first < ranges[i - 1].second) return fail(AR_ERR_INVALID_ARG, "matrices overlap");
+    default_scales(p);
+    (void)make_steps(kNsSteps, nullptr, !p->w_bf16, p->steps, p->ex0);
+    lay_out(p);
+    return AR_OK;
+  });
+  if (st != AR_OK) {
+    delete p;
+    return nullptr;
+  }
+  return p;
+}
+
+ar_status_t ar_muon_plan_set_iterations(ar_muon_plan_t *p, int n, const double *abc) {
+  if (!p) return fail(AR_ERR_INVALID_ARG, "Muon plan is NULL");
+  return guarded([&]() -> ar_status_t {
+    if (n < 1 || n > 32) return fail(AR_ERR_INVALID_ARG, "iterations must be from 1 to 32");
+    std::vector<MuonStep> steps;
+    int32_t ex0 = 0;
+    if (!make_steps(n, abc, !p->w_bf16, steps, ex0))
+      return fail(AR_ERR_INVALID_ARG, "the coefficients let singular values or a factor grow beyond bounds");
+    p->marks.wait();
+    p->steps = std::move(steps);
+    p->ex0 = ex0;
+    return AR_OK;
+  });
+}
+
+ar_status_t ar_muon_plan_set_scales(ar_muon_plan_t *p, const double *scales) {
+  if (!p) return fail(AR_ERR_INVALID_ARG, "Muon plan is NULL");
+  if (scales)
+    for (int i = 0; i < p->nmatrices; ++i)
+      if (!std::isfinite(static_cast<float>(scales[i])))
+        return fail(AR_ERR_INVALID_ARG, "scale of matrix " + std::to_string(i) + " is not a finite fp32 number");
+  p->release();
+  if (!scales) default_scales(p);
+  else
+    for (size_t i = 0; i < p->mats.size(); ++i) p->mats[i].scale = static_cast<float>(scales[p->index[i]]);
+  return AR_OK;
+}
+
+ar_status_t ar_muon_plan_prepare(ar_muon_plan_t *p) {
+  if (!p) return fail(AR_ERR_INVALID_ARG, "Muon plan is NULL");
+  return prepare(p);
+}
+
+ar_muon_stats_t ar_muon_plan_stats(const ar_muon_plan_t *p) {
+  ar_muon_stats_t s{};
+  if (!p) {
+    fail(AR_ERR_INVALID_ARG, "Muon plan is NULL");
+    return s;
+  }
+  s.nmatrices = p->nmatrices;
+  s.device = p->device;
+  s.iterations = static_cast<int32_t>(p->steps.size());
+  s.launches = p->mats.empty() ? 0 : 2 + 3 * s.iterations;
+  s.grad_bytes = p->g_bf16 ? 2 : 4;
+  s.weight_bytes = p->w_bf16 ? 2 : 4;
+  s.arena_count = static_cast<uint64_t>(p->arena);
+  s.workspace_bytes = p->mats.empty() ? 0 : p->mats_bytes + p->tiles_bytes + p->partial_bytes + p->ws_bytes;
+  return s;
+}
+
+ar_status_t ar_orthogonalize(ar_muon_plan_t *p, const void *grads, void *out, void *stream) {
+  if (!p) return fail(AR_ERR_INVALID_ARG, "Muon plan is NULL");
+  return guarded([&] { return run(p, MuonCall{grads, nullptr, nullptr, nullptr, out, nullptr}, stream); });
+}
+
+ar_status_t ar_muon_step(ar_muon_plan_t *p, const void *grads, float *momentum, void *weights, float *momentum_out,
+                         void *weights_out, const ar_muon_params_t *params, void *stream) {
+  if (!p) return fail(AR_ERR_INVALID_ARG, "Muon plan is NULL");
+  if (!params) return fail(AR_ERR_INVALID_ARG, "params is NULL");
+  return guarded([&] {
+    return run(p, MuonCall{grads, momentum, momentum_out ? momentum_out : momentum, weights,
+                           weights_out ? weights_out : weights, params}, stream);
+  });
+}
+
+void ar_muon_plan_destroy(ar_muon_plan_t *p) {
+  if (!p) return;
+  p->release();
+  delete p;
+}
+
+}  // extern "C"

@@ -1,0 +1,94 @@
+// operators.hpp -- interface between the C ABI and the kernels of the expert
+// products and of the Muon update.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+namespace ar_dev {
+
+// ---- Products grouped by expert (experts.hip)
+
+// Rows of expert e: [end of e - 1, end of e), where the ends are the running
+// maximum of ends[0 .. e], clamped to [0, tokens].
+struct ExpertArgs {
+  const void *x, *w, *dy;  // which are set depends on the product
+  void *out;
+  const int64_t *offsets;  // [experts] first element of expert e's matrix
+  const int32_t *ends;     // [experts]
+  int64_t tokens, in, outf;
+  int64_t xs, dys, outs;   // elements between rows of x, dy (y for the forward product's out) and out
+  int32_t experts;
+  bool bf16;               // element type of x, w, dy, y and dx
+  bool grad_bf16;          // element type of the weight gradients
+  bool accumulate;
+  bool aligned;            // every row and matrix starts on 16 bytes
+  bool vec_out;            // four consecutive outputs can be stored as one
+};
+
+hipError_t experts_forward(const ExpertArgs &a, hipStream_t s);
+hipError_t experts_input_grad(const ExpertArgs &a, hipStream_t s);
+hipError_t experts_weight_grad(const ExpertArgs &a, hipStream_t s);
+
+// ---- Newton-Schulz and Muon (muon.hip)
+
+// One matrix.  m <= n: its smaller and larger side; tall: rows > cols, worked
+// on transposed.  mp, np: m and n rounded up to kMuonPad.  x, a, b: first
+// element (16-bit) of its buffers in the workspace: two X buffers of two
+// planes (hi, lo) of mp x np, A and B of two planes of mp x mp.
+struct MuonMat {
+  int64_t at;  // first element in the arenas
+  int64_t x[2], a, b;
+  int32_t rows, cols, m, n, mp, np;
+  int32_t tall;
+  int32_t part0, parts;  // its partial sums of squares
+  int32_t chunk;         // elements of a part
+  float scale;
+  int32_t pad;
+};
+constexpr int kMuonPad = 64;
+
+struct MuonTile {
+  int32_t mat, m, n;  // tile row and column; a part's number in m
+};
+
+struct MuonArgs {
+  const MuonMat *mats;
+  const MuonTile *parts, *blocks, *sym, *full;  // work lists
+  int32_t nparts, nblocks, nsym, nfull;
+  int32_t shape_sym, shape_full;  // tile shapes (muon_tile)
+  double *partials;
+  uint16_t *ws;
+  const void *g;
+  const float *mom;
+  float *mom_out;
+  const void *w;
+  void *w_out;
+  bool g_bf16, w_bf16;
+  bool step, nesterov;
+  float mu, gscale, keep, lr;  // keep: 1 - lr * weight decay
+};
+
+// One step's factors: powers of two that the stored X, A and B and the next
+// X carry, and the polynomial.
+struct MuonStep {
+  float coef_a, coef_b, coef_c;
+  int32_t ex, ea, eb, ex_next;
+  bool pair_x;       // X is held as hi + lo
+  bool pair_next;    // so is the next X
+  bool pair_ab;      // so are A and B
+  bool last;
+  int32_t from;      // X buffer read
+};
+
+// Rows and columns of tile shape i (0: the largest).
+int muon_tile(int shape);
+constexpr int kMuonShapes = 2;
+
+hipError_t muon_begin(const MuonArgs &a, int32_t ex0, bool pair, hipStream_t s);
+hipError_t muon_gram(const MuonArgs &a, const MuonStep &k, hipStream_t s);
+hipError_t muon_poly(const MuonArgs &a, const MuonStep &k, hipStream_t s);
+hipError_t muon_apply(const MuonArgs &a, const MuonStep &k, hipStream_t s);
+
+}  // namespace ar_dev

@@ -642,6 +642,177 @@ double ar_overlap_step_time(int nchunks, const double *ready_s, const double *co
 ar_stats_t ar_bucket_stats(const ar_bucket_plan_t *bp);
 void ar_bucket_plan_destroy(ar_bucket_plan_t *bp);
 
+/* ---- Products grouped by expert ----
+ *
+ * The linear layers of a mixture of experts, whose weight gradients are what
+ * a rank's gradient arena collects before it is all-reduced.  Expert e's
+ * weight W_e is a row-major [out_features, in_features] matrix that starts at
+ * element weight_offsets[e] of an arena (the tensor offsets of
+ * ar_bucket_layout fit; NULL: the matrices lie back to back), so the weight
+ * gradients land where ar_bucket_allreduce reads them, and the event that
+ * marks the bucket ready can be recorded behind the call.
+ *
+ * The rows of x, y, dx and dy are sorted by expert: `ends` is a device array
+ * of nexperts int32, and expert e's rows are [end(e-1), end(e)) with
+ * end(e) = the largest of ends[0 .. e], clamped to [0, ntokens].  The counts
+ * stay on the device; no call waits for the host.
+ *
+ *   forward      y[t, o]    = sum_i x[t, i] W_e[o, i]
+ *   input_grad   dx[t, i]   = sum_o dy[t, o] W_e[o, i]
+ *   weight_grad  dW_e[o, i] = sum over the rows t of e of dy[t, o] x[t, i]
+ *                             (+ the old dW_e with accumulate != 0)
+ *
+ * Sums are fp32 and each result is rounded once to its type (nearest, ties
+ * to even).  Rows from end(nexperts-1) on are neither read nor written; an
+ * expert without rows gets a zero weight gradient (accumulate: is left as it
+ * was); elements of the arena outside the matrices are never touched.
+ * Infinities and NaN spread as in the formulas: a row's only into the row's
+ * own results (or, in weight_grad, into its expert's).  Results depend on the
+ * inputs alone (no atomics).
+ */
+typedef struct ar_experts ar_experts_t;
+
+typedef struct {
+  int32_t nexperts;
+  int32_t device;         /* device of the plan's table; -1 before it is prepared */
+  uint64_t in_features, out_features;
+  uint64_t elem_bytes;    /* of x, y, dx, dy and the weights */
+  uint64_t grad_bytes;    /* of the weight gradients         */
+  uint64_t arena_count;   /* elements an arena holds at least */
+} ar_experts_stats_t;
+
+/*
+ * dtype (of x, y, dx, dy and the weights) and grad_dtype (of the weight
+ * gradients): AR_FLOAT32 or AR_BFLOAT16; AR_FLOAT32 experts have AR_FLOAT32
+ * gradients (AR_ERR_UNSUPPORTED otherwise).  Features from 1 to 2^22, experts
+ * from 1 to 65536.  Returns NULL on error (AR_ERR_INVALID_ARG, also where the
+ * matrices overlap).  Host only.
+ */
+ar_experts_t *ar_experts_create(int nexperts, size_t in_features, size_t out_features, ar_dtype_t dtype,
+                                ar_dtype_t grad_dtype, const size_t *weight_offsets);
+/* Uploads the offset table to the current device (the first product does it
+ * otherwise; call it before capturing one into a HIP graph).  The plan is
+ * bound to that device. */
+ar_status_t ar_experts_prepare(ar_experts_t *plan);
+ar_experts_stats_t ar_experts_stats(const ar_experts_t *plan);
+/*
+ * The products.  Row strides are in elements (at least the features, at most
+ * 2^22); pointers are aligned to their elements (the fast path needs rows
+ * and matrices that start on 16 bytes, and feature counts that are multiples
+ * of 8).  The output overlaps no input.  Calls of one plan have no workspace:
+ * they may be in flight together on several streams, captured or not.
+ * ntokens = 0: forward and input_grad do nothing.  AR_ERR_INVALID_ARG for bad
+ * arguments or another device than the plan's; AR_ERR_UNSUPPORTED for a
+ * product beyond one launch grid; AR_ERR_HIP if the launch fails.
+ */
+ar_status_t ar_experts_forward(ar_experts_t *plan, const void *x, size_t x_stride, const void *weights, void *y,
+                               size_t y_stride, const int32_t *ends, size_t ntokens, void *stream);
+ar_status_t ar_experts_input_grad(ar_experts_t *plan, const void *dy, size_t dy_stride, const void *weights, void *dx,
+                                  size_t dx_stride, const int32_t *ends, size_t ntokens, void *stream);
+ar_status_t ar_experts_weight_grad(ar_experts_t *plan, const void *x, size_t x_stride, const void *dy,
+                                   size_t dy_stride, void *grads, int accumulate, const int32_t *ends, size_t ntokens,
+                                   void *stream);
+/* Waits for the plan's calls in flight (captured ones are the caller's to
+ * finish) and releases it. */
+void ar_experts_destroy(ar_experts_t *plan);
+
+/* ---- The update of weight matrices: Newton-Schulz and Muon ----
+ *
+ * What a training step does with a reduced gradient arena: each weight matrix
+ * U of the arena is replaced by a matrix with (nearly) the same singular
+ * vectors and singular values near 1,
+ *
+ *   X_0 = U / (||U||_F + 1e-7)
+ *   X_k+1 = a_k X_k + (b_k A + c_k A A) X_k,   A = X_k X_k^T
+ *
+ * (for a matrix of more rows than columns the same on its transpose), five
+ * steps with (a, b, c) = (3.4445, -4.7750, 2.0315) unless set otherwise; and
+ * the Muon step is
+ *
+ *   M' = mu M + s G           s = grad_scale, e.g. 1 / ranks after a sum
+ *   U  = s G + mu M'          (nesterov), or M'
+ *   W' = (1 - lr decay) W - lr scale O,   O = Newton-Schulz of U
+ *
+ * with scale = sqrt(max(1, rows / cols)) unless set otherwise.
+ *
+ * Matrix i is row-major [rows[i], cols[i]] and starts at element offsets[i]
+ * (NULL: back to back) of every arena: gradients, momentum, weights and
+ * orthogonalised output are laid out alike, as ar_bucket_layout lays out the
+ * gradients.  Elements outside the matrices are never touched.
+ *
+ * Precision.  The momentum is fp32 and its update and the norm are computed
+ * in fp32 and fp64.  The products run on fp16 matrix instructions with fp32
+ * sums; X, A and b A + c A A + a I are scaled by powers of two that keep them
+ * inside fp16's range whatever the input's size.  weight_dtype AR_FLOAT32:
+ * every factor is held as a sum of two fp16 (22 bits), three products each;
+ * the relative error is near that of fp32 arithmetic.  AR_BFLOAT16: X is held
+ * so up to the last step (a rounding of X is amplified by up to a per step,
+ * so a single fp16 costs 1e-2 and more on a matrix of few large singular
+ * values), the other factors as one fp16: the error stays below the bf16
+ * rounding of the result.
+ * A matrix that holds an infinity or NaN gives NaN in all its results (its
+ * momentum as the formula says) and changes no other matrix.
+ */
+typedef struct ar_muon_plan ar_muon_plan_t;
+
+typedef struct {
+  int32_t nmatrices;
+  int32_t device;            /* device of the plan's workspace; -1 before it is prepared */
+  int32_t iterations;
+  int32_t launches;          /* kernel launches of ar_orthogonalize */
+  uint64_t grad_bytes, weight_bytes; /* bytes of an element */
+  uint64_t arena_count;      /* elements an arena holds at least */
+  uint64_t workspace_bytes;  /* device memory the plan owns once prepared */
+} ar_muon_stats_t;
+
+typedef struct {
+  double lr, momentum, weight_decay;
+  double grad_scale;
+  int32_t nesterov; /* 0: U = M' */
+} ar_muon_params_t;
+
+/*
+ * grad_dtype (of the gradients) and weight_dtype (of the weights and of
+ * ar_orthogonalize's output): AR_FLOAT32 or AR_BFLOAT16.  rows and cols up to
+ * 2^20; a matrix with none of either is skipped.  Returns NULL on error
+ * (AR_ERR_INVALID_ARG, also where matrices overlap).  Host only.
+ */
+ar_muon_plan_t *ar_muon_plan_create(int nmatrices, const size_t *rows, const size_t *cols, const size_t *offsets,
+                                    ar_dtype_t grad_dtype, ar_dtype_t weight_dtype);
+/* n (1 to 32) steps with coefficients abc[3 k .. 3 k + 2]; abc = NULL: the
+ * default ones in every step.  AR_ERR_INVALID_ARG where singular values in
+ * [0, 1] could grow past 2^10 or a factor past 2^14 on the way.  Waits for
+ * the plan's calls in flight.  Host only. */
+ar_status_t ar_muon_plan_set_iterations(ar_muon_plan_t *plan, int n, const double *abc);
+/* scale[i] of matrix i (NULL: the default ones).  Finite.  Drops the plan's
+ * device tables after waiting for its calls in flight; the next call (or
+ * prepare) uploads new ones. */
+ar_status_t ar_muon_plan_set_scales(ar_muon_plan_t *plan, const double *scales);
+/* Allocates the plan's workspace and tables on the current device (the first
+ * call does it otherwise; call it before capturing one into a HIP graph). */
+ar_status_t ar_muon_plan_prepare(ar_muon_plan_t *plan);
+ar_muon_stats_t ar_muon_plan_stats(const ar_muon_plan_t *plan);
+/*
+ * out = Newton-Schulz of every matrix of grads.  out overlaps grads only if
+ * both are the same pointer and of one type (in place).  Calls of one plan
+ * share its workspace: they must not overlap in time, nor with replays of
+ * graphs that captured them.  Pointers are aligned to their elements.
+ * AR_ERR_INVALID_ARG, AR_ERR_OOM and AR_ERR_HIP as for ar_allreduce.
+ */
+ar_status_t ar_orthogonalize(ar_muon_plan_t *plan, const void *grads, void *out, void *stream);
+/*
+ * The Muon step.  momentum (fp32) and weights (weight_dtype) are read and
+ * written; with momentum_out or weights_out not NULL the new values go there
+ * instead and the old ones stay.  No two of the arenas overlap, except that
+ * an output may be its own input.  params is read during the call (a captured
+ * graph keeps its values).  Finite parameters; AR_ERR_INVALID_ARG otherwise.
+ */
+ar_status_t ar_muon_step(ar_muon_plan_t *plan, const void *grads, float *momentum, void *weights, float *momentum_out,
+                         void *weights_out, const ar_muon_params_t *params, void *stream);
+/* Waits for the plan's calls in flight (captured ones are the caller's to
+ * finish) and releases it. */
+void ar_muon_plan_destroy(ar_muon_plan_t *plan);
+
 #ifdef __cplusplus
 }
 #endif

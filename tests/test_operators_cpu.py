@@ -1,0 +1,209 @@
+"""Refusals, statistics and plan checks of the expert products and the Muon
+update on a host without a GPU: every bad call is turned away before any
+device work."""
+import ctypes
+
+import pytest
+import torch
+
+from gradient_all_reduce_ar_amd import _binding as B
+
+A = 1 << 20  # stands for a device address: never read, the calls fail first
+
+
+@pytest.fixture
+def experts():
+    p = B.ar_experts_create(4, 64, 32, "bf16", "fp32")
+    yield p
+    B.ar_experts_destroy(p)
+
+
+@pytest.fixture
+def muon():
+    p = B.ar_muon_plan_create([(64, 32), (16, 48)], "bf16", "fp32")
+    yield p
+    B.ar_muon_plan_destroy(p)
+
+
+def refused(status, fn, *a, **k):
+    with pytest.raises(B.ArError) as e:
+        fn(*a, **k)
+    assert e.value.status == status, str(e.value)
+    return str(e.value)
+
+
+@pytest.mark.parametrize("args,status", [
+    ((0, 64, 64, "bf16", "fp32"), B.AR_ERR_INVALID_ARG),
+    ((65537, 64, 64, "bf16", "fp32"), B.AR_ERR_INVALID_ARG),
+    ((4, 0, 64, "bf16", "fp32"), B.AR_ERR_INVALID_ARG),
+    ((4, 64, 0, "bf16", "fp32"), B.AR_ERR_INVALID_ARG),
+    ((4, (1 << 22) + 1, 64, "bf16", "fp32"), B.AR_ERR_INVALID_ARG),
+    ((4, 64, 64, "int8_ef", "fp32"), B.AR_ERR_INVALID_ARG),
+    ((4, 64, 64, "bf16", "bf16_each"), B.AR_ERR_INVALID_ARG),
+    ((4, 64, 64, 17, "fp32"), B.AR_ERR_INVALID_ARG),
+    ((4, 64, 64, "fp32", "bf16"), B.AR_ERR_UNSUPPORTED),
+    ((2, 4, 4, "bf16", "fp32", [0, 15]), B.AR_ERR_INVALID_ARG),  # overlapping matrices
+    ((2, 4, 4, "bf16", "fp32", [0, 1 << 62]), B.AR_ERR_INVALID_ARG),
+])
+def test_experts_create_refuses(args, status):
+    refused(status, B.ar_experts_create, *args)
+
+
+def test_experts_stats():
+    p = B.ar_experts_create(3, 5, 7, "bf16", "fp32", [100, 0, 35])
+    s = B.ar_experts_stats(p)
+    B.ar_experts_destroy(p)
+    assert s == {"nexperts": 3, "device": -1, "in_features": 5, "out_features": 7, "elem_bytes": 2, "grad_bytes": 4,
+                 "arena_count": 135}
+
+
+def test_experts_null_plan():
+    for fn in (B.ar_experts_forward, B.ar_experts_input_grad, B.ar_experts_weight_grad):
+        refused(B.AR_ERR_INVALID_ARG, fn, None, A, A, A, A)
+    refused(B.AR_ERR_INVALID_ARG, B.ar_experts_prepare, None)
+    B.ar_experts_destroy(None)
+
+
+def far(k):
+    """Addresses that lie far apart."""
+    return A + k * (1 << 30)
+
+
+@pytest.mark.parametrize("change,word", [
+    (dict(x=0), "x is NULL"), (dict(x=far(0) + 1), "aligned"), (dict(y=0), "y is NULL"), (dict(y=far(2) + 1), "aligned"),
+    (dict(w=0), "arena is NULL"), (dict(w=far(1) + 1), "arena is not aligned"), (dict(ends=0), "ends is NULL"),
+    (dict(ends=far(3) + 2), "ends is not aligned"), (dict(xs=63), "stride"), (dict(ys=31), "stride"),
+    (dict(xs=(1 << 22) + 1), "stride"), (dict(y=far(0) + 64), "overlaps"), (dict(y=far(1)), "overlaps"),
+    (dict(y=far(3)), "overlaps"), (dict(n=1 << 31), "tokens"),
+])
+def test_experts_forward_refuses(experts, change, word):
+    a = dict(x=far(0), w=far(1), y=far(2), ends=far(3), xs=64, ys=32, n=8) | change
+    msg = refused(B.AR_ERR_INVALID_ARG, B.ar_experts_forward, experts, a["x"], a["w"], a["y"], a["ends"],
+                  ntokens=a["n"], x_stride=a["xs"], y_stride=a["ys"])
+    assert word in msg
+
+
+@pytest.mark.parametrize("change,word", [
+    (dict(x=0), "x is NULL"), (dict(dy=0), "dy is NULL"), (dict(g=0), "arena is NULL"),
+    (dict(g=far(2) + 2), "arena is not aligned"), (dict(g=far(0)), "overlaps"), (dict(g=far(1)), "overlaps"),
+    (dict(g=far(3)), "overlaps"), (dict(ends=0), "ends is NULL"), (dict(n=0, ends=0), "ends is NULL"),
+])
+def test_experts_weight_grad_refuses(experts, change, word):
+    a = dict(x=far(0), dy=far(1), g=far(2), ends=far(3), n=8) | change
+    msg = refused(B.AR_ERR_INVALID_ARG, B.ar_experts_weight_grad, experts, a["x"], a["dy"], a["g"], a["ends"],
+                  ntokens=a["n"])
+    assert word in msg
+
+
+def test_experts_binding_checks_tensors(experts):
+    x = torch.zeros(8, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="not a device tensor"):
+        B.ar_experts_forward(experts, x, A, A, A)
+    with pytest.raises(ValueError, match="ntokens"):
+        B.ar_experts_forward(experts, A, A, A, A)
+    with pytest.raises(ValueError, match="own stride"):
+        B.ar_experts_forward(experts, x, A, A, A, x_stride=64)
+    with pytest.raises(ValueError, match="weight offsets"):
+        B.ar_experts_create(3, 4, 4, "bf16", "fp32", [0, 16])
+
+
+@pytest.mark.parametrize("args", [
+    ([(8, 8)], "int8_ef", "fp32"), ([(8, 8)], "fp32", "bf16_each"), ([(8, 8)], "fp32", 9),
+    ([((1 << 20) + 1, 1)], "fp32", "fp32"), ([(1 << 20, 1 << 20)], "fp32", "fp32"),
+    ([(4, 4), (4, 4)], "fp32", "fp32", [0, 15]), ([(4, 4)], "fp32", "fp32", [1 << 62]),
+])
+def test_muon_create_refuses(args):
+    refused(B.AR_ERR_INVALID_ARG, B.ar_muon_plan_create, *args)
+
+
+def test_muon_stats(muon):
+    s = B.ar_muon_plan_stats(muon)
+    assert (s["nmatrices"], s["device"], s["iterations"], s["arena_count"]) == (2, -1, 5, 64 * 32 + 16 * 48)
+    assert (s["grad_bytes"], s["weight_bytes"]) == (2, 4)
+    assert s["workspace_bytes"] > 0 and s["launches"] > 0
+    empty = B.ar_muon_plan_create([(0, 5), (3, 0)], "fp32", "fp32")
+    s = B.ar_muon_plan_stats(empty)
+    assert s["arena_count"] == 0 and s["workspace_bytes"] == 0 and s["launches"] == 0
+    B.ar_muon_plan_destroy(empty)
+
+
+@pytest.mark.parametrize("n,abc", [
+    (0, None), (33, None), (1, [(float("nan"), 0, 0)]), (1, [(float("inf"), 0, 0)]), (1, [(2000.0, 0, 0)]),
+    (1, [(0, 0, 1e5)]), (8, [(8.0, 0, 0)] * 8),
+])
+def test_muon_iterations_refused(muon, n, abc):
+    refused(B.AR_ERR_INVALID_ARG, B.ar_muon_plan_set_iterations, muon, n, abc)
+    assert B.ar_muon_plan_stats(muon)["iterations"] == 5
+
+
+def test_muon_iterations_set(muon):
+    B.ar_muon_plan_set_iterations(muon, 8, [(1.5, -0.5, 0.0)] * 8)
+    assert B.ar_muon_plan_stats(muon)["iterations"] == 8
+    B.ar_muon_plan_set_iterations(muon, 3)
+    assert B.ar_muon_plan_stats(muon)["iterations"] == 3
+    with pytest.raises(ValueError):
+        B.ar_muon_plan_set_iterations(muon, 2, [(1, 0, 0)])
+
+
+def test_muon_scales(muon):
+    B.ar_muon_plan_set_scales(muon, [0.5, 2.0])
+    B.ar_muon_plan_set_scales(muon)
+    refused(B.AR_ERR_INVALID_ARG, B.ar_muon_plan_set_scales, muon, [0.5, float("nan")])
+    refused(B.AR_ERR_INVALID_ARG, B.ar_muon_plan_set_scales, muon, [1e40, 1.0])
+    with pytest.raises(ValueError):
+        B.ar_muon_plan_set_scales(muon, [1.0])
+
+
+def test_muon_null_plan():
+    refused(B.AR_ERR_INVALID_ARG, B.ar_orthogonalize, None, A, A)
+    refused(B.AR_ERR_INVALID_ARG, B.ar_muon_step, None, A, A, A, lr=0.1)
+    refused(B.AR_ERR_INVALID_ARG, B.ar_muon_plan_prepare, None)
+    refused(B.AR_ERR_INVALID_ARG, B.ar_muon_plan_set_iterations, None, 5)
+    refused(B.AR_ERR_INVALID_ARG, B.ar_muon_plan_set_scales, None)
+    B.ar_muon_plan_destroy(None)
+
+
+@pytest.mark.parametrize("g,o,word", [
+    (0, far(1), "grads is NULL"), (far(0), 0, "out is NULL"), (far(0) + 1, far(1), "aligned"),
+    (far(0), far(1) + 2, "aligned"), (far(0), far(0) + 64, "overlap"), (far(0), far(0), "overlap"),  # bf16 and fp32
+])
+def test_orthogonalize_refuses(muon, g, o, word):
+    assert word in refused(B.AR_ERR_INVALID_ARG, B.ar_orthogonalize, muon, g, o)
+
+
+@pytest.mark.parametrize("change,word", [
+    (dict(g=0), "grads is NULL"), (dict(m=0), "momentum is NULL"), (dict(w=0), "NULL"),
+    (dict(m=far(1) + 2), "aligned"), (dict(m=far(0)), "overlap"), (dict(w=far(0)), "overlap"),
+    (dict(w=far(1)), "overlap"), (dict(mo=far(2)), "overlap"), (dict(wo=far(1)), "overlap"),
+    (dict(wo=far(2) + 64), "overlap"), (dict(mo=far(1) + 64), "overlap"), (dict(lr=float("nan")), "finite"),
+    (dict(mu=float("inf")), "finite"), (dict(decay=1e40, lr=1.0), "finite"), (dict(gs=1e39), "finite"),
+])
+def test_muon_step_refuses(muon, change, word):
+    a = dict(g=far(0), m=far(1), w=far(2), mo=None, wo=None, lr=0.1, mu=0.9, decay=0.0, gs=1.0) | change
+    msg = refused(B.AR_ERR_INVALID_ARG, B.ar_muon_step, muon, a["g"], a["m"], a["w"], a["lr"], mu=a["mu"],
+                  weight_decay=a["decay"], grad_scale=a["gs"], momentum_out=a["mo"], weights_out=a["wo"])
+    assert word in msg
+
+
+def test_muon_params_null(muon):
+    L = B.lib()
+    assert L.ar_muon_step(muon, far(0), far(1), far(2), None, None, None, None) == B.AR_ERR_INVALID_ARG
+    assert b"params" in L.ar_last_error()
+
+
+def test_muon_offsets_from_a_bucket_plan():
+    """The tensor offsets of a bucket layout are valid matrix and weight offsets."""
+    shapes = [(16, 32), (7, 5), (64, 64)]
+    bp = B.ar_bucket_plan_create(2, 1, [r * c for r, c in shapes], "bf16", "ring", 4096)
+    offs, arena = B.ar_bucket_layout(bp, len(shapes))
+    B.ar_bucket_plan_destroy(bp)
+    p = B.ar_muon_plan_create(shapes, "bf16", "bf16", offs)
+    assert B.ar_muon_plan_stats(p)["arena_count"] <= arena
+    B.ar_muon_plan_destroy(p)
+
+
+def test_c_struct_sizes():
+    """The ctypes mirrors have the C layout."""
+    assert ctypes.sizeof(B.ar_experts_stats_t) == 48
+    assert ctypes.sizeof(B.ar_muon_stats_t) == 48
+    assert ctypes.sizeof(B.ar_muon_params_t) == 40
