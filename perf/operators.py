@@ -9,6 +9,7 @@ orthogonalisation alone, and the whole Muon step).
 ``exact`` is the definition in fp64.
 """
 import math
+import sys
 
 import numpy as np
 import torch
@@ -177,7 +178,8 @@ class _Plan:
         self.handle, self.destroy = handle, destroy
 
     def __del__(self):
-        self.destroy(self.handle)
+        if not sys.is_finalizing():  # then the library's module is gone already
+            self.destroy(self.handle)
 
 
 def prepare(case, seed):
