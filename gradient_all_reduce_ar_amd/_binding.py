@@ -674,37 +674,62 @@ def ar_bucket_plan_destroy(bp):
 
 # ------------------------------------------- products grouped by expert
 
-def _check_device(t, device, what):
-    """A tensor's device has to be the plan's (device: -1 before it is known)."""
-    if device >= 0 and hasattr(t, "device") and t.device.index not in (None, device):
-        raise ValueError(f"{what} is on device {t.device.index}; the plan is on device {device}")
+class _ExpertsInfo:
+    """What the checks of a call need of a plan, read once; `device` is the one the plan is bound to (None
+    before its first call with tensors, which prepares it)."""
+    __slots__ = ("plan", "nexperts", "inf", "outf", "elem", "grad", "arena", "device")
+
+    def __init__(self, plan):
+        s = lib().ar_experts_stats(plan)
+        self.plan = plan
+        self.nexperts, self.inf, self.outf = s.nexperts, s.in_features, s.out_features
+        self.elem, self.grad, self.arena = s.elem_bytes, s.grad_bytes, s.arena_count
+        self.device = None
+
+    def bind(self):
+        _check(lib().ar_experts_prepare(self.plan))
+        self.device = lib().ar_experts_stats(self.plan).device
 
 
-def _rows(t, stride, rows, features, elem, device, what):
+_experts_info = {}  # by handle, until the plan is destroyed
+
+
+def _same_device(info, t, what):
+    """Every tensor of a call, and of all calls of a plan, lies on one device."""
+    if info.device is None:
+        info.bind()
+    d = t.get_device()
+    if d != info.device:
+        raise ValueError(f"{what} is on device {d}; the plan is on device {info.device}")
+
+
+def _rows(info, t, stride, rows, features, what):
     """(pointer, row stride in elements) of a [rows, features] argument: a
     device tensor whose rows are contiguous, or an address with its stride."""
     if not hasattr(t, "data_ptr"):
         return _ptr(t), features if stride is None else int(stride)
     if stride is not None:
         raise ValueError(f"{what}: a tensor brings its own stride")
-    if not getattr(t, "is_cuda", False):
+    if not t.is_cuda:
         raise ValueError(f"{what} is not a device tensor")
-    _check_device(t, device, what)
-    if t.dim() != 2 or t.element_size() != elem or tuple(t.shape) != (rows, features):
-        raise ValueError(f"{what} is {tuple(t.shape)} of {t.element_size()} bytes; wanted ({rows}, {features}) of {elem}")
-    if features > 1 and rows > 0 and t.stride(1) != 1:
+    _same_device(info, t, what)
+    shape = t.shape
+    if len(shape) != 2 or shape[0] != rows or shape[1] != features or t.element_size() != info.elem:
+        raise ValueError(f"{what} is {tuple(shape)} of {t.element_size()} bytes; wanted ({rows}, {features}) of {info.elem}")
+    st = t.stride()
+    if st[1] != 1 and features > 1 and rows > 0:
         raise ValueError(f"{what}: rows are not contiguous")
-    return t.data_ptr(), t.stride(0) if rows > 1 else features
+    return t.data_ptr(), st[0] if rows > 1 else features
 
 
-def _arena(t, count, elem, device, what):
+def _arena(info, t, count, elem, what):
     """Pointer of an arena of at least count elements: a contiguous device
     tensor, or an address."""
     if not hasattr(t, "data_ptr"):
         return _ptr(t)
-    if not getattr(t, "is_cuda", False):
+    if not t.is_cuda:
         raise ValueError(f"{what} is not a device tensor")
-    _check_device(t, device, what)
+    _same_device(info, t, what)
     if not t.is_contiguous():
         raise ValueError(f"{what} is not contiguous")
     if t.element_size() != elem or t.numel() < count:
@@ -720,14 +745,14 @@ def _tokens(rows, ntokens, what):
     return int(rows.shape[0])
 
 
-def _ends(ends, nexperts, device):
+def _ends(info, ends):
     if not hasattr(ends, "data_ptr"):
         return _ptr(ends)
-    if not getattr(ends, "is_cuda", False):
+    if not ends.is_cuda:
         raise ValueError("ends is not a device tensor")
-    _check_device(ends, device, "ends")
-    if ends.element_size() != 4 or ends.is_floating_point() or not ends.is_contiguous() or ends.numel() < nexperts:
-        raise ValueError(f"ends: wanted {nexperts} contiguous int32")
+    _same_device(info, ends, "ends")
+    if ends.element_size() != 4 or ends.is_floating_point() or ends.numel() < info.nexperts or not ends.is_contiguous():
+        raise ValueError(f"ends: wanted {info.nexperts} contiguous int32")
     return ends.data_ptr()
 
 
@@ -742,6 +767,7 @@ def ar_experts_create(nexperts, in_features, out_features, dtype, grad_dtype=Non
                                 d if grad_dtype is None else _code(DTYPES, grad_dtype), offs)
     if not p:
         _raise()
+    _experts_info[p] = _ExpertsInfo(p)
     return p
 
 
@@ -754,49 +780,52 @@ def ar_experts_stats(plan):
     return {k: getattr(s, k) for k, _ in s._fields_}
 
 
-def _experts_rows_call(fn, plan, rows, weights, out, ends, stream, ntokens, stride, out_stride, names, features):
-    s = lib().ar_experts_stats(plan)
-    n = _tokens(rows, ntokens, names[0])
-    fi, fo = (s.in_features, s.out_features) if features == "in" else (s.out_features, s.in_features)
-    p, ps = _rows(rows, stride, n, fi, s.elem_bytes, s.device, names[0])
-    o, os_ = _rows(out, out_stride, n, fo, s.elem_bytes, s.device, names[1])
-    w = _arena(weights, s.arena_count, s.elem_bytes, s.device, "weights")
-    _check(fn(plan, p, ps, w, o, os_, _ends(ends, s.nexperts, s.device), n, _stream(stream)))
+def _experts_of(plan):
+    info = _experts_info.get(plan)
+    if info is None:  # no plan, or one that this module did not make
+        if not plan:
+            _check(lib().ar_experts_prepare(None))
+        info = _experts_info[plan] = _ExpertsInfo(plan)
+    return info
 
 
 def ar_experts_forward(plan, x, weights, y, ends, stream=None, ntokens=None, x_stride=None, y_stride=None):
     """y[t] = W_e x[t] for the rows t of expert e.  x [tokens, in], y [tokens, out]: tensors with contiguous
     rows, or addresses (then ntokens, and the strides if rows are not dense); ends: int32 on the device."""
-    if not plan:
-        _check(lib().ar_experts_forward(plan, None, 0, None, None, 0, None, 0, None))
-    _experts_rows_call(lib().ar_experts_forward, plan, x, weights, y, ends, stream, ntokens, x_stride, y_stride,
-                       ("x", "y"), "in")
+    i = _experts_of(plan)
+    n = _tokens(x, ntokens, "x")
+    xp, xs = _rows(i, x, x_stride, n, i.inf, "x")
+    yp, ys = _rows(i, y, y_stride, n, i.outf, "y")
+    if _lib.ar_experts_forward(plan, xp, xs, _arena(i, weights, i.arena, i.elem, "weights"), yp, ys, _ends(i, ends), n,
+                               _stream(stream)) != AR_OK:
+        _raise()
 
 
 def ar_experts_input_grad(plan, dy, weights, dx, ends, stream=None, ntokens=None, dy_stride=None, dx_stride=None):
     """dx[t] = W_e^T dy[t] for the rows t of expert e (arguments as ar_experts_forward's)."""
-    if not plan:
-        _check(lib().ar_experts_input_grad(plan, None, 0, None, None, 0, None, 0, None))
-    _experts_rows_call(lib().ar_experts_input_grad, plan, dy, weights, dx, ends, stream, ntokens, dy_stride,
-                       dx_stride, ("dy", "dx"), "out")
+    i = _experts_of(plan)
+    n = _tokens(dy, ntokens, "dy")
+    dp, ds = _rows(i, dy, dy_stride, n, i.outf, "dy")
+    xp, xs = _rows(i, dx, dx_stride, n, i.inf, "dx")
+    if _lib.ar_experts_input_grad(plan, dp, ds, _arena(i, weights, i.arena, i.elem, "weights"), xp, xs, _ends(i, ends),
+                                  n, _stream(stream)) != AR_OK:
+        _raise()
 
 
 def ar_experts_weight_grad(plan, x, dy, grads, ends, accumulate=False, stream=None, ntokens=None, x_stride=None,
                            dy_stride=None):
     """dW_e = (old dW_e +) the sum over e's rows t of dy[t] x[t]^T, into the gradient arena."""
-    L = lib()
-    if not plan:
-        _check(L.ar_experts_weight_grad(plan, None, 0, None, 0, None, 0, None, 0, None))
-    s = L.ar_experts_stats(plan)
+    i = _experts_of(plan)
     n = _tokens(x, ntokens, "x")
-    xp, xs = _rows(x, x_stride, n, s.in_features, s.elem_bytes, s.device, "x")
-    dp, ds = _rows(dy, dy_stride, n, s.out_features, s.elem_bytes, s.device, "dy")
-    g = _arena(grads, s.arena_count, s.grad_bytes, s.device, "grads")
-    _check(L.ar_experts_weight_grad(plan, xp, xs, dp, ds, g, 1 if accumulate else 0,
-                                    _ends(ends, s.nexperts, s.device), n, _stream(stream)))
+    xp, xs = _rows(i, x, x_stride, n, i.inf, "x")
+    dp, ds = _rows(i, dy, dy_stride, n, i.outf, "dy")
+    if _lib.ar_experts_weight_grad(plan, xp, xs, dp, ds, _arena(i, grads, i.arena, i.grad, "grads"),
+                                   1 if accumulate else 0, _ends(i, ends), n, _stream(stream)) != AR_OK:
+        _raise()
 
 
 def ar_experts_destroy(plan):
+    _experts_info.pop(plan, None)
     lib().ar_experts_destroy(plan)
 
 
@@ -835,6 +864,7 @@ def ar_muon_plan_set_scales(plan, scales=None):
         if len(scales) != n:
             raise ValueError(f"{len(scales)} scales for {n} matrices")
         arr = (ctypes.c_double * max(n, 1))(*[float(v) for v in scales])
+    _muon_info.pop(plan, None)  # the plan is no longer bound to a device
     _check(lib().ar_muon_plan_set_scales(plan, arr))
 
 
@@ -847,32 +877,54 @@ def ar_muon_plan_stats(plan):
     return {k: getattr(s, k) for k, _ in s._fields_}
 
 
+class _MuonInfo:
+    __slots__ = ("plan", "arena", "grad", "weight", "device")
+
+    def __init__(self, plan):
+        s = lib().ar_muon_plan_stats(plan)
+        self.plan = plan
+        self.arena, self.grad, self.weight = s.arena_count, s.grad_bytes, s.weight_bytes
+        self.device = None
+
+    def bind(self):
+        _check(lib().ar_muon_plan_prepare(self.plan))
+        self.device = lib().ar_muon_plan_stats(self.plan).device
+
+
+_muon_info = {}
+
+
+def _muon_of(plan):
+    info = _muon_info.get(plan)
+    if info is None:  # its first call
+        if not plan:
+            _check(lib().ar_muon_plan_prepare(None))
+        info = _muon_info[plan] = _MuonInfo(plan)
+    return info
+
+
 def ar_orthogonalize(plan, grads, out, stream=None):
     """out = Newton-Schulz of every matrix of the gradient arena (out in the plan's weight type)."""
-    L = lib()
-    if not plan:
-        _check(L.ar_orthogonalize(plan, None, None, None))
-    s = L.ar_muon_plan_stats(plan)
-    g = _arena(grads, s.arena_count, s.grad_bytes, s.device, "grads")
-    o = _arena(out, s.arena_count, s.weight_bytes, s.device, "out")
-    _check(L.ar_orthogonalize(plan, g, o, _stream(stream)))
+    i = _muon_of(plan)
+    g = _arena(i, grads, i.arena, i.grad, "grads")
+    if _lib.ar_orthogonalize(plan, g, _arena(i, out, i.arena, i.weight, "out"), _stream(stream)) != AR_OK:
+        _raise()
 
 
 def ar_muon_step(plan, grads, momentum, weights, lr, mu=0.95, weight_decay=0.0, grad_scale=1.0, nesterov=True,
                  momentum_out=None, weights_out=None, stream=None):
     """One Muon step on the arenas; momentum (fp32) and weights are updated in place unless the outputs are given."""
-    L = lib()
+    i = _muon_of(plan)
     prm = ar_muon_params_t(lr, mu, weight_decay, grad_scale, 1 if nesterov else 0)
-    if not plan:
-        _check(L.ar_muon_step(plan, None, None, None, None, None, ctypes.byref(prm), None))
-    s = L.ar_muon_plan_stats(plan)
-    g = _arena(grads, s.arena_count, s.grad_bytes, s.device, "grads")
-    m = _arena(momentum, s.arena_count, 4, s.device, "momentum")
-    w = _arena(weights, s.arena_count, s.weight_bytes, s.device, "weights")
-    mo = None if momentum_out is None else _arena(momentum_out, s.arena_count, 4, s.device, "momentum_out")
-    wo = None if weights_out is None else _arena(weights_out, s.arena_count, s.weight_bytes, s.device, "weights_out")
-    _check(L.ar_muon_step(plan, g, m, w, mo, wo, ctypes.byref(prm), _stream(stream)))
+    g = _arena(i, grads, i.arena, i.grad, "grads")
+    m = _arena(i, momentum, i.arena, 4, "momentum")
+    w = _arena(i, weights, i.arena, i.weight, "weights")
+    mo = None if momentum_out is None else _arena(i, momentum_out, i.arena, 4, "momentum_out")
+    wo = None if weights_out is None else _arena(i, weights_out, i.arena, i.weight, "weights_out")
+    if _lib.ar_muon_step(plan, g, m, w, mo, wo, ctypes.byref(prm), _stream(stream)) != AR_OK:
+        _raise()
 
 
 def ar_muon_plan_destroy(plan):
+    _muon_info.pop(plan, None)
     lib().ar_muon_plan_destroy(plan)

@@ -30,6 +30,7 @@ namespace {
 
 constexpr double kEps = 1e-7;
 constexpr int kThreads = 256;
+constexpr int kJoinLds = 65536;  // of a join's workgroup: two to a CU
 
 template <bool BF>
 __device__ __forceinline__ float load1(const void *p, int64_t i) {
@@ -204,136 +205,237 @@ __global__ __launch_bounds__(kThreads) void muon_scale(MuonArgs a, int ex, bool 
   }
 }
 
-// Workgroups go round the 8 XCDs (each with an L2 of its own) in turn; this
-// gives every XCD one run of neighbouring tiles.
-__device__ __forceinline__ int xcd_run(int p, int n) {
-  const int q = n / 8, r = n % 8, x = p % 8;
-  return x * q + min(x, r) + p / 8;
-}
-
 __device__ __forceinline__ float pow2(int e) { return ldexpf(1.0f, e); }
 
 __device__ __forceinline__ fx4 times(fx4 v, float f) { return fx4{v[0] * f, v[1] * f, v[2] * f, v[3] * f}; }
 
-// Stores C[m][n .. n+3] and, off the diagonal tiles, C[n .. n+3][m].
-__device__ __forceinline__ void store_sym(uint16_t *c, int ld, int m, int n, fx4 v, bool pair, bool mirror) {
-  const int64_t plane = static_cast<int64_t>(ld) * ld;
-  const int64_t at = static_cast<int64_t>(m) * ld + n;
-  store_pair4(c + at, c + plane + at, v, pair);
-  if (!mirror) return;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    _Float16 h, l;
-    split(v[i], h, l);
-    const int64_t to = static_cast<int64_t>(n + i) * ld + m;
-    c[to] = __builtin_bit_cast(uint16_t, h);
-    if (pair) c[plane + to] = __builtin_bit_cast(uint16_t, l);
+// Where the sums of a tile go: row(m, n, v) takes C[m][n .. n + 3], column(m,
+// n, v) takes C[m .. m + 3][n].  A and B are stored along rows, and off the
+// diagonal tiles along columns too, as the transposed tile; a tall matrix's
+// result, which is held transposed, along columns only.
+enum Product { kGram, kPoly, kMul, kLast };
+
+// A = X X^T
+struct FinishGram {
+  uint16_t *out;
+  int64_t plane;
+  float f;
+  int mp, ld;
+  bool pair, mirror;
+  __device__ __forceinline__ FinishGram(const MuonArgs &a, const MuonStep &k, const MuonMat &mat, bool mir)
+      : out(a.ws + mat.a), plane(static_cast<int64_t>(mat.mp) * mat.mp), f(pow2(k.ea - 2 * k.ex)), mp(mat.mp),
+        ld(mat.mp), pair(k.pair_ab), mirror(mir) {}
+  __device__ __forceinline__ bool along_rows() const { return true; }
+  __device__ __forceinline__ bool along_columns() const { return mirror; }
+  __device__ __forceinline__ void put(int r, int c, fx4 v) const {
+    if (r >= mp || c >= mp) return;
+    const int64_t at = static_cast<int64_t>(r) * ld + c;
+    store_pair4(out + at, out + plane + at, times(v, f), pair);
   }
+  __device__ __forceinline__ void row(int m, int n, fx4 v) const { put(m, n, v); }
+  __device__ __forceinline__ void column(int m, int n, fx4 v) const { put(n, m, v); }
+};
+
+// B = a I + b A + c A A
+struct FinishPoly {
+  uint16_t *out;
+  const uint16_t *src;
+  int64_t plane;
+  float fa, fb, fc;
+  int mp, ld;
+  bool pair, mirror;
+  __device__ __forceinline__ FinishPoly(const MuonArgs &a, const MuonStep &k, const MuonMat &mat, bool mir)
+      : out(a.ws + mat.b), src(a.ws + mat.a), plane(static_cast<int64_t>(mat.mp) * mat.mp),
+        fa(k.coef_a * pow2(k.eb)), fb(k.coef_b * pow2(k.eb - k.ea)), fc(k.coef_c * pow2(k.eb - 2 * k.ea)), mp(mat.mp),
+        ld(mat.mp), pair(k.pair_ab), mirror(mir) {}
+  __device__ __forceinline__ bool along_rows() const { return true; }
+  __device__ __forceinline__ bool along_columns() const { return mirror; }
+  // B[r][c .. c + 3]: A is as symmetric as its tiles were stored, so the
+  // transposed tile reads it where it will lie itself
+  __device__ __forceinline__ void put(int r, int c, fx4 v) const {
+    if (r >= mp || c >= mp) return;
+    const int64_t at = static_cast<int64_t>(r) * ld + c;
+    _Float16 h[4], l[4] = {0, 0, 0, 0};
+    __builtin_memcpy(h, __builtin_assume_aligned(src + at, 8), 8);
+    if (pair) __builtin_memcpy(l, __builtin_assume_aligned(src + plane + at, 8), 8);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      v[i] = fc * v[i] + fb * (static_cast<float>(h[i]) + static_cast<float>(l[i])) + (r == c + i ? fa : 0.0f);
+    store_pair4(out + at, out + plane + at, v, pair);
+  }
+  __device__ __forceinline__ void row(int m, int n, fx4 v) const { put(m, n, v); }
+  __device__ __forceinline__ void column(int m, int n, fx4 v) const { put(n, m, v); }
+};
+
+// X <- B X
+struct FinishMul {
+  uint16_t *out;
+  int64_t plane;
+  float f;
+  int mp, np, ld;
+  bool pair;
+  __device__ __forceinline__ FinishMul(const MuonArgs &a, const MuonStep &k, const MuonMat &mat, bool)
+      : out(a.ws + mat.x[k.from ^ 1]), plane(static_cast<int64_t>(mat.mp) * mat.np),
+        f(pow2(k.ex_next - k.eb - k.ex)), mp(mat.mp), np(mat.np), ld(mat.np), pair(k.pair_next) {}
+  __device__ __forceinline__ bool along_rows() const { return true; }
+  __device__ __forceinline__ bool along_columns() const { return false; }
+  __device__ __forceinline__ void row(int m, int n, fx4 v) const {
+    if (m >= mp || n >= np) return;
+    const int64_t at = static_cast<int64_t>(m) * ld + n;
+    store_pair4(out + at, out + plane + at, times(v, f), pair);
+  }
+  __device__ __forceinline__ void column(int, int, fx4) const {}
+};
+
+// The result: X, or the new weights.
+template <bool WBF>
+struct FinishLast {
+  const void *w;
+  void *w_out;
+  int64_t at;
+  float f, keep, lr;
+  int m_, n_, cols;
+  bool step, tall;
+  __device__ __forceinline__ FinishLast(const MuonArgs &a, const MuonStep &k, const MuonMat &mat, bool)
+      : w(a.w), w_out(a.w_out), at(mat.at), f(pow2(-k.eb - k.ex)), keep(a.keep), lr(a.lr * mat.scale), m_(mat.m),
+        n_(mat.n), cols(mat.cols), step(a.step), tall(mat.tall) {}
+  __device__ __forceinline__ bool along_rows() const { return !tall; }
+  __device__ __forceinline__ bool along_columns() const { return tall; }
+  // W[r][c .. c + 3] of the matrix as given, `left` columns from c on
+  __device__ __forceinline__ void put(int r, int c, int left, fx4 v) const {
+    v = times(v, f);
+    const int64_t to = at + static_cast<int64_t>(r) * cols + c;
+    if (left >= 4) {
+      if (step) {
+        const fx4 o = load4<WBF>(w, to);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = keep * o[i] - lr * v[i];
+      }
+      store4<WBF>(w_out, to, v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+        if (i < left) store1<WBF>(w_out, to + i, step ? keep * load1<WBF>(w, to + i) - lr * v[i] : v[i]);
+    }
+  }
+  __device__ __forceinline__ void row(int m, int n, fx4 v) const {
+    if (m < m_ && n < n_) put(m, n, n_ - n, v);
+  }
+  __device__ __forceinline__ void column(int m, int n, fx4 v) const {
+    if (m < m_ && n < n_) put(n, m, m_ - m, v);
+  }
+};
+
+template <class Out, class F>
+__device__ __forceinline__ void leave(char *lds, int pass, int tid, int m0, int n0, const F &f) {
+  if (f.along_rows()) Out::rows(lds, pass, tid, [&](int m, int n, fx4 v) { f.row(m0 + m, n0 + n, v); });
+  if (f.along_columns()) Out::columns(lds, pass, tid, [&](int m, int n, fx4 v) { f.column(m0 + m, n0 + n, v); });
 }
 
-// A = X X^T (POLY false) and B = a I + b A + c A A (POLY true).
-template <class S, bool POLY>
-__global__ __launch_bounds__(S::kThreads) void muon_sym(MuonArgs a, MuonStep k) {
+template <Product PR, bool WBF>
+struct FinishOf {
+  using type = FinishLast<WBF>;
+};
+template <>
+struct FinishOf<kGram, false> {
+  using type = FinishGram;
+};
+template <>
+struct FinishOf<kPoly, false> {
+  using type = FinishPoly;
+};
+template <>
+struct FinishOf<kMul, false> {
+  using type = FinishMul;
+};
+
+template <Product PR>
+__device__ __forceinline__ const MuonWork &work_of(const MuonArgs &a) {
+  return PR == kGram ? a.gram : PR == kPoly ? a.poly : a.mul;
+}
+
+// The products of one step: each workgroup works through its items.  A split
+// item's sums are stored in the order that the threads hold them.
+template <class S, Product PR, bool WBF>
+__global__ __launch_bounds__(S::kThreads) void muon_product(MuonArgs a, MuonStep k) {
+  constexpr bool kSym = PR == kGram || PR == kPoly;
   static_assert(S::BM == S::BN, "square tiles");
   extern __shared__ __align__(16) char lds[];
-  const MuonTile t = a.sym[xcd_run(blockIdx.x, gridDim.x)];
-  const MuonMat &mat = a.mats[t.mat];
-  const int mp = mat.mp, m0 = t.m * S::BM, n0 = t.n * S::BN;
-  const int64_t ld = POLY ? mp : mat.np;
-  const uint16_t *src = a.ws + (POLY ? mat.a : mat.x[k.from]);
-  const int64_t plane = mp * ld;
-  const bool pair = k.pair_ab;  // then X is a pair too
-  const uint16_t *hm = src + m0 * ld, *hn = src + n0 * ld;
-  const uint16_t *sa[3] = {hm, hm, hm + plane}, *sb[3] = {hn, hn + plane, hn};
-  using P = TileProduct<kF16, S, kMajorK, kMajorK, true>;
-  P p;
-  p.run(lds, sa, sb, pair ? 3 : 1, ld, ld, min(S::BM, mp - m0), min(S::BN, mp - n0), ld);
-  const bool mirror = t.m != t.n;
-  uint16_t *out = a.ws + (POLY ? mat.b : mat.a);
-  if constexpr (!POLY) {
-    const float f = pow2(k.ea - 2 * k.ex);
-    p.each([&](int m, int n, fx4 v) {
-      m += m0;
-      n += n0;
-      if (m < mp && n < mp) store_sym(out, mp, m, n, times(v, f), pair, mirror);
-    });
-  } else {
-    const float fa = k.coef_a * pow2(k.eb), fb = k.coef_b * pow2(k.eb - k.ea), fc = k.coef_c * pow2(k.eb - 2 * k.ea);
-    p.each([&](int m, int n, fx4 v) {
-      m += m0;
-      n += n0;
-      if (m >= mp || n >= mp) return;
-      const int64_t at = static_cast<int64_t>(m) * mp + n;
-      _Float16 h[4], l[4] = {0, 0, 0, 0};
-      __builtin_memcpy(h, __builtin_assume_aligned(src + at, 8), 8);
-      if (pair) __builtin_memcpy(l, __builtin_assume_aligned(src + plane + at, 8), 8);
+  const MuonWork &w = work_of<PR>(a);
+  for (int it = w.first[blockIdx.x]; it < w.first[blockIdx.x + 1]; ++it) {
+    const MuonItem t = w.items[it];
+    const MuonMat &mat = a.mats[t.mat];
+    const int mp = mat.mp, cols = kSym ? mp : mat.np, m0 = t.m * S::BM, n0 = t.n * S::BN;
+    const int64_t lda = PR == kGram ? mat.np : mat.mp, ldb = PR == kPoly ? mat.mp : mat.np;
+    const uint16_t *x = a.ws + mat.x[k.from] + t.k0 * (kSym ? 1 : ldb), *sq = a.ws + (PR == kPoly ? mat.a : mat.b) + t.k0;
+    const uint16_t *pa = (PR == kGram ? x : sq) + m0 * lda;
+    const uint16_t *pb = PR == kPoly ? sq + n0 * ldb : PR == kGram ? x + n0 * ldb : x + n0;
+    // X X^T for a single A takes X's hi alone: lo lies below A's rounding
+    const int pairs = k.pair_ab ? 3 : !kSym && k.pair_x ? 2 : 1;
+    using P = TileProduct<kF16, S, kMajorK, kSym ? kMajorK : kMajorMN, true>;
+    P p;
+    p.run(lds, pa, pb, lda, ldb, min(S::BM, mp - m0), min(S::BN, cols - n0), t.k1 - t.k0, pairs, mp * lda, mp * ldb);
+    if constexpr (S::BM * S::BN == kMuonSlot) {
+      if (t.slot >= 0) {
+        fx4 *slot = reinterpret_cast<fx4 *>(a.slots + static_cast<int64_t>(t.slot) * kMuonSlot) + threadIdx.x;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        v[i] = fc * v[i] + fb * (static_cast<float>(h[i]) + static_cast<float>(l[i])) + (m == n + i ? fa : 0.0f);
-      store_sym(out, mp, m, n, v, pair, mirror);
-    });
-  }
-}
-
-// X <- B X, or after the last step the result.
-template <class S, bool LAST, bool WBF>
-__global__ __launch_bounds__(S::kThreads) void muon_mul(MuonArgs a, MuonStep k) {
-  extern __shared__ __align__(16) char lds[];
-  const MuonTile t = a.full[xcd_run(blockIdx.x, gridDim.x)];
-  const MuonMat &mat = a.mats[t.mat];
-  const int mp = mat.mp, np = mat.np, m0 = t.m * S::BM, n0 = t.n * S::BN;
-  const int64_t xplane = static_cast<int64_t>(mp) * np, bplane = static_cast<int64_t>(mp) * mp;
-  const uint16_t *b = a.ws + mat.b + static_cast<int64_t>(m0) * mp, *x = a.ws + mat.x[k.from] + n0;
-  const uint16_t *sa[3] = {b, b, b + bplane}, *sb[3] = {x, x + xplane, x};
-  using P = TileProduct<kF16, S, kMajorK, kMajorMN, true>;
-  P p;
-  p.run(lds, sa, sb, k.pair_ab ? 3 : k.pair_x ? 2 : 1, mp, np, min(S::BM, mp - m0), min(S::BN, np - n0), mp);
-  if constexpr (!LAST) {
-    const float f = pow2(k.ex_next - k.eb - k.ex);
-    uint16_t *out = a.ws + mat.x[k.from ^ 1];
-    p.each([&](int m, int n, fx4 v) {
-      m += m0;
-      n += n0;
-      if (m >= mp || n >= np) return;
-      const int64_t at = static_cast<int64_t>(m) * np + n;
-      store_pair4(out + at, out + xplane + at, times(v, f), k.pair_next);
-    });
-  } else {
-    const float f = pow2(-k.eb - k.ex), lr = a.lr * mat.scale;
-    p.each([&](int m, int n, fx4 v) {
-      m += m0;
-      n += n0;
-      if (m >= mat.m || n >= mat.n) return;
-      const int64_t stride = mat.tall ? mat.cols : 1;
-      const int64_t at = mat.at + (mat.tall ? static_cast<int64_t>(n) * mat.cols + m
-                                            : static_cast<int64_t>(m) * mat.cols + n);
-      v = times(v, f);
-      const int left = mat.n - n;
-      if (!mat.tall && left >= 4) {
-        if (a.step) {
-          const fx4 w = load4<WBF>(a.w, at);
+        for (int i = 0; i < S::FM; ++i)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] = a.keep * w[i] - lr * v[i];
-        }
-        store4<WBF>(a.w_out, at, v);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (i < left) {
-            const int64_t to = at + i * stride;
-            store1<WBF>(a.w_out, to, a.step ? a.keep * load1<WBF>(a.w, to) - lr * v[i] : v[i]);
-          }
+          for (int j = 0; j < S::FN; ++j) slot[(i * S::FN + j) * S::kThreads] = p.acc[i][j];
+        continue;
       }
-    });
+    }
+    const typename FinishOf<PR, WBF>::type f(a, k, mat, t.m != t.n);
+    using Out = TileOut<S, P::kLds>;
+    Out::all(lds, p.acc, [&](int pass, int tid) { leave<Out>(lds, pass, tid, m0, n0, f); });
   }
 }
 
-using Shape0 = Shape<128, 128, 2, 2>;
-using Shape1 = Shape<64, 64, 2, 2>;
+// Split tiles: one pass of one tile's way out per workgroup.
+template <class S, Product PR, bool WBF>
+__global__ __launch_bounds__(S::kThreads) void muon_join(MuonArgs a, MuonStep k) {
+  using Out = TileOut<S, kJoinLds>;
+  extern __shared__ __align__(16) char lds[];
+  const MuonWork &w = work_of<PR>(a);
+  const MuonJoin t = w.joins[blockIdx.x / Out::kPasses];
+  const int pass = blockIdx.x % Out::kPasses;
+  const MuonMat &mat = a.mats[t.mat];
+  const fx4 *slot = reinterpret_cast<const fx4 *>(a.slots + static_cast<int64_t>(t.slot) * kMuonSlot) +
+                    static_cast<int64_t>(pass) * Out::IP * S::FN * S::kThreads + threadIdx.x;
+  fx4 v[Out::IP][S::FN];
+#pragma unroll
+  for (int i = 0; i < Out::IP; ++i)
+#pragma unroll
+    for (int j = 0; j < S::FN; ++j) v[i][j] = slot[(i * S::FN + j) * S::kThreads];
+  for (int c = 1; c < t.count; ++c) {
+    slot += kMuonSlot / 4;
+#pragma unroll
+    for (int i = 0; i < Out::IP; ++i)
+#pragma unroll
+      for (int j = 0; j < S::FN; ++j) {
+        const fx4 u = slot[(i * S::FN + j) * S::kThreads];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[i][j][e] += u[e];
+      }
+  }
+  Out::put(lds, v, threadIdx.x);
+  __syncthreads();
+  const typename FinishOf<PR, WBF>::type f(a, k, mat, t.m != t.n);
+  leave<Out>(lds, pass, threadIdx.x, t.m * S::BM, t.n * S::BN, f);
+}
+
+using Shape0 = Shape<256, 256, 2, 4>;
+using Shape1 = Shape<128, 128, 2, 2>;
+using Shape2 = Shape<64, 64, 2, 2, 4>;
 
 template <class K, class... A>
 hipError_t go(K kernel, int grid, int threads, int lds, hipStream_t s, const A &...args) {
   if (grid == 0) return hipSuccess;
+  if (lds > 65536) {  // more than 64 KB of LDS has to be asked for
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(kernel),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    if (e != hipSuccess) return e;
+  }
   AR_LAUNCH(kernel, dim3(grid), dim3(threads), lds, s, args...);
   return hipGetLastError();
 }
@@ -343,16 +445,30 @@ constexpr int lds_of() {
   return TileProduct<kF16, S, kMajorK, kMajorK, true>::kLds;
 }
 
-template <class S>
-hipError_t mul(const MuonArgs &a, const MuonStep &k, hipStream_t s) {
-  if (!k.last) return go(muon_mul<S, false, false>, a.nfull, S::kThreads, lds_of<S>(), s, a, k);
-  return a.w_bf16 ? go(muon_mul<S, true, true>, a.nfull, S::kThreads, lds_of<S>(), s, a, k)
-                  : go(muon_mul<S, true, false>, a.nfull, S::kThreads, lds_of<S>(), s, a, k);
+template <class S, Product PR, bool WBF>
+hipError_t product_of(const MuonArgs &a, const MuonWork &w, const MuonStep &k, hipStream_t s) {
+  // the call's mark goes on its last kernel
+  const LaunchEvents ev = t_launch_events;
+  if (w.njoins > 0) t_launch_events = LaunchEvents{};
+  const hipError_t e = go(muon_product<S, PR, WBF>, w.groups, S::kThreads, lds_of<S>(), s, a, k);
+  t_launch_events = ev;
+  if (e != hipSuccess || w.njoins == 0) return e;
+  if constexpr (S::BM * S::BN == kMuonSlot)
+    return go(muon_join<S, PR, WBF>, w.njoins * TileOut<S, kJoinLds>::kPasses, S::kThreads, kJoinLds, s, a, k);
+  else
+    return hipErrorInvalidValue;  // only the largest tiles are split
+}
+
+template <Product PR, bool WBF>
+hipError_t product(const MuonArgs &a, const MuonWork &w, const MuonStep &k, hipStream_t s) {
+  return w.shape == 0   ? product_of<Shape0, PR, WBF>(a, w, k, s)
+         : w.shape == 1 ? product_of<Shape1, PR, WBF>(a, w, k, s)
+                        : product_of<Shape2, PR, WBF>(a, w, k, s);
 }
 
 }  // namespace
 
-int muon_tile(int shape) { return shape == 0 ? Shape0::BM : Shape1::BM; }
+int muon_tile(int shape) { return shape == 0 ? Shape0::BM : shape == 1 ? Shape1::BM : Shape2::BM; }
 
 hipError_t muon_begin(const MuonArgs &a, int32_t ex0, bool pair, hipStream_t s) {
   hipError_t e;
@@ -372,17 +488,16 @@ hipError_t muon_begin(const MuonArgs &a, int32_t ex0, bool pair, hipStream_t s) 
 }
 
 hipError_t muon_gram(const MuonArgs &a, const MuonStep &k, hipStream_t s) {
-  if (a.shape_sym == 0) return go(muon_sym<Shape0, false>, a.nsym, Shape0::kThreads, lds_of<Shape0>(), s, a, k);
-  return go(muon_sym<Shape1, false>, a.nsym, Shape1::kThreads, lds_of<Shape1>(), s, a, k);
+  return product<kGram, false>(a, a.gram, k, s);
 }
 
 hipError_t muon_poly(const MuonArgs &a, const MuonStep &k, hipStream_t s) {
-  if (a.shape_sym == 0) return go(muon_sym<Shape0, true>, a.nsym, Shape0::kThreads, lds_of<Shape0>(), s, a, k);
-  return go(muon_sym<Shape1, true>, a.nsym, Shape1::kThreads, lds_of<Shape1>(), s, a, k);
+  return product<kPoly, false>(a, a.poly, k, s);
 }
 
 hipError_t muon_apply(const MuonArgs &a, const MuonStep &k, hipStream_t s) {
-  return a.shape_full == 0 ? mul<Shape0>(a, k, s) : mul<Shape1>(a, k, s);
+  if (!k.last) return product<kMul, false>(a, a.mul, k, s);
+  return a.w_bf16 ? product<kLast, true>(a, a.mul, k, s) : product<kLast, false>(a, a.mul, k, s);
 }
 
 }  // namespace ar_dev

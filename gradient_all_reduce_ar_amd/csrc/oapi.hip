@@ -237,17 +237,27 @@ struct ar_muon_plan {
   int64_t arena = 0;                  // elements an arena holds at least
   std::vector<ar_dev::MuonStep> steps;
   int32_t ex0 = 0;
-  // work lists, one after another, and the sizes of the workspace
-  std::vector<ar_dev::MuonTile> tiles;
-  int32_t nparts = 0, nblocks = 0, nsym = 0, nfull = 0, shape_sym = 0, shape_full = 0;
-  size_t mats_bytes = 0, tiles_bytes = 0, partial_bytes = 0, ws_bytes = 0;
+  // Work lists.  table holds them all for the device, one after another (see
+  // fill_table): the offsets are in bytes.
+  std::vector<ar_dev::MuonTile> parts, blocks;
+  struct Work {
+    std::vector<ar_dev::MuonItem> items;
+    std::vector<int32_t> first;
+    std::vector<ar_dev::MuonJoin> joins;
+    int32_t shape = 0;
+    size_t at_items = 0, at_first = 0, at_joins = 0;
+  } gram, poly, mul;
+  std::vector<char> table;
+  size_t at_parts = 0, at_blocks = 0;
+  // workspace: sums of squares, partial tiles, then X, A and B
+  size_t partial_bytes = 0, slot_bytes = 0, ws_bytes = 0;
   int device = -1;
-  void *d_mats = nullptr, *d_tiles = nullptr, *d_work = nullptr;  // d_work: partials, then X, A and B
+  void *d_table = nullptr, *d_work = nullptr;
   ar_host::CallMarks marks;
 
   void release() {
     marks.release();
-    for (void **p : {&d_mats, &d_tiles, &d_work}) {
+    for (void **p : {&d_table, &d_work}) {
       if (*p) (void)hipFree(*p);
       *p = nullptr;
     }
@@ -335,9 +345,159 @@ bool make_steps(int n, const double *abc, bool pair_ab, std::vector<MuonStep> &s
 
 int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 
+// One product over all matrices: a tile's row, column and contraction steps
+// (of kStep elements).
+constexpr int kStep = 64;
+struct Tile {
+  int32_t mat, m, n, steps;
+};
+
+// Tile shapes: workgroups that run at once, and the microseconds of a tile's
+// contraction step where every CU has one workgroup at most (`alone`, a launch
+// of up to 256 tiles) and where the launch is full, and of the rest of a
+// tile's work.  Measured, e.g. alone: X X^T of 512 x 2048 with pairs 150, 68
+// and 42 us with the three shapes; full: of 12288 x 4096 831, 982, 1232.
+struct ShapeCost {
+  int32_t slots;
+  double alone, full, rest;
+};
+constexpr ShapeCost kCost[ar_dev::kMuonShapes] = {{256, 1.45, 1.7, 12.0}, {512, 0.65, 1.2, 5.0}, {512, 0.42, 0.8, 3.5}};
+// A split launch also writes and reads its partial tiles (256 KiB each, at
+// the rate of a large copy) and launches the join.
+constexpr double kJoinLaunch = 6.0, kJoinSlot = 2 * 262144 / 4.7e6;
+constexpr int32_t kMinPiece = 4;  // steps of a piece at least
+
+// The time until the last tile is done if each goes, in order, to the
+// workgroup with the least to do.  pairs: planes' products of a step.
+double list_time(const std::vector<Tile> &tiles, const ShapeCost &c, int pairs) {
+  std::vector<double> heap(c.slots, 0.0);  // the least on top
+  const auto more = [](double x, double y) { return x > y; };
+  const double step = pairs * (tiles.size() <= 256 ? c.alone : c.full);
+  double last = 0;
+  for (const Tile &t : tiles) {
+    std::pop_heap(heap.begin(), heap.end(), more);
+    heap.back() += t.steps * step + c.rest;
+    last = std::max(last, heap.back());
+    std::push_heap(heap.begin(), heap.end(), more);
+  }
+  return last;
+}
+
+// Splits a launch of the largest tiles over its workgroups: each gets whole
+// tiles while they fit into an equal share of the steps; the other tiles are
+// cut along the contraction to fill what is left of the shares.
+void split_tiles(const std::vector<Tile> &tiles, int32_t groups, ar_muon_plan::Work &w) {
+  int64_t total = 0;
+  for (const Tile &t : tiles) total += t.steps;
+  const int64_t share = (total + groups - 1) / groups + kMinPiece;
+  std::vector<std::vector<ar_dev::MuonItem>> of(groups);
+  std::vector<std::pair<int64_t, int32_t>> heap;  // (steps, workgroup), the least on top
+  for (int32_t g = 0; g < groups; ++g) heap.push_back({0, g});
+  const auto more = [](const auto &x, const auto &y) { return x > y; };
+  std::make_heap(heap.begin(), heap.end(), more);
+  std::vector<Tile> rest;
+  for (const Tile &t : tiles) {
+    if (heap.front().first + t.steps > share) {
+      rest.push_back(t);
+      continue;
+    }
+    std::pop_heap(heap.begin(), heap.end(), more);
+    heap.back().first += t.steps;
+    of[heap.back().second].push_back({t.mat, t.m, t.n, 0, t.steps * kStep, -1});
+    std::push_heap(heap.begin(), heap.end(), more);
+  }
+  // The first piece of each tile starts at the contraction's beginning, so
+  // that the workgroups that do these read the same columns of the operands
+  // at the same time; what is left of the tiles is dealt out in order.
+  struct Piece {
+    int32_t group, k0, k1;
+  };
+  std::vector<std::vector<Piece>> pieces(rest.size());
+  std::vector<int64_t> left(groups);
+  for (const auto &h : heap) left[h.second] = share - h.first;
+  std::vector<int32_t> room;
+  for (int32_t g = 0; g < groups; ++g)
+    if (left[g] >= kMinPiece) room.push_back(g);
+  auto give = [&](size_t i, int32_t g, int32_t from, int64_t n) {
+    const int32_t all = rest[i].steps;
+    if (all - from - n < kMinPiece) n = all - from;
+    pieces[i].push_back({g, from, static_cast<int32_t>(from + n)});
+    left[g] -= n;
+    return static_cast<int32_t>(from + n);
+  };
+  std::vector<int32_t> done(rest.size(), 0);
+  for (size_t i = 0; i < rest.size() && i < room.size(); ++i)
+    done[i] = give(i, room[i], 0, std::min<int64_t>(rest[i].steps, left[room[i]]));
+  int32_t g = 0;
+  for (size_t i = 0; i < rest.size(); ++i)
+    while (done[i] < rest[i].steps) {
+      while (g + 1 < groups && left[g] < kMinPiece) ++g;
+      const int64_t need = rest[i].steps - done[i];
+      done[i] = give(i, g, done[i], g + 1 == groups ? need : std::min(need, left[g]));
+    }
+  int32_t slot = 0;
+  for (size_t i = 0; i < rest.size(); ++i) {
+    const Tile &t = rest[i];
+    const int32_t n = static_cast<int32_t>(pieces[i].size());
+    if (n > 1) w.joins.push_back({t.mat, t.m, t.n, slot, n});
+    for (const Piece &x : pieces[i])
+      of[x.group].push_back({t.mat, t.m, t.n, x.k0 * kStep, x.k1 * kStep, n > 1 ? slot++ : -1});
+  }
+  // workgroup b runs on XCD b % 8: neighbouring shares go to one XCD, whose
+  // L2 then holds the operands that their tiles share
+  for (int32_t b = 0; b < groups; ++b) {
+    const int32_t s = groups % 8 ? b : b % 8 * (groups / 8) + b / 8;
+    w.first.push_back(static_cast<int32_t>(w.items.size()));
+    w.items.insert(w.items.end(), of[s].begin(), of[s].end());
+  }
+  w.first.push_back(static_cast<int32_t>(w.items.size()));
+}
+
+// Chooses the tile shape, whole or split, with the least modelled time, and
+// makes the launch's lists.
+template <class List>
+void plan_product(List list, int pairs, ar_muon_plan::Work &w) {
+  w = ar_muon_plan::Work{};
+  double best = 0;
+  bool split = false;
+  std::vector<Tile> tiles;
+  for (int i = 0; i < ar_dev::kMuonShapes; ++i) {
+    std::vector<Tile> t = list(ar_dev::muon_tile(i));
+    const ShapeCost &c = kCost[i];
+    const double whole = list_time(t, c, pairs);
+    double time = whole;
+    bool cut = false;
+    if (i == 0) {
+      int64_t total = 0;
+      for (const Tile &x : t) total += x.steps;
+      // pieces: about one per workgroup and one per split tile
+      const double n = static_cast<double>(t.size()), pieces = c.slots + std::min<double>(n, c.slots);
+      const double even = (static_cast<double>(total) / c.slots + kMinPiece) * pairs * c.full +
+                          std::ceil(n / c.slots) * c.rest + kJoinLaunch + pieces * kJoinSlot;
+      cut = even < whole;
+      time = std::min(even, whole);
+    }
+    if (tiles.empty() || time < best) {
+      best = time;
+      split = cut;
+      w.shape = i;
+      tiles = std::move(t);
+    }
+  }
+  if (split) return split_tiles(tiles, kCost[w.shape].slots, w);
+  // one workgroup per tile, neighbours on one XCD
+  const int32_t n = static_cast<int32_t>(tiles.size()), q = n / 8, r = n % 8;
+  for (int32_t b = 0; b < n; ++b) {
+    const int32_t x = b % 8;
+    const Tile &t = tiles[x * q + std::min(x, r) + b / 8];
+    w.first.push_back(b);
+    w.items.push_back({t.mat, t.m, t.n, 0, t.steps * kStep, -1});
+  }
+  w.first.push_back(n);
+}
+
 // Work lists and workspace layout.
 void lay_out(ar_muon_plan *p) {
-  p->tiles.clear();
   const bool pair_ab = !p->w_bf16;
   int64_t ws = 0, part0 = 0;
   auto take = [&](int64_t n) {
@@ -345,12 +505,13 @@ void lay_out(ar_muon_plan *p) {
     ws += n;
     return at;
   };
-  int64_t sym0 = 0, full0 = 0;  // tiles of the largest shape
-  const int64_t t0 = ar_dev::muon_tile(0);
-  for (MuonMat &m : p->mats) {
-    const int64_t size = static_cast<int64_t>(m.rows) * m.cols, x = static_cast<int64_t>(m.mp) * m.np;
+  const int32_t nm = static_cast<int32_t>(p->mats.size());
+  for (int32_t i = 0; i < nm; ++i) {
+    MuonMat &m = p->mats[i];
+    const int64_t size = static_cast<int64_t>(m.rows) * m.cols;
+    const int64_t x = static_cast<int64_t>(m.mp) * m.np;
     const int64_t sq = static_cast<int64_t>(m.mp) * m.mp * (pair_ab ? 2 : 1);
-    for (int i = 0; i < 2; ++i) m.x[i] = take(2 * x);
+    for (int b = 0; b < 2; ++b) m.x[b] = take(2 * x);
     m.a = take(sq);
     m.b = take(sq);
     // parts: of 4096 elements, larger where a matrix would have more than 1024
@@ -358,51 +519,63 @@ void lay_out(ar_muon_plan *p) {
     m.parts = static_cast<int32_t>((size + m.chunk - 1) / m.chunk);
     m.part0 = static_cast<int32_t>(part0);
     part0 += m.parts;
-    const int64_t r = up(m.mp, t0) / t0, c = up(m.np, t0) / t0;
-    sym0 += r * (r + 1) / 2;
-    full0 += r * c;
+    for (int32_t k = 0; k < m.parts; ++k) p->parts.push_back({i, k, 0});
+    for (int32_t r = 0; r < m.mp / 64; ++r)
+      for (int32_t c = 0; c < m.np / 64; ++c) p->blocks.push_back({i, r, c});
   }
-  p->shape_sym = sym0 >= 256 ? 0 : 1;
-  p->shape_full = full0 >= 256 ? 0 : 1;
-  const int32_t nm = static_cast<int32_t>(p->mats.size());
-  for (int32_t i = 0; i < nm; ++i)
-    for (int32_t k = 0; k < p->mats[i].parts; ++k) p->tiles.push_back({i, k, 0});
-  p->nparts = static_cast<int32_t>(p->tiles.size());
-  for (int32_t i = 0; i < nm; ++i)
-    for (int32_t r = 0; r < p->mats[i].mp / 64; ++r)
-      for (int32_t c = 0; c < p->mats[i].np / 64; ++c) p->tiles.push_back({i, r, c});
-  p->nblocks = static_cast<int32_t>(p->tiles.size()) - p->nparts;
   // product tiles: the matrices of the longest contraction first, so that
-  // what is left at a launch's end is short
+  // what is left at a launch's end is short; bands of kBand row tiles are
+  // swept together, so that neighbours share operands
+  constexpr int32_t kBand = 8;
   std::vector<int32_t> order(nm);
   for (int32_t i = 0; i < nm; ++i) order[i] = i;
   auto longest = [&](auto key) {
-    std::stable_sort(order.begin(), order.end(), [&](int32_t a, int32_t b) { return key(p->mats[a]) > key(p->mats[b]); });
+    std::stable_sort(order.begin(), order.end(),
+                     [&](int32_t a, int32_t b) { return key(p->mats[a]) > key(p->mats[b]); });
   };
-  constexpr int32_t kBand = 8;  // row tiles that are swept together
+  auto tiles = [&](int64_t bt, bool sym, bool wide) {  // wide: contracted over n, not m
+    std::vector<Tile> t;
+    for (int32_t i : order) {
+      const MuonMat &m = p->mats[i];
+      const int32_t r = static_cast<int32_t>(up(m.mp, bt) / bt), c = sym ? r : static_cast<int32_t>(up(m.np, bt) / bt);
+      const int32_t steps = (wide ? m.np : m.mp) / kStep;
+      for (int32_t m0 = 0; m0 < r; m0 += kBand)
+        for (int32_t n = sym ? m0 : 0; n < c; ++n)
+          for (int32_t k = m0; k < std::min(r, m0 + kBand); ++k)
+            if (!sym || n >= k) t.push_back({i, k, n, steps});
+    }
+    return t;
+  };
   longest([](const MuonMat &m) { return m.np; });
-  int64_t bt = ar_dev::muon_tile(p->shape_sym);
-  for (int32_t i : order) {
-    const int32_t r = static_cast<int32_t>(up(p->mats[i].mp, bt) / bt);
-    for (int32_t m0 = 0; m0 < r; m0 += kBand)
-      for (int32_t n = m0; n < r; ++n)
-        for (int32_t m = m0; m < std::min(r, m0 + kBand); ++m)
-          if (n >= m) p->tiles.push_back({i, m, n});
-  }
-  p->nsym = static_cast<int32_t>(p->tiles.size()) - p->nparts - p->nblocks;
+  plan_product([&](int64_t bt) { return tiles(bt, true, true); }, pair_ab ? 3 : 1, p->gram);
   longest([](const MuonMat &m) { return m.mp; });
-  bt = ar_dev::muon_tile(p->shape_full);
-  for (int32_t i : order) {
-    const int32_t r = static_cast<int32_t>(up(p->mats[i].mp, bt) / bt), c = static_cast<int32_t>(up(p->mats[i].np, bt) / bt);
-    for (int32_t m0 = 0; m0 < r; m0 += kBand)
-      for (int32_t n = 0; n < c; ++n)
-        for (int32_t m = m0; m < std::min(r, m0 + kBand); ++m) p->tiles.push_back({i, m, n});
-  }
-  p->nfull = static_cast<int32_t>(p->tiles.size()) - p->nparts - p->nblocks - p->nsym;
-  p->mats_bytes = p->mats.size() * sizeof(MuonMat);
-  p->tiles_bytes = p->tiles.size() * sizeof(MuonTile);
+  plan_product([&](int64_t bt) { return tiles(bt, true, false); }, pair_ab ? 3 : 1, p->poly);
+  plan_product([&](int64_t bt) { return tiles(bt, false, false); }, pair_ab ? 3 : 2, p->mul);
+  int64_t slots = 0;
+  for (const ar_muon_plan::Work *w : {&p->gram, &p->poly, &p->mul})
+    for (const ar_dev::MuonJoin &j : w->joins) slots = std::max<int64_t>(slots, j.slot + j.count);
   p->partial_bytes = static_cast<size_t>(up(part0 * 8, 256));
+  p->slot_bytes = static_cast<size_t>(slots) * ar_dev::kMuonSlot * 4;
   p->ws_bytes = static_cast<size_t>(ws) * 2;
+}
+
+// The device table's contents: the matrices, then every list.
+void fill_table(ar_muon_plan *p) {
+  p->table.clear();
+  auto put = [&](const auto &v) {
+    const size_t at = p->table.size(), bytes = v.size() * sizeof(v[0]);
+    p->table.resize(static_cast<size_t>(up(static_cast<int64_t>(at + bytes), 256)));
+    if (bytes) std::memcpy(p->table.data() + at, v.data(), bytes);
+    return at;
+  };
+  (void)put(p->mats);
+  p->at_parts = put(p->parts);
+  p->at_blocks = put(p->blocks);
+  for (ar_muon_plan::Work *w : {&p->gram, &p->poly, &p->mul}) {
+    w->at_items = put(w->items);
+    w->at_first = put(w->first);
+    w->at_joins = put(w->joins);
+  }
 }
 
 void default_scales(ar_muon_plan *p) {
@@ -419,9 +592,10 @@ ar_status_t prepare(ar_muon_plan *p) {
     return AR_OK;
   }
   if (!p->mats.empty()) {
-    e = ar_host::device_table(&p->d_mats, p->mats.data(), p->mats_bytes);
-    if (e == hipSuccess) e = ar_host::device_table(&p->d_tiles, p->tiles.data(), p->tiles_bytes);
-    if (e == hipSuccess) e = ar_host::device_table(&p->d_work, nullptr, p->partial_bytes + p->ws_bytes);
+    fill_table(p);
+    e = ar_host::device_table(&p->d_table, p->table.data(), p->table.size());
+    if (e == hipSuccess)
+      e = ar_host::device_table(&p->d_work, nullptr, p->partial_bytes + p->slot_bytes + p->ws_bytes);
     if (e != hipSuccess) {
       p->release();
       return e == hipErrorOutOfMemory ? fail(AR_ERR_OOM, "Muon workspace allocation") : hip_fail(e, "Muon tables");
@@ -485,20 +659,25 @@ ar_status_t run(ar_muon_plan *p, const MuonCall &c, void *stream) {
   }
   ar_status_t st = prepare(p);
   if (st != AR_OK || p->mats.empty()) return st;
-  const MuonTile *t = static_cast<const MuonTile *>(p->d_tiles);
-  a.mats = static_cast<const MuonMat *>(p->d_mats);
-  a.parts = t;
-  a.blocks = a.parts + p->nparts;
-  a.sym = a.blocks + p->nblocks;
-  a.full = a.sym + p->nsym;
-  a.nparts = p->nparts;
-  a.nblocks = p->nblocks;
-  a.nsym = p->nsym;
-  a.nfull = p->nfull;
-  a.shape_sym = p->shape_sym;
-  a.shape_full = p->shape_full;
-  a.partials = static_cast<double *>(p->d_work);
-  a.ws = reinterpret_cast<uint16_t *>(static_cast<char *>(p->d_work) + p->partial_bytes);
+  const char *t = static_cast<const char *>(p->d_table);
+  a.mats = reinterpret_cast<const MuonMat *>(t);
+  a.parts = reinterpret_cast<const MuonTile *>(t + p->at_parts);
+  a.blocks = reinterpret_cast<const MuonTile *>(t + p->at_blocks);
+  a.nparts = static_cast<int32_t>(p->parts.size());
+  a.nblocks = static_cast<int32_t>(p->blocks.size());
+  auto work = [t](const ar_muon_plan::Work &w) {
+    return ar_dev::MuonWork{reinterpret_cast<const ar_dev::MuonItem *>(t + w.at_items),
+                            reinterpret_cast<const int32_t *>(t + w.at_first),
+                            reinterpret_cast<const ar_dev::MuonJoin *>(t + w.at_joins),
+                            static_cast<int32_t>(w.first.size()) - 1, static_cast<int32_t>(w.joins.size()), w.shape};
+  };
+  a.gram = work(p->gram);
+  a.poly = work(p->poly);
+  a.mul = work(p->mul);
+  char *dw = static_cast<char *>(p->d_work);
+  a.partials = reinterpret_cast<double *>(dw);
+  a.slots = reinterpret_cast<float *>(dw + p->partial_bytes);
+  a.ws = reinterpret_cast<uint16_t *>(dw + p->partial_bytes + p->slot_bytes);
   a.g = c.g;
   a.mom = c.mom;
   a.mom_out = c.mom_out;
@@ -667,6 +846,7 @@ ar_muon_plan_t *ar_muon_plan_create(int nmatrices, const size_t *rows, const siz
     default_scales(p);
     (void)make_steps(kNsSteps, nullptr, !p->w_bf16, p->steps, p->ex0);
     lay_out(p);
+    fill_table(p);
     return AR_OK;
   });
   if (st != AR_OK) {
@@ -718,11 +898,12 @@ ar_muon_stats_t ar_muon_plan_stats(const ar_muon_plan_t *p) {
   s.nmatrices = p->nmatrices;
   s.device = p->device;
   s.iterations = static_cast<int32_t>(p->steps.size());
-  s.launches = p->mats.empty() ? 0 : 2 + 3 * s.iterations;
+  const int32_t joins = !p->gram.joins.empty() + !p->poly.joins.empty() + !p->mul.joins.empty();
+  s.launches = p->mats.empty() ? 0 : 2 + (3 + joins) * s.iterations;
   s.grad_bytes = p->g_bf16 ? 2 : 4;
   s.weight_bytes = p->w_bf16 ? 2 : 4;
   s.arena_count = static_cast<uint64_t>(p->arena);
-  s.workspace_bytes = p->mats.empty() ? 0 : p->mats_bytes + p->tiles_bytes + p->partial_bytes + p->ws_bytes;
+  s.workspace_bytes = p->mats.empty() ? 0 : p->table.size() + p->partial_bytes + p->slot_bytes + p->ws_bytes;
   return s;
 }
 

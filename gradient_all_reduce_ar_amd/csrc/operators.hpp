@@ -36,7 +36,7 @@ hipError_t experts_weight_grad(const ExpertArgs &a, hipStream_t s);
 // One matrix.  m <= n: its smaller and larger side; tall: rows > cols, worked
 // on transposed.  mp, np: m and n rounded up to kMuonPad.  x, a, b: first
 // element (16-bit) of its buffers in the workspace: two X buffers of two
-// planes (hi, lo) of mp x np, A and B of two planes of mp x mp.
+// planes (hi, lo) of mp x np, A and B of one or two planes of mp x mp.
 struct MuonMat {
   int64_t at;  // first element in the arenas
   int64_t x[2], a, b;
@@ -45,7 +45,6 @@ struct MuonMat {
   int32_t part0, parts;  // its partial sums of squares
   int32_t chunk;         // elements of a part
   float scale;
-  int32_t pad;
 };
 constexpr int kMuonPad = 64;
 
@@ -53,12 +52,31 @@ struct MuonTile {
   int32_t mat, m, n;  // tile row and column; a part's number in m
 };
 
+// A product tile's contraction range [k0, k1) that one workgroup works on.
+// slot >= 0: the tile is split; the range's sums go to that slot of the
+// partial tiles, and a join adds the slots and finishes the tile.
+struct MuonItem {
+  int32_t mat, m, n, k0, k1, slot;
+};
+// A split tile: its slots are slot .. slot + count - 1.
+struct MuonJoin {
+  int32_t mat, m, n, slot, count;
+};
+// One launch's work: workgroup b does items first[b] .. first[b + 1] - 1.
+struct MuonWork {
+  const MuonItem *items;
+  const int32_t *first;
+  const MuonJoin *joins;
+  int32_t groups, njoins, shape;  // shape: of the tiles (muon_tile)
+};
+
 struct MuonArgs {
   const MuonMat *mats;
-  const MuonTile *parts, *blocks, *sym, *full;  // work lists
-  int32_t nparts, nblocks, nsym, nfull;
-  int32_t shape_sym, shape_full;  // tile shapes (muon_tile)
+  const MuonTile *parts, *blocks;  // work lists
+  int32_t nparts, nblocks;
+  MuonWork gram, poly, mul;  // X X^T, A A, B X
   double *partials;
+  float *slots;  // partial tiles
   uint16_t *ws;
   const void *g;
   const float *mom;
@@ -82,9 +100,11 @@ struct MuonStep {
   int32_t from;      // X buffer read
 };
 
-// Rows and columns of tile shape i (0: the largest).
+// Rows and columns of tile shape i (0: the largest, the one that can be
+// split into partial tiles of kMuonSlot sums).
 int muon_tile(int shape);
-constexpr int kMuonShapes = 2;
+constexpr int kMuonShapes = 3;
+constexpr int kMuonSlot = 256 * 256;
 
 hipError_t muon_begin(const MuonArgs &a, int32_t ex0, bool pair, hipStream_t s);
 hipError_t muon_gram(const MuonArgs &a, const MuonStep &k, hipStream_t s);

@@ -147,48 +147,50 @@ struct Operand {
 
   __device__ __forceinline__ void advance() { base += MJ == kMajorK ? kStepK : kStepK * ld; }
 
-  // Starts the loads of the stage at `base`, of whose contraction elements
-  // the first `left` exist (the rest are zeros).
-  __device__ __forceinline__ void load(int left, uint32_t lds) {
+  // For the last stage, of whose contraction elements the first `left` exist:
+  // the loads of the others give zeros.
+  __device__ __forceinline__ void cut(int left) {
     if constexpr (ALIGNED) {
-      const uint32_t wave = lds + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * (1024 * kPer);
-      if (left >= kStepK) {
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) load_to_lds(base, off[j], wave + j * 1024);
-      } else {
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-          int row, col;
-          where(j, row, col);
-          const bool in = (MJ == kMajorK ? col * 8 : row) < left;
-          load_to_lds(base, in ? off[j] : kOutOfRange, wave + j * 1024);
-        }
-      }
-    } else {
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
         int row, col;
         where(j, row, col);
-        const uint16_t *p;
-        int n;  // elements that exist
-        if constexpr (MJ == kMajorK) {
-          p = base + static_cast<int64_t>(min(row, valid - 1)) * ld + col * 8;
-          n = left - col * 8;
-        } else {
-          p = base + static_cast<int64_t>(row) * ld + col * 8;
-          n = row < left ? valid - col * 8 : 0;
-        }
-        s16x8 v = {};
-        if (n >= 8) {
-          __builtin_memcpy(&v, p, 16);
-        } else if (n > 0) {
-#pragma unroll
-          for (int i = 0; i < 7; ++i)
-            if (i < n) v[i] = static_cast<short>(p[i]);
-        }
-        reg[j] = v;
+        if ((MJ == kMajorK ? col * 8 : row) >= left) off[j] = kOutOfRange;
       }
     }
+  }
+
+  // Starts load j of the stage at `base`.  left: as for cut(), which the
+  // aligned form has called before if that is less than a stage.
+  __device__ __forceinline__ void load_one(int j, int left, uint32_t lds) {
+    if constexpr (ALIGNED) {
+      load_to_lds(base, off[j], lds + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * (1024 * kPer) + j * 1024);
+    } else {
+      int row, col;
+      where(j, row, col);
+      const uint16_t *p;
+      int n;  // elements that exist
+      if constexpr (MJ == kMajorK) {
+        p = base + static_cast<int64_t>(min(row, valid - 1)) * ld + col * 8;
+        n = left - col * 8;
+      } else {
+        p = base + static_cast<int64_t>(row) * ld + col * 8;
+        n = row < left ? valid - col * 8 : 0;
+      }
+      s16x8 v = {};
+      if (n >= 8) {
+        __builtin_memcpy(&v, p, 16);
+      } else if (n > 0) {
+#pragma unroll
+        for (int i = 0; i < 7; ++i)
+          if (i < n) v[i] = static_cast<short>(p[i]);
+      }
+      reg[j] = v;
+    }
+  }
+  __device__ __forceinline__ void load(int left, uint32_t lds) {
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) load_one(j, left, lds);
   }
 
   // The register path's second half: what load() read goes to LDS.
@@ -220,17 +222,113 @@ struct Operand {
   }
 };
 
-// Tile shape: BM x BN by WM x WN waves, each wave 16-row fragments.
-template <int BM_, int BN_, int WM_, int WN_>
+// Tile shape: BM x BN by WM x WN waves, each wave 16-row fragments; the LDS
+// holds kStages stages (of aligned operands; of others two).
+template <int BM_, int BN_, int WM_, int WN_, int STAGES = 2>
 struct Shape {
-  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, kStages = STAGES;
   static constexpr int kThreads = 64 * WM * WN;
   static constexpr int FM = BM / WM / 16, FN = BN / WN / 16;  // fragments of a wave
 };
 
-// The contraction: nseg pairs (A_s, B_s) of length k each, added into one sum
-// (a product of numbers held as sums of 16-bit parts is such a list).
-// Finishes with all LDS reads done.
+// The way out of a tile.  A lane's four sums lie in one row, 16 rows to an
+// instruction: stored from there, memory would see 32- or 64-byte pieces (a
+// weight gradient of 64 experts, 738 MB of fp32: 346 us; with whole lines and
+// non-temporal stores 196).  So the sums pass through the LDS, which the
+// contraction no longer needs, IP rows of fragments of each wave at a time,
+// and leave it along rows or along columns, four sums to a lane.
+// Banks: 16-byte chunk c of row r is kept at c ^ ((r >> 2 ^ r << 2) & 15),
+// which takes 8 values over 8 neighbouring rows (the writes) and 16 over 16
+// neighbouring groups of four rows (the reads along columns).
+template <class S, int LDS>
+struct TileOut {
+  static constexpr int kRowBytes = S::BN * 4;
+  // rows of fragments of a wave that fit, a power of two
+  static constexpr int fit(int ip) { return ip * 16 * S::WM * kRowBytes <= LDS ? ip : fit(ip / 2); }
+  static constexpr int IP = fit(S::FM), kPasses = S::FM / IP, kRows = IP * 16 * S::WM;
+  static_assert(S::BN >= 64 && IP >= 1, "16 chunks to a row, and room for one row of fragments");
+
+  static __device__ __forceinline__ char *at(char *lds, int row, int chunk) {
+    return lds + row * kRowBytes + ((chunk ^ (((row >> 2) ^ (row << 2)) & 15)) << 4);
+  }
+  // Tile row of the pass's row r.
+  static __device__ __forceinline__ int tile_row(int pass, int r) {
+    return r / (IP * 16) * (S::BM / S::WM) + pass * IP * 16 + r % (IP * 16);
+  }
+  // v: this thread's sums of fragment rows pass * IP ..
+  static __device__ __forceinline__ void put(char *lds, const fx4 (&v)[IP][S::FN], int tid) {
+    const int wave = tid >> 6, lane = tid & 63;
+    const int row = wave / S::WN * (IP * 16) + (lane & 15), chunk = wave % S::WN * (S::BN / S::WN / 4) + (lane >> 4);
+#pragma unroll
+    for (int i = 0; i < IP; ++i)
+#pragma unroll
+      for (int j = 0; j < S::FN; ++j) *reinterpret_cast<fx4 *>(at(lds, row + i * 16, chunk + j * 4)) = v[i][j];
+  }
+  // f(m, n, v): v holds C[m][n .. n + 3] of the tile, neighbouring lanes along n.
+  template <class F>
+  static __device__ __forceinline__ void rows(char *lds, int pass, int tid, F f) {
+    constexpr int kAll = kRows * S::BN / 4;
+    static_assert(kAll % S::kThreads == 0, "whole rounds");
+#pragma unroll 4
+    for (int r = 0; r < kAll / S::kThreads; ++r) {
+      const int c = r * S::kThreads + tid, row = c / (S::BN / 4), chunk = c % (S::BN / 4);
+      f(tile_row(pass, row), chunk * 4, *reinterpret_cast<const fx4 *>(at(lds, row, chunk)));
+    }
+  }
+  // f(m, n, v): v holds C[m .. m + 3][n], neighbouring lanes along m.
+  template <class F>
+  static __device__ __forceinline__ void columns(char *lds, int pass, int tid, F f) {
+    constexpr int kAll = kRows / 4 * S::BN;
+#pragma unroll 4
+    for (int r = 0; r < kAll / S::kThreads; ++r) {
+      const int c = r * S::kThreads + tid, row = c % (kRows / 4) * 4, n = c / (kRows / 4);
+      fx4 v;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = reinterpret_cast<const float *>(at(lds, row + i, n >> 2))[n & 3];
+      f(tile_row(pass, row), n, v);
+    }
+  }
+  // All of acc through f(pass, thread), called when the pass's sums are in
+  // the LDS.  The thread number is hidden from the compiler, which would
+  // compute the addresses of the way out before the contraction and hold them
+  // in registers through it.
+  template <class F>
+  static __device__ __forceinline__ void all(char *lds, const fx4 (&acc)[S::FM][S::FN], F f) {
+    int tid = threadIdx.x;
+    asm volatile("" : "+v"(tid));
+#pragma unroll
+    for (int pass = 0; pass < kPasses; ++pass) {
+      fx4 v[IP][S::FN];
+#pragma unroll
+      for (int i = 0; i < IP; ++i)
+#pragma unroll
+        for (int j = 0; j < S::FN; ++j) v[i][j] = acc[pass * IP + i][j];
+      if (pass > 0) __syncthreads();
+      put(lds, v, tid);
+      __syncthreads();
+      f(pass, tid);
+    }
+    __syncthreads();
+  }
+};
+
+// The contraction over k, or over up to three pairs of planes of length k
+// (a multiple of kStepK then) added into one sum: numbers held as the sum of
+// two 16-bit planes, hi and lo, give hi hi + hi lo + lo hi (three pairs), or
+// hi hi + hi lo where A has one plane (two).  Finishes with all LDS reads
+// done.
+//
+// Two loops.  Tiles of 256 x 256 with 8 waves (two per SIMD) hold their
+// fragments in two register sets: while the matrix instructions work on one
+// half of a stage, the other half's LDS reads and the next stage but one's
+// loads are issued between them, so that a stage costs one meeting and no
+// wait for the LDS.  Smaller tiles leave room for several workgroups on a CU,
+// which cover each other's waits, and read each fragment right before its
+// use.  bf16, 8192^3, both operands kMajorK: 1.36 PFLOP/s with the first loop
+// and this tile, 1.19 with the second; 128 x 128 tiles of 4 waves 1.05 with
+// the second, 0.99 with the first.  (16 waves with the second loop: 1.27; 4
+// waves of 128 x 128 with the first: 0.96; two wave groups that alternate
+// between LDS reads and matrix instructions: 1.24.)
 template <Elem16 E, class S, Major AM, Major BMJ, bool ALIGNED>
 struct TileProduct {
   using Elem = uint16_t;
@@ -238,51 +336,93 @@ struct TileProduct {
   using OpA = Operand<AM, S::BM, S::kThreads, ALIGNED>;
   using OpB = Operand<BMJ, S::BN, S::kThreads, ALIGNED>;
   static constexpr int kStage = OpA::kBytes + OpB::kBytes;
-  static constexpr int kLds = 2 * kStage;
+  static constexpr int kStages = ALIGNED ? S::kStages : 2;
+  static constexpr int kLds = kStages * kStage;
+  static constexpr bool kTwoSets = ALIGNED && S::BM * S::BN >= 256 * 256;
   fx4 acc[S::FM][S::FN];
+  OpA oa;
+  OpB ob;
+  // what is loaded next: stage `at` of `per` of pair `pair`
+  const uint16_t *a0, *b0;
+  int64_t lo_a, lo_b;  // elements from a hi plane to its lo plane
+  int64_t k, at, per;
+  int pair, pairs;
 
-  __device__ __forceinline__ void run(char *lds, const uint16_t *const *a, const uint16_t *const *b, int nseg,
-                                      int64_t lda, int64_t ldb, int validm, int validn, int64_t k) {
+  __device__ __forceinline__ int left() const {
+    return static_cast<int>(min(k - at * kStepK, static_cast<int64_t>(kStepK)));
+  }
+  __device__ __forceinline__ void next() {
+    if (++at < per) {
+      oa.advance();
+      ob.advance();
+    } else if (++pair < pairs) {
+      at = 0;
+      oa.base = a0 + (pair == 2 ? lo_a : 0);
+      ob.base = b0 + (pair == 1 ? lo_b : 0);
+    }
+  }
+  // Only a list of one pair may end inside a stage: the masks of cut() stay.
+  __device__ __forceinline__ int existing() {
+    const int n = left();
+    if (n < kStepK) {
+      oa.cut(n);
+      ob.cut(n);
+    }
+    return n;
+  }
+  __device__ __forceinline__ void load(uint32_t stage) {
+    const int n = existing();
+    oa.load(n, stage);
+    ob.load(n, stage + OpA::kBytes);
+    next();
+  }
+  __device__ __forceinline__ void land(char *stage) {
+    oa.land(stage);
+    ob.land(stage + OpA::kBytes);
+  }
+
+  __device__ __forceinline__ void run(char *lds, const uint16_t *a, const uint16_t *b, int64_t lda, int64_t ldb,
+                                      int validm, int validn, int64_t length, int npairs = 1, int64_t plane_a = 0,
+                                      int64_t plane_b = 0) {
 #pragma unroll
     for (int i = 0; i < S::FM; ++i)
 #pragma unroll
       for (int j = 0; j < S::FN; ++j) acc[i][j] = fx4{0, 0, 0, 0};
-    if (k <= 0) return;
+    if (length <= 0) return;
+    a0 = a;
+    b0 = b;
+    lo_a = plane_a;
+    lo_b = plane_b;
+    pairs = npairs;
+    k = length;
+    pair = 0;
+    at = 0;
+    per = (k + kStepK - 1) / kStepK;
+    oa.init(a, lda, validm);
+    ob.init(b, ldb, validn);
+    if constexpr (kTwoSets) two_sets(lds, per * pairs);
+    else one_set(lds, per * pairs);
+  }
+
+  __device__ __forceinline__ void one_set(char *lds, int64_t steps) {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int rm = wave / S::WN * (S::BM / S::WM), rn = wave % S::WN * (S::BN / S::WN);
     const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_offset(lds));
-    OpA oa;
-    OpB ob;
-    oa.init(a[0], lda, validm);
-    ob.init(b[0], ldb, validn);
-    const int64_t per = (k + kStepK - 1) / kStepK;
-    int seg = 0;
-    int64_t at = 0;  // stage of the segment that is loaded next
-    auto load = [&](int buf) {
-      const int left = static_cast<int>(min(k - at * kStepK, static_cast<int64_t>(kStepK)));
-      oa.load(left, lds0 + buf * kStage);
-      ob.load(left, lds0 + buf * kStage + OpA::kBytes);
-      if (++at < per) {
-        oa.advance();
-        ob.advance();
-      } else if (++seg < nseg) {
-        at = 0;
-        oa.base = a[seg];
-        ob.base = b[seg];
-      }
-    };
-    auto land = [&](int buf) {
-      oa.land(lds + buf * kStage);
-      ob.land(lds + buf * kStage + OpA::kBytes);
-    };
-    const int64_t steps = per * nseg;
-    load(0);
-    land(0);
+    constexpr int kAhead = kStages - 1;  // stages in flight when a step begins
+    constexpr int kLoads = OpA::kPer + OpB::kPer;
+    for (int i = 0; i < kAhead && i < steps; ++i) load(lds0 + i * kStage);
+    land(lds);
+    int buf = 0, to = kAhead;  // stage read, stage loaded
     for (int64_t t = 0; t < steps; ++t) {
-      const int buf = static_cast<int>(t & 1);
-      if constexpr (ALIGNED) loads_done_and_meet();
-      else __syncthreads();
-      if (t + 1 < steps) load(buf ^ 1);
+      if constexpr (!ALIGNED) {
+        __syncthreads();
+      } else if (kAhead > 1 && t + kAhead <= steps) {  // all but the newest kAhead - 1 stages have landed
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((kAhead - 1) * kLoads) : "memory");
+      } else {
+        loads_done_and_meet();
+      }
+      const bool more = t + kAhead < steps;
+      if (more) load(lds0 + to * kStage);
       const char *sa = lds + buf * kStage, *sb = sa + OpA::kBytes;
 #pragma unroll
       for (int ks = 0; ks < kStepK / 32; ++ks) {
@@ -296,25 +436,72 @@ struct TileProduct {
 #pragma unroll
           for (int j = 0; j < S::FN; ++j) acc[i][j] = mfma16<E>(fb[j], fa[i], acc[i][j]);
       }
-      if (t + 1 < steps) land(buf ^ 1);
+      if (more) land(lds + to * kStage);
+      buf = buf + 1 == kStages ? 0 : buf + 1;
+      to = to + 1 == kStages ? 0 : to + 1;
     }
     __syncthreads();
   }
 
-  __device__ __forceinline__ void run(char *lds, const uint16_t *a, const uint16_t *b, int64_t lda, int64_t ldb,
-                                      int validm, int validn, int64_t k) {
-    run(lds, &a, &b, 1, lda, ldb, validm, validn, k);
-  }
-
-  // f(m, n, v): v holds C[m][n .. n + 3] of the tile.
-  template <class F>
-  __device__ __forceinline__ void each(F f) const {
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    const int rm = wave / S::WN * (S::BM / S::WM) + (lane & 15), rn = wave % S::WN * (S::BN / S::WN) + (lane >> 4) * 4;
+  // Stage t lies in half t & 1 of the LDS.  Its first 32 contraction elements
+  // are in register set 0 when step t begins.  Step t: matrix instructions on
+  // set 0 while set 1 reads the stage's other 32; then every wave is done
+  // with the stage, and stage t + 1 has landed (its loads began a step ago):
+  // matrix instructions on set 1 while set 0 reads stage t + 1 and stage
+  // t + 2's loads start into the half that stage t leaves.
+  __device__ __forceinline__ void two_sets(char *lds, int64_t steps) {
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int rm = wave / S::WN * (S::BM / S::WM), rn = wave % S::WN * (S::BN / S::WN);
+    const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_offset(lds));
+    constexpr int kReads = S::FM + S::FN, kLoads = OpA::kPer + OpB::kPer;
+    s16x8 fa[2][S::FM], fb[2][S::FN];
+    auto read = [&](int set, const char *stage, int ks, int r) {
+      if (r < S::FN) fb[set][r] = OpB::fragment(stage + OpA::kBytes, rn + r * 16, ks);
+      else fa[set][r - S::FN] = OpA::fragment(stage, rm + (r - S::FN) * 16, ks);
+    };
+    load(lds0);
+    if (steps > 1) {
+      load(lds0 + kStage);
+      asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(kLoads) : "memory");
+    } else {
+      loads_done_and_meet();
+    }
 #pragma unroll
-    for (int i = 0; i < S::FM; ++i)
+    for (int r = 0; r < kReads; ++r) read(0, lds, 0, r);
+    for (int64_t t = 0; t < steps; ++t) {
+      const int buf = static_cast<int>(t & 1);
+      const char *stage = lds + buf * kStage, *other = lds + (buf ^ 1) * kStage;
 #pragma unroll
-      for (int j = 0; j < S::FN; ++j) f(rm + i * 16, rn + j * 16, acc[i][j]);
+      for (int i = 0; i < S::FM; ++i) {
+#pragma unroll
+        for (int r = i * kReads / S::FM; r < (i + 1) * kReads / S::FM; ++r) read(1, stage, 1, r);
+#pragma unroll
+        for (int j = 0; j < S::FN; ++j) acc[i][j] = mfma16<E>(fb[0][j], fa[0][i], acc[i][j]);
+        __builtin_amdgcn_sched_barrier(0);  // keeps the reads spread among the products
+      }
+      loads_done_and_meet();
+      const bool more = t + 2 < steps;
+      const uint32_t da = lds0 + buf * kStage, db = da + OpA::kBytes;
+      const int n = more ? existing() : kStepK;
+#pragma unroll
+      for (int i = 0; i < S::FM; ++i) {
+        if (more) {
+#pragma unroll
+          for (int r = i * kLoads / S::FM; r < (i + 1) * kLoads / S::FM; ++r) {
+            if (r < OpA::kPer) oa.load_one(r, n, da);
+            else ob.load_one(r - OpA::kPer, n, db);
+          }
+        }
+        // (behind the last stage: what another tile or stage left, not used)
+#pragma unroll
+        for (int r = i * kReads / S::FM; r < (i + 1) * kReads / S::FM; ++r) read(0, other, 0, r);
+#pragma unroll
+        for (int j = 0; j < S::FN; ++j) acc[i][j] = mfma16<E>(fb[1][j], fa[1][i], acc[i][j]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if (more) next();
+    }
+    loads_done_and_meet();
   }
 };
 

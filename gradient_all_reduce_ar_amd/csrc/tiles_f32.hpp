@@ -132,16 +132,6 @@ struct TileProductF32 {
     }
     __syncthreads();
   }
-
-  template <class F>
-  __device__ __forceinline__ void each(F f) const {
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    const int rm = wave / S::WN * (S::BM / S::WM) + (lane & 15), rn = wave % S::WN * (S::BN / S::WN) + (lane >> 4) * 4;
-#pragma unroll
-    for (int i = 0; i < S::FM; ++i)
-#pragma unroll
-      for (int j = 0; j < S::FN; ++j) f(rm + i * 16, rn + j * 16, acc[i][j]);
-  }
 };
 
 }  // namespace ar_dev
