@@ -177,8 +177,8 @@ class _Plan:
     def __init__(self, handle, destroy):
         self.handle, self.destroy = handle, destroy
 
-    def __del__(self):
-        if not sys.is_finalizing():  # then the library's module is gone already
+    def __del__(self, finalizing=sys.is_finalizing):
+        if not finalizing():  # then the library's module is gone already
             self.destroy(self.handle)
 
 
