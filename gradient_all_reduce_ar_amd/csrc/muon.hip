@@ -424,6 +424,232 @@ __global__ __launch_bounds__(S::kThreads) void muon_join(MuonArgs a, MuonStep k)
   leave<Out>(lds, pass, threadIdx.x, t.m * S::BM, t.n * S::BN, f);
 }
 
+// ---- Small matrices: everything in one launch
+//
+// A matrix whose X (hi and lo) and A or B fit into the LDS is worked on by one
+// workgroup from the gradient to the result.  The work is tens of matrix
+// instructions per wave and step; what a step costs is the LDS's latency and
+// five meetings, where a launch per product costs 4 to 6 us: four 64 x 64
+// matrices took 65 us in 17 launches and take 18 us here.  Each wave has
+// one block of every product, so that A can be overwritten by B and X by B X
+// after a meeting; the code is kept short (loops, not unrolled), since most of
+// it runs once and comes from memory.  m and n are padded with zeros to
+// multiples of 32; rows have 32 bytes more than their elements, so that eight
+// neighbouring rows start in different banks.
+__host__ __device__ constexpr int64_t pad32(int64_t v) { return (v + 31) / 32 * 32; }
+// Blocks of kRows x 32, one per wave: up to 64 x 64 in 8 waves of 16-row
+// blocks, up to 16 of 32 x 32 (128 x 128, 64 x 256) in 16 waves.
+template <bool TINY>
+struct Small {
+  static constexpr int kWaves = TINY ? 8 : 16, TX = TINY ? 1 : 2, kRows = 16 * TX, kThreads = 64 * kWaves;
+};
+
+template <int TX>  // 16-row fragments of the block: 1 or 2
+struct SmallTask {
+  static constexpr int kRows = 16 * TX;
+  fx4 acc[TX][2];
+  // kRows x 32 block at (i, j) of P Q over k, a multiple of 32.  P: rows of
+  // `pp` bytes along k; Q: the same with QT (Q^T in memory), else rows along
+  // the columns.  lo planes lie lp and lq bytes behind; pairs as in
+  // TileProduct::run.
+  template <bool QT>
+  __device__ __forceinline__ void run(const char *p, int pp, int lp, const char *q, int pq, int lq, int i, int j, int k,
+                                      int pairs) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int x = 0; x < TX; ++x)
+#pragma unroll
+      for (int y = 0; y < 2; ++y) acc[x][y] = fx4{0, 0, 0, 0};
+    const char *pr = p + (i + (lane & 15)) * pp + (lane >> 4) * 16;
+    const char *qr = QT ? q + (j + (lane & 15)) * pq + (lane >> 4) * 16
+                        : q + ((lane >> 4) * 8 + ((lane & 15) >> 2)) * pq + j * 2 + (lane & 3) * 8;
+    auto left = [&](int plane, int x, int ks) {
+      return *reinterpret_cast<const s16x8 *>(pr + plane * lp + x * 16 * pp + ks * 64);
+    };
+    auto right = [&](int plane, int y, int ks) {
+      if constexpr (QT) {
+        return *reinterpret_cast<const s16x8 *>(qr + plane * lq + y * 16 * pq + ks * 64);
+      } else {
+        s16x4 h[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          h[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)const_cast<char *>(
+              qr + plane * lq + (ks * 32 + e * 4) * pq + y * 32));
+        return s16x8(__builtin_shufflevector(h[0], h[1], 0, 1, 2, 3, 4, 5, 6, 7));
+      }
+    };
+    for (int ks = 0; ks < k / 32; ++ks) {
+      s16x8 ph[TX], qh[2], pl[TX] = {}, ql[2] = {};
+#pragma unroll
+      for (int x = 0; x < TX; ++x) {
+        ph[x] = left(0, x, ks);
+        if (pairs == 3) pl[x] = left(1, x, ks);
+      }
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        qh[y] = right(0, y, ks);
+        if (pairs >= 2) ql[y] = right(1, y, ks);
+      }
+#pragma unroll
+      for (int x = 0; x < TX; ++x)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          acc[x][y] = mfma16<kF16>(qh[y], ph[x], acc[x][y]);
+          if (pairs >= 2) acc[x][y] = mfma16<kF16>(ql[y], ph[x], acc[x][y]);
+          if (pairs == 3) acc[x][y] = mfma16<kF16>(qh[y], pl[x], acc[x][y]);
+        }
+    }
+  }
+  // f(m, n, v): v holds [m][n .. n + 3] of the product.
+  template <class F>
+  __device__ __forceinline__ void each(int i, int j, F f) const {
+    const_cast<SmallTask *>(this)->change(i, j, [&](int m, int n, const fx4 &v) { f(m, n, v); });
+  }
+  template <class F>
+  __device__ __forceinline__ void change(int i, int j, F f) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int x = 0; x < TX; ++x)
+#pragma unroll
+      for (int y = 0; y < 2; ++y) f(i + x * 16 + (lane & 15), j + y * 16 + (lane >> 4) * 4, acc[x][y]);
+  }
+};
+
+template <bool GBF, bool WBF, bool STEP, bool TINY>
+__global__ __launch_bounds__(Small<TINY>::kThreads) void muon_small_kernel(MuonArgs a, MuonSteps st) {
+  using Sm = Small<TINY>;
+  extern __shared__ __align__(16) char lds[];
+  __shared__ double sums[Sm::kWaves];
+  const MuonMat &mat = a.mats[blockIdx.x];
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int mp = static_cast<int>(pad32(mat.m)), np = static_cast<int>(pad32(mat.n));
+  const int px = np * 2 + 32, pq = mp * 2 + 32, lx = mp * px, lq = mp * pq;
+  char *const x = lds, *const q = lds + 2 * lx;
+  const int cols = mat.cols, size = mat.rows * cols, whole = size & ~3;
+  // momentum and norm; the last size % 4 elements one by one
+  double sum = 0;
+#pragma unroll 2
+  for (int i = tid * 4; i < whole; i += Sm::kThreads * 4) {
+    const int64_t at = mat.at + i;
+    fx4 u = load4<GBF>(a.g, at);
+    if constexpr (STEP) {
+      fx4 m = load4<false>(a.mom, at);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        m[e] = momentum_of(a, u[e], m[e]);
+        u[e] = update_of(a, u[e], m[e]);
+      }
+      store4<false>(a.mom_out, at, m);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sum += static_cast<double>(u[e]) * u[e];
+  }
+  if (whole + tid < size) {
+    const int64_t at = mat.at + whole + tid;
+    float u = load1<GBF>(a.g, at);
+    if constexpr (STEP) {
+      const float m1 = momentum_of(a, u, a.mom[at]);
+      a.mom_out[at] = m1;
+      u = update_of(a, u, m1);
+    }
+    sum += static_cast<double>(u) * u;
+  }
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d);
+  if ((tid & 63) == 0) sums[wave] = sum;
+  for (int i = tid * 16; i < 2 * lx; i += Sm::kThreads * 16) *reinterpret_cast<ux4 *>(x + i) = ux4{0, 0, 0, 0};
+  __syncthreads();  // also: the new momentum can be read back
+  sum = 0;
+  for (int w = 0; w < Sm::kWaves; ++w) sum += sums[w];
+  const double inv = ldexp(1.0, st.ex0) / (sqrt(sum) + kEps);
+  auto fill = [&](int r, int c, float u) {
+    _Float16 hi, lo;
+    split(static_cast<float>(u * inv), hi, lo);
+    char *to = mat.tall ? x + c * px + r * 2 : x + r * px + c * 2;
+    *reinterpret_cast<_Float16 *>(to) = hi;
+    *reinterpret_cast<_Float16 *>(to + lx) = lo;
+  };
+  for (int i = tid * 4; i < whole; i += Sm::kThreads * 4) {
+    const int64_t at = mat.at + i;
+    fx4 u = load4<GBF>(a.g, at);
+    if constexpr (STEP) {
+      const fx4 m1 = load4<false>(a.mom_out, at);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) u[e] = update_of(a, u[e], m1[e]);
+    }
+    int r = i / cols, c = i - r * cols;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      fill(r, c, u[e]);
+      if (++c == cols) {
+        c = 0;
+        ++r;
+      }
+    }
+  }
+  if (whole + tid < size) {
+    const int i = whole + tid;
+    const float g = load1<GBF>(a.g, mat.at + i);
+    fill(i / cols, i % cols, STEP ? update_of(a, g, a.mom_out[mat.at + i]) : g);
+  }
+  __syncthreads();
+
+  // the wave's blocks of A and B (i, ja) and of X (i2, jx)
+  const int nb = mp / Sm::kRows, nm = mp / 32, nn = np / 32;
+  const bool square = wave < nb * nm, wide = wave < nb * nn;
+  const int i = wave / nm * Sm::kRows, j = wave % nm * 32, ix = wave / nn * Sm::kRows, jx = wave % nn * 32;
+  auto put = [&](char *base, int pitch, int plane, int m, int n, fx4 v) {
+    char *to = base + m * pitch + n * 2;
+    store_pair4(reinterpret_cast<uint16_t *>(to), reinterpret_cast<uint16_t *>(to + plane), v, true);
+  };
+  SmallTask<Sm::TX> task;
+  for (int step = 0; step < st.n; ++step) {
+    const MuonStep &k = st.k[step];
+    const int pairs = k.pair_ab ? 3 : 1;
+    if (square) {  // A = X X^T
+      const float f = pow2(k.ea - 2 * k.ex);
+      task.template run<true>(x, px, lx, x, px, lx, i, j, np, pairs);
+      task.each(i, j, [&](int m, int n, fx4 v) { put(q, pq, lq, m, n, times(v, f)); });
+    }
+    __syncthreads();
+    if (square) {  // B = a I + b A + c A A
+      const float fa = k.coef_a * pow2(k.eb), fb = k.coef_b * pow2(k.eb - k.ea), fc = k.coef_c * pow2(k.eb - 2 * k.ea);
+      task.template run<true>(q, pq, lq, q, pq, lq, i, j, mp, pairs);
+      task.change(i, j, [&](int m, int n, fx4 &v) {
+        const char *p = q + m * pq + n * 2;
+        _Float16 h[4], l[4] = {0, 0, 0, 0};
+        __builtin_memcpy(h, __builtin_assume_aligned(p, 8), 8);
+        if (k.pair_ab) __builtin_memcpy(l, __builtin_assume_aligned(p + lq, 8), 8);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          v[e] = fc * v[e] + fb * (static_cast<float>(h[e]) + static_cast<float>(l[e])) + (m == n + e ? fa : 0.0f);
+      });
+    }
+    __syncthreads();
+    if (square) task.each(i, j, [&](int m, int n, fx4 v) { put(q, pq, lq, m, n, v); });
+    __syncthreads();
+    if (wide) task.template run<false>(q, pq, lq, x, px, lx, ix, jx, mp, k.pair_ab ? 3 : k.pair_x ? 2 : 1);
+    if (k.last) break;
+    __syncthreads();
+    if (wide) {  // X <- B X
+      const float f = pow2(k.ex_next - k.eb - k.ex);
+      task.each(ix, jx, [&](int m, int n, fx4 v) { put(x, px, lx, m, n, times(v, f)); });
+    }
+    __syncthreads();
+  }
+  if (!wide) return;
+  const FinishLast<WBF> f(a, st.k[st.n - 1], mat, false);
+  task.each(ix, jx, [&](int m, int n, fx4 v) {
+    if (!mat.tall) {
+      f.row(m, n, v);
+    } else if (m < mat.m) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (n + e < mat.n) f.put(n + e, m, 1, fx4{v[e], 0, 0, 0});
+    }
+  });
+}
+
 using Shape0 = Shape<256, 256, 2, 4>;
 using Shape1 = Shape<128, 128, 2, 2>;
 using Shape2 = Shape<64, 64, 2, 2, 4>;
@@ -469,6 +695,34 @@ hipError_t product(const MuonArgs &a, const MuonWork &w, const MuonStep &k, hipS
 }  // namespace
 
 int muon_tile(int shape) { return shape == 0 ? Shape0::BM : shape == 1 ? Shape1::BM : Shape2::BM; }
+
+int64_t muon_small_lds(int64_t m, int64_t n) {
+  const int64_t mp = pad32(m), np = pad32(n);
+  // one block for each of the 16 waves; then the LDS holds it
+  return mp / 32 * (np / 32) <= Small<false>::kWaves ? 2 * mp * (np * 2 + 32 + mp * 2 + 32) : 0;
+}
+
+namespace {
+
+template <bool TINY>
+hipError_t small(const MuonArgs &a, const MuonSteps &k, int32_t nmats, int32_t lds, hipStream_t s) {
+  constexpr int t = Small<TINY>::kThreads;
+  if (a.step)
+    return a.g_bf16 ? (a.w_bf16 ? go(muon_small_kernel<true, true, true, TINY>, nmats, t, lds, s, a, k)
+                                : go(muon_small_kernel<true, false, true, TINY>, nmats, t, lds, s, a, k))
+                    : (a.w_bf16 ? go(muon_small_kernel<false, true, true, TINY>, nmats, t, lds, s, a, k)
+                                : go(muon_small_kernel<false, false, true, TINY>, nmats, t, lds, s, a, k));
+  return a.g_bf16 ? (a.w_bf16 ? go(muon_small_kernel<true, true, false, TINY>, nmats, t, lds, s, a, k)
+                              : go(muon_small_kernel<true, false, false, TINY>, nmats, t, lds, s, a, k))
+                  : (a.w_bf16 ? go(muon_small_kernel<false, true, false, TINY>, nmats, t, lds, s, a, k)
+                              : go(muon_small_kernel<false, false, false, TINY>, nmats, t, lds, s, a, k));
+}
+
+}  // namespace
+
+hipError_t muon_small(const MuonArgs &a, const MuonSteps &k, int32_t nmats, int32_t lds, bool tiny, hipStream_t s) {
+  return tiny ? small<true>(a, k, nmats, lds, s) : small<false>(a, k, nmats, lds, s);
+}
 
 hipError_t muon_begin(const MuonArgs &a, int32_t ex0, bool pair, hipStream_t s) {
   hipError_t e;

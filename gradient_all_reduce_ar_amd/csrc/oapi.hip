@@ -237,6 +237,8 @@ struct ar_muon_plan {
   int64_t arena = 0;                  // elements an arena holds at least
   std::vector<ar_dev::MuonStep> steps;
   int32_t ex0 = 0;
+  int32_t small_lds = 0;  // > 0: one launch, a workgroup per matrix (muon_small)
+  bool tiny = true;       // then: every matrix is up to 64 x 64
   // Work lists.  table holds them all for the device, one after another (see
   // fill_table): the offsets are in bytes.
   std::vector<ar_dev::MuonTile> parts, blocks;
@@ -498,6 +500,17 @@ void plan_product(List list, int pairs, ar_muon_plan::Work &w) {
 
 // Work lists and workspace layout.
 void lay_out(ar_muon_plan *p) {
+  int64_t lds = 0;
+  for (const MuonMat &m : p->mats) {
+    const int64_t n = ar_dev::muon_small_lds(m.m, m.n);
+    if (n == 0) lds = INT64_MAX;
+    lds = std::max(lds, n);
+    p->tiny = p->tiny && m.n <= 64;
+  }
+  if (lds > 0 && lds < INT64_MAX) {
+    p->small_lds = static_cast<int32_t>(lds);
+    return;
+  }
   const bool pair_ab = !p->w_bf16;
   int64_t ws = 0, part0 = 0;
   auto take = [&](int64_t n) {
@@ -594,7 +607,7 @@ ar_status_t prepare(ar_muon_plan *p) {
   if (!p->mats.empty()) {
     fill_table(p);
     e = ar_host::device_table(&p->d_table, p->table.data(), p->table.size());
-    if (e == hipSuccess)
+    if (e == hipSuccess && p->small_lds == 0)
       e = ar_host::device_table(&p->d_work, nullptr, p->partial_bytes + p->slot_bytes + p->ws_bytes);
     if (e != hipSuccess) {
       p->release();
@@ -689,6 +702,16 @@ ar_status_t run(ar_muon_plan *p, const MuonCall &c, void *stream) {
   hipEvent_t mark = nullptr;
   st = p->marks.of(s, &mark);
   if (st != AR_OK) return st;
+  if (p->small_lds > 0) {
+    ar_dev::MuonSteps k{};
+    k.n = static_cast<int32_t>(p->steps.size());
+    k.ex0 = p->ex0;
+    std::copy(p->steps.begin(), p->steps.end(), k.k);
+    ar_dev::t_launch_events = ar_dev::LaunchEvents{nullptr, mark};
+    const hipError_t e = ar_dev::muon_small(a, k, static_cast<int32_t>(p->mats.size()), p->small_lds, p->tiny, s);
+    ar_dev::t_launch_events = ar_dev::LaunchEvents{};
+    return e == hipSuccess ? AR_OK : hip_fail(e, "kernel launch");
+  }
   hipError_t e = ar_dev::muon_begin(a, p->ex0, p->steps[0].pair_x, s);
   for (const MuonStep &k : p->steps) {
     if (e == hipSuccess) e = ar_dev::muon_gram(a, k, s);
@@ -859,7 +882,7 @@ ar_muon_plan_t *ar_muon_plan_create(int nmatrices, const size_t *rows, const siz
 ar_status_t ar_muon_plan_set_iterations(ar_muon_plan_t *p, int n, const double *abc) {
   if (!p) return fail(AR_ERR_INVALID_ARG, "Muon plan is NULL");
   return guarded([&]() -> ar_status_t {
-    if (n < 1 || n > 32) return fail(AR_ERR_INVALID_ARG, "iterations must be from 1 to 32");
+    if (n < 1 || n > ar_dev::kMuonMaxSteps) return fail(AR_ERR_INVALID_ARG, "iterations must be from 1 to 32");
     std::vector<MuonStep> steps;
     int32_t ex0 = 0;
     if (!make_steps(n, abc, !p->w_bf16, steps, ex0))
@@ -899,7 +922,7 @@ ar_muon_stats_t ar_muon_plan_stats(const ar_muon_plan_t *p) {
   s.device = p->device;
   s.iterations = static_cast<int32_t>(p->steps.size());
   const int32_t joins = !p->gram.joins.empty() + !p->poly.joins.empty() + !p->mul.joins.empty();
-  s.launches = p->mats.empty() ? 0 : 2 + (3 + joins) * s.iterations;
+  s.launches = p->mats.empty() ? 0 : p->small_lds > 0 ? 1 : 2 + (3 + joins) * s.iterations;
   s.grad_bytes = p->g_bf16 ? 2 : 4;
   s.weight_bytes = p->w_bf16 ? 2 : 4;
   s.arena_count = static_cast<uint64_t>(p->arena);

@@ -100,6 +100,19 @@ struct MuonStep {
   int32_t from;      // X buffer read
 };
 
+constexpr int kMuonMaxSteps = 32;
+struct MuonSteps {
+  int32_t n, ex0;
+  MuonStep k[kMuonMaxSteps];
+};
+
+// Plans whose matrices all fit into the LDS of one CU run in one launch, a
+// workgroup per matrix: LDS bytes of an m x n matrix there (m <= n), 0 if it
+// does not fit.
+int64_t muon_small_lds(int64_t m, int64_t n);
+// tiny: all matrices are up to 64 x 64.
+hipError_t muon_small(const MuonArgs &a, const MuonSteps &k, int32_t nmats, int32_t lds, bool tiny, hipStream_t s);
+
 // Rows and columns of tile shape i (0: the largest, the one that can be
 // split into partial tiles of kMuonSlot sums).
 int muon_tile(int shape);

@@ -86,7 +86,8 @@ def check(got, want, tol, what):
 SHAPES = [
     [(1, 1)], [(1, 7)], [(9, 1)], [(64, 64)], [(33, 47), (47, 33), (1, 5), (64, 128), (128, 64)], [(65, 129)],
     [(130, 66)], [(255, 515)], [(300, 200), (16, 16), (200, 300)], [(8, 2048)], [(2048, 8)], [(512, 768), (768, 512)],
-    [(64, 64)] * 20, [(1024, 1024)],
+    [(64, 64)] * 20, [(1024, 1024)], [(128, 128), (1, 300)], [(64, 512), (512, 60)], [(65, 500)], [(96, 256)] * 3,
+    [(1, 1), (33, 47), (600, 300), (5, 3), (64, 64), (1, 700), (700, 1)],  # small ones beside one that is not
 ]
 
 
