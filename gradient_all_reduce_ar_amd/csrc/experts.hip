@@ -13,6 +13,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdint>
 #include <type_traits>
 
@@ -315,7 +316,10 @@ __global__ __launch_bounds__(P::Sh::kThreads) void experts_weights(ExpertArgs a)
   using T = typename P::Elem;
   extern __shared__ __align__(16) char lds[];
   const int mt = static_cast<int>((a.outf + S::BM - 1) / S::BM), nt = static_cast<int>((a.in + S::BN - 1) / S::BN);
-  const int64_t id = xcd_run(blockIdx.x, gridDim.x);
+  // Tiles in the order of the workgroups, which go round the XCDs: all of the
+  // device then writes one neighbourhood of the arena at a time (16384 rows,
+  // 64 experts, 2048 x 1408: 272 us; 323 with a run of tiles per XCD).
+  const int64_t id = blockIdx.x;
   const int per = mt * nt;
   const int e = static_cast<int>(id / per);
   int tm, tn;
@@ -393,17 +397,36 @@ hipError_t launch_rows(const ExpertArgs &a, hipStream_t s) {
   return launch(experts_rows<P, GRAD>, grid, S::kThreads, P::kLds, a, s);
 }
 
-// The largest tile whose rows the experts fill and which gives the CUs enough
-// workgroups, by the mean rows of an expert and the number of tiles.  bf16,
-// microseconds with Big / Square / Half / Small (rows, experts, in x out):
-//   16384, 8, 4096 x 12288 (2048 rows each):  1590 / 1890 / 2450 / 4690
-//   16384, 64, 1408 x 2048 (input gradient):   144 /  155 /  175 /  298
-//   16384, 4, 2048 x 2048 (544 big tiles):     191 /  178 /  196 /  402
-//   8192, 32, 2048 x 2048:                     138 /  129 /  140 /  213
-//   2048, 32, 2048 x 2048 (64 rows each):       81 /   96 /   72 /   80
-//   4096, 8, 1024 x 1024 (576 half tiles):      35 /   21 /   20 /   32
-//   1000, 8, 2047 x 1023 (184 half tiles):       - /   52 /   42 /   31
-//   64, 32, 4096 x 1536:                         - /   82 /   82 /   73
+// Which tile: the least of modelled times.  A tile's time is that of its
+// contraction steps (of 64) and a rest; `slots` tiles run at once.  One
+// workgroup on a CU goes faster than several (`alone`, launches of up to 256
+// tiles).  The model against measured times, bf16 (rows, experts, in x out:
+// Big / Square / Half / Small, microseconds):
+//   16384, 8, 4096 x 12288:  1570 / 1920 / 2370 / 4700   measured 1590 / 1890 / 2370 / 4690
+//   16384, 4, 2048 x 2048:    199 /  180 /  210 /  410             191 /  178 /  196 /  402
+//   8192, 32, 2048 x 2048:    133 /  130 /  131 /  210             138 /  129 /  140 /  213
+//   4096, 8, 1024 x 1024:      35 /   24 /   22 /   33              35 /   21 /   20 /   32
+//   64, 32, 4096 x 1536:      190 /   82 /   76 /   40                - /   82 /   82 /   73
+// fp32 (3001, 8, 1024 x 1536): - / 176 / 132 / 122, measured - / 140 / 131 / 126.
+struct TileCost {
+  double slots, alone, full, rest;
+};
+constexpr TileCost kBF16Cost[4] = {{256, 1.45, 1.7, 12}, {512, 0.65, 1.2, 5}, {768, 0.55, 1.12, 4}, {768, 0.4, 0.57, 3.5}};
+constexpr TileCost kF32Cost[4] = {{0, 0, 0, 0}, {512, 5.0, 10.7, 5}, {768, 2.8, 8.0, 4}, {768, 0.9, 2.1, 3.5}};
+
+template <class S, bool GRAD>
+double rows_time(const ExpertArgs &a, const TileCost &c) {
+  const double n = static_cast<double>(GRAD ? a.in : a.outf), steps = static_cast<double>(GRAD ? a.outf : a.in) / 64;
+  const double e = static_cast<double>(std::min<int64_t>(a.experts, a.tokens)), t = static_cast<double>(a.tokens);
+  // every expert ends inside a tile, half of it unused on average
+  const double tiles = std::max(e, t / S::BM + e / 2) * std::ceil(n / S::BN);
+  double rounds = tiles / c.slots;
+  // short launches end with a round that is not full; in long ones with
+  // several workgroups on a CU these end at different times
+  rounds = rounds < 2 || c.slots <= 256 ? std::ceil(rounds) : rounds + 0.5;
+  return rounds * (std::ceil(steps) * (tiles <= 256 ? c.alone : c.full) + c.rest);
+}
+
 template <bool GRAD>
 hipError_t rows(const ExpertArgs &a, hipStream_t s) {
   const int64_t e = a.experts;
@@ -418,11 +441,13 @@ hipError_t rows(const ExpertArgs &a, hipStream_t s) {
                     : launch(experts_few<false>, grid, 64 * kFewWaves, 0, a, s);
     }
   }
-  if (a.bf16 && a.aligned && a.tokens >= 256 * e && row_tiles<Big, GRAD>(a) >= 1024)
-    return launch_rows<Big, GRAD>(a, s);
-  if (a.tokens >= 128 * e && row_tiles<Square, GRAD>(a) >= 512) return launch_rows<Square, GRAD>(a, s);
-  if (a.tokens >= 48 * e && row_tiles<Half, GRAD>(a) >= 256) return launch_rows<Half, GRAD>(a, s);
-  return launch_rows<Small, GRAD>(a, s);
+  const TileCost *c = a.bf16 ? kBF16Cost : kF32Cost;
+  const double big = a.bf16 && a.aligned ? rows_time<Big, GRAD>(a, c[0]) : 1e300;
+  const double square = rows_time<Square, GRAD>(a, c[1]), half = rows_time<Half, GRAD>(a, c[2]);
+  const double small = rows_time<Small, GRAD>(a, c[3]);
+  if (big <= std::min({square, half, small})) return launch_rows<Big, GRAD>(a, s);
+  if (square <= std::min(half, small)) return launch_rows<Square, GRAD>(a, s);
+  return half <= small ? launch_rows<Half, GRAD>(a, s) : launch_rows<Small, GRAD>(a, s);
 }
 
 template <class S>
@@ -452,11 +477,18 @@ hipError_t launch_weights(const ExpertArgs &a, hipStream_t s) {
 hipError_t experts_forward(const ExpertArgs &a, hipStream_t s) { return rows<false>(a, s); }
 hipError_t experts_input_grad(const ExpertArgs &a, hipStream_t s) { return rows<true>(a, s); }
 
-// Square and Half, microseconds: 16384 rows, 64 experts, 2048 x 1408: 213 and
-// 236 (Big 221); 16384, 2, 512 x 512 (32 square tiles): 120 and 100; rows that
-// are not aligned, 8192, 8, 2047 x 2047: 546 and 485; fp32, 8192, 4, 2048 x
-// 2048: 987 and 1099.
+// Big where its tiles give every CU one and an expert's rows fill a few
+// steps; Half where Square's would leave CUs idle, and for operands that are
+// not aligned.  Microseconds Big / Square / Half (rows, experts, in x out):
+//   16384, 64, 2048 x 1408:         264 / 272 / 300
+//   16384, 8, 4096 x 2048:          295 / 346 /   -
+//   4096, 32, 2048 x 1024 (128 rows each, bf16 gradients): 68 / 65 / -
+//   16384, 2, 512 x 512 (32 square tiles):  245 / 120 / 100
+//   8192, 8, 2047 x 2047:             - / 546 / 485
+//   fp32, 8192, 4, 2048 x 2048:       - / 987 / 1099
 hipError_t experts_weight_grad(const ExpertArgs &a, hipStream_t s) {
+  if (a.bf16 && a.aligned && a.tokens >= 256 * static_cast<int64_t>(a.experts) && weight_tiles<Big>(a) >= 256)
+    return launch_weights<Big>(a, s);
   const bool half = weight_tiles<Square>(a) < 256 || (a.bf16 && !a.aligned);
   return half ? launch_weights<Half>(a, s) : launch_weights<Square>(a, s);
 }

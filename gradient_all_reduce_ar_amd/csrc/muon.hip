@@ -456,10 +456,11 @@ struct SmallTask {
   __device__ __forceinline__ void run(const char *p, int pp, int lp, const char *q, int pq, int lq, int i, int j, int k,
                                       int pairs) {
     const int lane = threadIdx.x & 63;
+    fx4 low[TX][2];  // hi lo + lo hi, added at the end (see TileProduct)
 #pragma unroll
     for (int x = 0; x < TX; ++x)
 #pragma unroll
-      for (int y = 0; y < 2; ++y) acc[x][y] = fx4{0, 0, 0, 0};
+      for (int y = 0; y < 2; ++y) acc[x][y] = low[x][y] = fx4{0, 0, 0, 0};
     const char *pr = p + (i + (lane & 15)) * pp + (lane >> 4) * 16;
     const char *qr = QT ? q + (j + (lane & 15)) * pq + (lane >> 4) * 16
                         : q + ((lane >> 4) * 8 + ((lane & 15) >> 2)) * pq + j * 2 + (lane & 3) * 8;
@@ -495,10 +496,16 @@ struct SmallTask {
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
           acc[x][y] = mfma16<kF16>(qh[y], ph[x], acc[x][y]);
-          if (pairs >= 2) acc[x][y] = mfma16<kF16>(ql[y], ph[x], acc[x][y]);
-          if (pairs == 3) acc[x][y] = mfma16<kF16>(qh[y], pl[x], acc[x][y]);
+          if (pairs >= 2) low[x][y] = mfma16<kF16>(ql[y], ph[x], low[x][y]);
+          if (pairs == 3) low[x][y] = mfma16<kF16>(qh[y], pl[x], low[x][y]);
         }
     }
+#pragma unroll
+    for (int x = 0; x < TX; ++x)
+#pragma unroll
+      for (int y = 0; y < 2; ++y)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[x][y][e] += low[x][y][e];
   }
   // f(m, n, v): v holds [m][n .. n + 3] of the product.
   template <class F>

@@ -314,9 +314,12 @@ struct TileOut {
 
 // The contraction over k, or over up to three pairs of planes of length k
 // (a multiple of kStepK then) added into one sum: numbers held as the sum of
-// two 16-bit planes, hi and lo, give hi hi + hi lo + lo hi (three pairs), or
-// hi hi + hi lo where A has one plane (two).  Finishes with all LDS reads
-// done.
+// two 16-bit planes, hi and lo, give hi lo + lo hi + hi hi (three pairs), or
+// hi lo + hi hi where A has one plane (two).  The small products come first:
+// every addition to a sum is off by a part of the sum (the matrix instruction
+// cuts), and with hi hi first the other two pairs would add to the full sum
+// (X X^T of 64 x 2432: 4.9e-6 off, in this order 2.1e-6).  Finishes with all
+// LDS reads done.
 //
 // Two loops.  Tiles of 256 x 256 with 8 waves (two per SIMD) hold their
 // fragments in two register sets: while the matrix instructions work on one
@@ -357,8 +360,8 @@ struct TileProduct {
       ob.advance();
     } else if (++pair < pairs) {
       at = 0;
-      oa.base = a0 + (pair == 2 ? lo_a : 0);
-      ob.base = b0 + (pair == 1 ? lo_b : 0);
+      oa.base = a0 + (pair + 2 == pairs ? lo_a : 0);
+      ob.base = b0;
     }
   }
   // Only a list of one pair may end inside a stage: the masks of cut() stay.
@@ -399,7 +402,7 @@ struct TileProduct {
     at = 0;
     per = (k + kStepK - 1) / kStepK;
     oa.init(a, lda, validm);
-    ob.init(b, ldb, validn);
+    ob.init(b + (pairs > 1 ? lo_b : 0), ldb, validn);
     if constexpr (kTwoSets) two_sets(lds, per * pairs);
     else one_set(lds, per * pairs);
   }
