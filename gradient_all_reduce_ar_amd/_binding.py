@@ -55,7 +55,7 @@ class ar_cost_params_t(ctypes.Structure):
 class ar_experts_stats_t(ctypes.Structure):
     _fields_ = [("nexperts", ctypes.c_int32), ("device", ctypes.c_int32), ("in_features", ctypes.c_uint64),
                 ("out_features", ctypes.c_uint64), ("elem_bytes", ctypes.c_uint64), ("grad_bytes", ctypes.c_uint64),
-                ("arena_count", ctypes.c_uint64)]
+                ("arena_count", ctypes.c_uint64), ("workspace_bytes", ctypes.c_uint64)]
 
 
 class ar_muon_stats_t(ctypes.Structure):

@@ -20,7 +20,6 @@
 #include "kernels.hpp"
 #include "operators.hpp"
 #include "tiles.hpp"
-#include "tiles_f32.hpp"
 
 namespace ar_dev {
 namespace {
@@ -177,7 +176,7 @@ __device__ __forceinline__ fx4 load4(const void *base, int64_t at, int n, bool v
 template <class P, bool GRAD>
 __global__ __launch_bounds__(P::Sh::kThreads) void experts_rows(ExpertArgs a) {
   using S = typename P::Sh;
-  using T = typename P::Elem;
+  using T = typename P::T;
   extern __shared__ __align__(16) char lds[];
   const int64_t n = GRAD ? a.in : a.outf, k = GRAD ? a.outf : a.in;
   const int nt = static_cast<int>((n + S::BN - 1) / S::BN);
@@ -212,14 +211,14 @@ struct Few {
   using T = std::conditional_t<BF, uint16_t, float>;
   static constexpr int kVec = 16 / sizeof(T);  // elements of a 16-byte load
   static constexpr int kPiece = 8 * kVec;      // of 128 bytes
-  struct Frag {
+  struct Piece {
     ux4 v[2];
   };
   // The lane's two loads of the piece at p (its own 32 bytes), of which the
   // first `n` elements exist.
   template <bool WHOLE>
-  static __device__ __forceinline__ Frag load(const T *p, int64_t n) {
-    Frag f;
+  static __device__ __forceinline__ Piece load(const T *p, int64_t n) {
+    Piece f;
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       f.v[c] = ux4{0, 0, 0, 0};
@@ -235,16 +234,11 @@ struct Few {
     }
     return f;
   }
-  static __device__ __forceinline__ fx4 add(const Frag &w, const Frag &x, fx4 acc) {
+  static __device__ __forceinline__ fx4 add(const Piece &w, const Piece &x, fx4 acc) {
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      if constexpr (BF) {
-        acc = mfma16<kBF16>(__builtin_bit_cast(s16x8, w.v[c]), __builtin_bit_cast(s16x8, x.v[c]), acc);
-      } else {
-        const fx4 fw = __builtin_bit_cast(fx4, w.v[c]), fx = __builtin_bit_cast(fx4, x.v[c]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(fw[i], fx[i], acc, 0, 0, 0);
-      }
+      constexpr Elem E = BF ? kBF16 : kF32;
+      acc = mfma16<E>(__builtin_bit_cast(Frag<E>, w.v[c]), __builtin_bit_cast(Frag<E>, x.v[c]), acc);
     }
     return acc;
   }
@@ -270,7 +264,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void experts_few(ExpertArgs a) {
   int64_t b = wave;
   auto work = [&](auto n) {
     constexpr int N = decltype(n)::value;
-    typename F::Frag fw[N], f0[N], f1[N];
+    typename F::Piece fw[N], f0[N], f1[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) fw[i] = F::template load<true>(w + (b + i * kFewWaves) * F::kPiece, 0);
 #pragma unroll
@@ -291,7 +285,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void experts_few(ExpertArgs a) {
   while (b < whole) work(std::integral_constant<int, 1>{});
   if (b == whole && a.in % F::kPiece != 0) {  // the piece that the rows end in
     const int64_t at = whole * F::kPiece, left = a.in - at - own;
-    const typename F::Frag fw = F::template load<false>(w + at, left);
+    const typename F::Piece fw = F::template load<false>(w + at, left);
     acc[0] = F::add(fw, F::template load<false>(x0 + at, left), acc[0]);
     if (two) acc[1] = F::add(fw, F::template load<false>(x1 + at, left), acc[1]);
   }
@@ -310,50 +304,122 @@ __global__ __launch_bounds__(64 * kFewWaves) void experts_few(ExpertArgs a) {
   if (m < t.rows && left > 0) store4<BF>(a.out, (t.row + m) * a.outs + n0 + (lane >> 4) * 4, v, left, a.vec_out);
 }
 
-template <class P, bool GBF>
-__global__ __launch_bounds__(P::Sh::kThreads) void experts_weights(ExpertArgs a) {
-  using S = typename P::Sh;
-  using T = typename P::Elem;
-  extern __shared__ __align__(16) char lds[];
+// One tile of one expert's weight gradient.
+struct WeightTile {
+  int e, row, rows;  // expert, its first row and number of rows
+  int64_t m0, n0;
+  int validm, validn;
+};
+template <class S>
+__device__ __forceinline__ WeightTile weight_tile(const ExpertArgs &a, int64_t id) {
+  WeightTile t;
   const int mt = static_cast<int>((a.outf + S::BM - 1) / S::BM), nt = static_cast<int>((a.in + S::BN - 1) / S::BN);
-  // Tiles in the order of the workgroups, which go round the XCDs: all of the
-  // device then writes one neighbourhood of the arena at a time (16384 rows,
-  // 64 experts, 2048 x 1408: 272 us; 323 with a run of tiles per XCD).
-  const int64_t id = blockIdx.x;
   const int per = mt * nt;
-  const int e = static_cast<int>(id / per);
   int tm, tn;
+  t.e = static_cast<int>(id / per);
   band_tile(static_cast<int>(id % per), mt, nt, tm, tn);
   int carry = 0, lo = 0, hi = 0;
-  for (int e0 = 0; e0 <= e; e0 += 64) scan_ends(a, e0, carry, lo, hi);
-  const int r0 = __builtin_amdgcn_readfirstlane(__shfl(lo, e & 63));
-  const int rows = __builtin_amdgcn_readfirstlane(__shfl(hi, e & 63)) - r0;
-  if (a.accumulate && rows == 0) return;
-  const int64_t m0 = static_cast<int64_t>(tm) * S::BM, n0 = static_cast<int64_t>(tn) * S::BN;
-  const int validm = static_cast<int>(min(static_cast<int64_t>(S::BM), a.outf - m0));
-  const int validn = static_cast<int>(min(static_cast<int64_t>(S::BN), a.in - n0));
-  const T *dy = static_cast<const T *>(a.dy) + r0 * a.dys + m0;
-  const T *x = static_cast<const T *>(a.x) + r0 * a.xs + n0;
-  const int64_t out = a.offsets[e] + m0 * a.in + n0;
-  P p;
-  p.run(lds, dy, x, a.dys, a.xs, validm, validn, rows);
-  using Out = TileOut<S, P::kLds>;
-  Out::all(lds, p.acc, [&](int pass, int tid) {
-    Out::rows(lds, pass, tid, [&](int m, int c, fx4 v) {
-      if (m >= validm || c >= validn) return;
-      const int64_t at = out + m * a.in + c;
-      if (a.accumulate) {
-        const fx4 old = load4<GBF>(a.out, at, validn - c, a.vec_out);
+  for (int e0 = 0; e0 <= t.e; e0 += 64) scan_ends(a, e0, carry, lo, hi);
+  t.row = __builtin_amdgcn_readfirstlane(__shfl(lo, t.e & 63));
+  t.rows = __builtin_amdgcn_readfirstlane(__shfl(hi, t.e & 63)) - t.row;
+  t.m0 = static_cast<int64_t>(tm) * S::BM;
+  t.n0 = static_cast<int64_t>(tn) * S::BN;
+  t.validm = static_cast<int>(min(static_cast<int64_t>(S::BM), a.outf - t.m0));
+  t.validn = static_cast<int>(min(static_cast<int64_t>(S::BN), a.in - t.n0));
+  return t;
+}
+
+// One pass of the tile's way into the arena.
+template <class Out, bool GBF>
+__device__ __forceinline__ void store_weights(const ExpertArgs &a, const WeightTile &t, char *lds, int pass, int tid) {
+  const int64_t out = a.offsets[t.e] + t.m0 * a.in + t.n0;
+  Out::rows(lds, pass, tid, [&](int m, int c, fx4 v) {
+    if (m >= t.validm || c >= t.validn) return;
+    const int64_t at = out + m * a.in + c;
+    if (a.accumulate) {
+      const fx4 old = load4<GBF>(a.out, at, t.validn - c, a.vec_out);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] += old[i];
-      }
-      store4<GBF, true>(a.out, at, v, validn - c, a.vec_out);
-    });
+      for (int i = 0; i < 4; ++i) v[i] += old[i];
+    }
+    store4<GBF, true>(a.out, at, v, t.validn - c, a.vec_out);
   });
 }
 
-template <class K>
-hipError_t launch(K kernel, int64_t grid, int threads, int lds, const ExpertArgs &a, hipStream_t s) {
+// Rows of one of `parts` parts of an expert's rows: whole stages.
+__device__ __forceinline__ int part_rows(int rows, int parts) { return ((rows + parts - 1) / parts + 63) & ~63; }
+
+// gridDim.y > 1: the expert's rows are cut into as many parts, whose sums go to
+// slots (in the order that the threads hold them) for experts_join.
+template <class P, bool GBF>
+__global__ __launch_bounds__(P::Sh::kThreads) void experts_weights(ExpertArgs a) {
+  using S = typename P::Sh;
+  using T = typename P::T;
+  extern __shared__ __align__(16) char lds[];
+  // Tiles in the order of the workgroups, which go round the XCDs: all of the
+  // device then writes one neighbourhood of the arena at a time (16384 rows,
+  // 64 experts, 2048 x 1408: 272 us; 323 with a run of tiles per XCD).
+  WeightTile t = weight_tile<S>(a, blockIdx.x);
+  if (a.accumulate && t.rows == 0) return;
+  const bool split = gridDim.y > 1;
+  int row = t.row, rows = t.rows;
+  if (split) {
+    const int part = part_rows(t.rows, gridDim.y), at = part * static_cast<int>(blockIdx.y);
+    if (at >= t.rows) return;
+    row += at;
+    rows = min(part, t.rows - at);
+  }
+  P p;
+  p.run(lds, static_cast<const T *>(a.dy) + row * a.dys + t.m0, static_cast<const T *>(a.x) + row * a.xs + t.n0, a.dys,
+        a.xs, t.validm, t.validn, rows);
+  if constexpr (S::BM * S::BN == kExpertSlot) {
+    if (split) {
+      fx4 *slot = reinterpret_cast<fx4 *>(a.slots + (static_cast<int64_t>(blockIdx.x) * gridDim.y + blockIdx.y) * kExpertSlot) +
+                  threadIdx.x;
+#pragma unroll
+      for (int i = 0; i < S::FM; ++i)
+#pragma unroll
+        for (int j = 0; j < S::FN; ++j) slot[(i * S::FN + j) * S::kThreads] = p.acc[i][j];
+      return;
+    }
+  }
+  using Out = TileOut<S, P::kLds>;
+  Out::all(lds, p.acc, [&](int pass, int tid) { store_weights<Out, GBF>(a, t, lds, pass, tid); });
+}
+
+// Adds the parts of each tile in their order; one row of fragments of a tile
+// per workgroup.
+template <class S, bool GBF>
+__global__ __launch_bounds__(S::kThreads) void experts_join(ExpertArgs a, int parts) {
+  constexpr int kLds = 16 * S::WM * S::BN * 4;
+  using Out = TileOut<S, kLds>;
+  static_assert(Out::IP == 1, "one row of fragments");
+  __shared__ __align__(16) char lds[kLds];
+  const int64_t id = blockIdx.x / S::FM;
+  const int pass = blockIdx.x % S::FM;
+  const WeightTile t = weight_tile<S>(a, id);
+  if (a.accumulate && t.rows == 0) return;
+  const fx4 *slot = reinterpret_cast<const fx4 *>(a.slots + id * parts * kExpertSlot) +
+                    static_cast<int64_t>(pass) * S::FN * S::kThreads + threadIdx.x;
+  fx4 v[1][S::FN];
+#pragma unroll
+  for (int j = 0; j < S::FN; ++j) v[0][j] = fx4{0, 0, 0, 0};
+  const int part = part_rows(t.rows, parts);
+  for (int at = 0; at < t.rows; at += part) {
+#pragma unroll
+    for (int j = 0; j < S::FN; ++j) {
+      const fx4 u = slot[j * S::kThreads];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[0][j][e] += u[e];
+    }
+    slot += kExpertSlot / 4;
+  }
+  Out::put(lds, v, threadIdx.x);
+  __syncthreads();
+  store_weights<Out, GBF>(a, t, lds, pass, threadIdx.x);
+}
+
+template <class K, class... A>
+hipError_t launch(K kernel, int64_t grid, int parts, int threads, int lds, hipStream_t s, const A &...args) {
   if (grid == 0) return hipSuccess;
   if (grid * threads > 0x7fffffff) return hipErrorInvalidConfiguration;
   // more than 64 KB of LDS has to be asked for
@@ -362,7 +428,7 @@ hipError_t launch(K kernel, int64_t grid, int threads, int lds, const ExpertArgs
                                              hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess) return e;
   }
-  AR_LAUNCH(kernel, dim3(static_cast<uint32_t>(grid)), dim3(threads), lds, s, a);
+  AR_LAUNCH(kernel, dim3(static_cast<uint32_t>(grid), parts), dim3(threads), lds, s, args...);
   return hipGetLastError();
 }
 
@@ -379,22 +445,20 @@ int64_t row_tiles(const ExpertArgs &a) {
   return (a.tokens / S::BM + std::min<int64_t>(a.experts, a.tokens)) * ((n + S::BN - 1) / S::BN);
 }
 
+template <Elem E, class S, bool GRAD, bool ALIGNED>
+hipError_t launch_rows(const ExpertArgs &a, hipStream_t s) {
+  using P = TileProduct<E, S, kMajorK, GRAD ? kMajorMN : kMajorK, ALIGNED>;
+  return launch(experts_rows<P, GRAD>, row_tiles<S, GRAD>(a), 1, S::kThreads, P::kLds, s, a);
+}
+
 template <class S, bool GRAD>
 hipError_t launch_rows(const ExpertArgs &a, hipStream_t s) {
-  const int64_t grid = row_tiles<S, GRAD>(a);
-  constexpr Major B = GRAD ? kMajorMN : kMajorK;
-  if constexpr (S::BM < 256) {  // the 256-row tile is for aligned bf16 alone
-    if (!a.bf16) {
-      using P = TileProductF32<S, kMajorK, B, false>;
-      return launch(experts_rows<P, GRAD>, grid, S::kThreads, P::kLds, a, s);
-    }
-    if (!a.aligned) {
-      using P = TileProduct<kBF16, S, kMajorK, B, false>;
-      return launch(experts_rows<P, GRAD>, grid, S::kThreads, P::kLds, a, s);
-    }
-  }
-  using P = TileProduct<kBF16, S, kMajorK, B, true>;
-  return launch(experts_rows<P, GRAD>, grid, S::kThreads, P::kLds, a, s);
+  if (a.aligned)
+    return a.bf16 ? launch_rows<kBF16, S, GRAD, true>(a, s) : launch_rows<kF32, S, GRAD, true>(a, s);
+  if constexpr (S::BM < 256)  // the largest tile is for aligned operands
+    return a.bf16 ? launch_rows<kBF16, S, GRAD, false>(a, s) : launch_rows<kF32, S, GRAD, false>(a, s);
+  else
+    return hipErrorInvalidValue;
 }
 
 // Which tile: the least of modelled times.  A tile's time is that of its
@@ -407,12 +471,15 @@ hipError_t launch_rows(const ExpertArgs &a, hipStream_t s) {
 //   8192, 32, 2048 x 2048:    133 /  130 /  131 /  210             138 /  129 /  140 /  213
 //   4096, 8, 1024 x 1024:      35 /   24 /   22 /   33              35 /   21 /   20 /   32
 //   64, 32, 4096 x 1536:      190 /   82 /   76 /   40                - /   82 /   82 /   73
-// fp32 (3001, 8, 1024 x 1536): - / 176 / 132 / 122, measured - / 140 / 131 / 126.
+// fp32:
+//   8192, 4, 2048 x 2048:    1000 / 670 / 595 / 760   measured 984 / 647 / 589 / 718
+//   3001, 8, 1024 x 1536:     500 / 131 /  95 / 127            254 / 135 / 109 / 125
+//   500, 4, 1000 x 1000:      250 /  77 /  44 /  36            250 /  72 /  43 /  28
 struct TileCost {
   double slots, alone, full, rest;
 };
 constexpr TileCost kBF16Cost[4] = {{256, 1.45, 1.7, 12}, {512, 0.65, 1.2, 5}, {768, 0.55, 1.12, 4}, {768, 0.4, 0.57, 3.5}};
-constexpr TileCost kF32Cost[4] = {{0, 0, 0, 0}, {512, 5.0, 10.7, 5}, {768, 2.8, 8.0, 4}, {768, 0.9, 2.1, 3.5}};
+constexpr TileCost kF32Cost[4] = {{256, 15, 15, 12}, {512, 4.5, 7.9, 5}, {768, 2.5, 5.7, 4}, {768, 0.9, 2.0, 3.5}};
 
 template <class S, bool GRAD>
 double rows_time(const ExpertArgs &a, const TileCost &c) {
@@ -437,12 +504,12 @@ hipError_t rows(const ExpertArgs &a, hipStream_t s) {
     const int64_t bytes = std::min(e, a.tokens) * a.in * a.outf * (a.bf16 ? 2 : 4);
     if (a.tokens <= 16 * e && bytes <= 16 << 20) {
       const int64_t grid = (a.tokens / kFewRows + std::min(e, a.tokens)) * ((a.outf + kFewCols - 1) / kFewCols);
-      return a.bf16 ? launch(experts_few<true>, grid, 64 * kFewWaves, 0, a, s)
-                    : launch(experts_few<false>, grid, 64 * kFewWaves, 0, a, s);
+      return a.bf16 ? launch(experts_few<true>, grid, 1, 64 * kFewWaves, 0, s, a)
+                    : launch(experts_few<false>, grid, 1, 64 * kFewWaves, 0, s, a);
     }
   }
   const TileCost *c = a.bf16 ? kBF16Cost : kF32Cost;
-  const double big = a.bf16 && a.aligned ? rows_time<Big, GRAD>(a, c[0]) : 1e300;
+  const double big = a.aligned ? rows_time<Big, GRAD>(a, c[0]) : 1e300;
   const double square = rows_time<Square, GRAD>(a, c[1]), half = rows_time<Half, GRAD>(a, c[2]);
   const double small = rows_time<Small, GRAD>(a, c[3]);
   if (big <= std::min({square, half, small})) return launch_rows<Big, GRAD>(a, s);
@@ -455,21 +522,44 @@ int64_t weight_tiles(const ExpertArgs &a) {
   return ((a.outf + S::BM - 1) / S::BM) * ((a.in + S::BN - 1) / S::BN) * a.experts;
 }
 
+// A split launch of few tiles: parts per expert, at least kPartRows rows each
+// on average, and partial tiles for at most kMaxSlots workgroups.
+constexpr int64_t kMaxSlots = 512, kMaxParts = 16, kPartRows = 256;
+int64_t most_parts(int64_t tiles) { return tiles <= 0 ? 1 : std::clamp<int64_t>(kMaxSlots / tiles, 1, kMaxParts); }
+
+template <Elem E, class S, bool GBF, bool ALIGNED>
+hipError_t launch_weights(const ExpertArgs &a, hipStream_t s) {
+  using P = TileProduct<E, S, kMajorMN, kMajorMN, ALIGNED>;
+  const int64_t tiles = weight_tiles<S>(a);
+  if constexpr (S::BM * S::BN == kExpertSlot) {
+    // 8001 rows of one expert, 512 x 768 (48 tiles): 73 us whole, 26 us in
+    // parts; 16000, 2, 1024 x 1024 (256 tiles): 96 and 67
+    const int64_t parts = std::min(most_parts(tiles), a.tokens / a.experts / kPartRows);
+    if (parts > 1 && a.slots) {
+      const LaunchEvents ev = t_launch_events;  // the call's mark goes on its last kernel
+      t_launch_events = LaunchEvents{};
+      const hipError_t e =
+          launch(experts_weights<P, GBF>, tiles, static_cast<int>(parts), S::kThreads, P::kLds, s, a);
+      t_launch_events = ev;
+      if (e != hipSuccess) return e;
+      return launch(experts_join<S, GBF>, tiles * S::FM, 1, S::kThreads, 0, s, a, static_cast<int>(parts));
+    }
+  }
+  return launch(experts_weights<P, GBF>, tiles, 1, S::kThreads, P::kLds, s, a);
+}
+
 template <class S>
 hipError_t launch_weights(const ExpertArgs &a, hipStream_t s) {
-  const int64_t grid = weight_tiles<S>(a);
-  if (!a.bf16) {
-    using P = TileProductF32<S, kMajorMN, kMajorMN, false>;
-    return launch(experts_weights<P, false>, grid, S::kThreads, P::kLds, a, s);
-  }
-  if (!a.aligned) {
-    using P = TileProduct<kBF16, S, kMajorMN, kMajorMN, false>;
-    return a.grad_bf16 ? launch(experts_weights<P, true>, grid, S::kThreads, P::kLds, a, s)
-                       : launch(experts_weights<P, false>, grid, S::kThreads, P::kLds, a, s);
-  }
-  using P = TileProduct<kBF16, S, kMajorMN, kMajorMN, true>;
-  return a.grad_bf16 ? launch(experts_weights<P, true>, grid, S::kThreads, P::kLds, a, s)
-                     : launch(experts_weights<P, false>, grid, S::kThreads, P::kLds, a, s);
+  if (a.aligned)
+    return !a.bf16       ? launch_weights<kF32, S, false, true>(a, s)
+           : a.grad_bf16 ? launch_weights<kBF16, S, true, true>(a, s)
+                         : launch_weights<kBF16, S, false, true>(a, s);
+  if constexpr (S::BM < 256)
+    return !a.bf16       ? launch_weights<kF32, S, false, false>(a, s)
+           : a.grad_bf16 ? launch_weights<kBF16, S, true, false>(a, s)
+                         : launch_weights<kBF16, S, false, false>(a, s);
+  else
+    return hipErrorInvalidValue;
 }
 
 }  // namespace
@@ -485,12 +575,22 @@ hipError_t experts_input_grad(const ExpertArgs &a, hipStream_t s) { return rows<
 //   4096, 32, 2048 x 1024 (128 rows each, bf16 gradients): 68 / 65 / -
 //   16384, 2, 512 x 512 (32 square tiles):  245 / 120 / 100
 //   8192, 8, 2047 x 2047:             - / 546 / 485
-//   fp32, 8192, 4, 2048 x 2048:       - / 987 / 1099
+//   fp32, 8192, 4, 2048 x 2048:       - / 582 / 548
 hipError_t experts_weight_grad(const ExpertArgs &a, hipStream_t s) {
   if (a.bf16 && a.aligned && a.tokens >= 256 * static_cast<int64_t>(a.experts) && weight_tiles<Big>(a) >= 256)
     return launch_weights<Big>(a, s);
-  const bool half = weight_tiles<Square>(a) < 256 || (a.bf16 && !a.aligned);
+  const bool half = weight_tiles<Square>(a) < 256 || !a.bf16 || !a.aligned;
   return half ? launch_weights<Half>(a, s) : launch_weights<Square>(a, s);
+}
+
+int64_t experts_weight_slots(int64_t experts, int64_t in, int64_t outf) {
+  static_assert(Half::BM * Half::BN == kExpertSlot, "Half's tiles are the ones that are split");
+  ExpertArgs a{};
+  a.experts = static_cast<int32_t>(experts);
+  a.in = in;
+  a.outf = outf;
+  const int64_t tiles = weight_tiles<Half>(a), parts = most_parts(tiles);
+  return parts > 1 ? tiles * parts : 0;
 }
 
 }  // namespace ar_dev

@@ -93,12 +93,16 @@ struct ar_experts {
   bool offsets_by_8 = true;  // every matrix starts on a multiple of 8 elements
   int device = -1;
   void *d_offsets = nullptr;
+  size_t slot_bytes = 0;     // partial tiles of split weight gradients
+  void *d_slots = nullptr;
   ar_host::CallMarks marks;
 
   void release() {
     marks.release();
-    if (d_offsets) (void)hipFree(d_offsets);
-    d_offsets = nullptr;
+    for (void **p : {&d_offsets, &d_slots}) {
+      if (*p) (void)hipFree(*p);
+      *p = nullptr;
+    }
     device = -1;
   }
 };
@@ -124,8 +128,11 @@ ar_status_t prepare(ar_experts *ex) {
     return AR_OK;
   }
   e = ar_host::device_table(&ex->d_offsets, ex->offsets.data(), ex->offsets.size() * sizeof(int64_t));
-  if (e == hipErrorOutOfMemory) return fail(AR_ERR_OOM, "expert offset table allocation");
-  if (e != hipSuccess) return hip_fail(e, "expert offset table");
+  if (e == hipSuccess && ex->slot_bytes > 0) e = ar_host::device_table(&ex->d_slots, nullptr, ex->slot_bytes);
+  if (e != hipSuccess) {
+    ex->release();
+    return e == hipErrorOutOfMemory ? fail(AR_ERR_OOM, "expert workspace allocation") : hip_fail(e, "expert tables");
+  }
   ex->device = dev;
   return AR_OK;
 }
@@ -175,6 +182,7 @@ ar_status_t run(ar_experts *ex, Which which, const RowsArg &r1, const RowsArg &r
   if (t == 0 && which != kWeightGrad) return AR_OK;
   ar_dev::ExpertArgs a{};
   a.offsets = static_cast<const int64_t *>(ex->d_offsets);
+  a.slots = static_cast<float *>(ex->d_slots);
   a.ends = ends;
   a.tokens = t;
   a.in = ex->in;
@@ -183,14 +191,18 @@ ar_status_t run(ar_experts *ex, Which which, const RowsArg &r1, const RowsArg &r
   a.bf16 = ex->bf16;
   a.grad_bf16 = ex->grad_bf16;
   a.accumulate = accumulate;
-  const bool rows16 = on(r1.p, 16) && r1.stride % 8 == 0;
+  // 16-byte rows; and offsets inside a tile of 256 rows fit into 31 bits
+  const size_t vec = static_cast<size_t>(16 / elem), far = (size_t{1} << 23) / elem;
+  auto rows16 = [&](const RowsArg &r) { return on(r.p, 16) && r.stride % vec == 0 && r.stride <= far; };
+  const bool by16 = static_cast<size_t>(ex->in) % vec == 0 && static_cast<size_t>(ex->out) % vec == 0 &&
+                    static_cast<size_t>(ex->in) <= far;
   if (which == kWeightGrad) {
     a.x = r1.p;
     a.xs = static_cast<int64_t>(r1.stride);
     a.dy = r2.p;
     a.dys = static_cast<int64_t>(r2.stride);
     a.out = const_cast<void *>(arena);
-    a.aligned = rows16 && on(r2.p, 16) && r2.stride % 8 == 0 && ex->in % 8 == 0 && ex->out % 8 == 0;
+    a.aligned = rows16(r1) && rows16(r2) && by16;
     a.vec_out = on(arena, 4 * aelem) && ex->in % 4 == 0 && ex->offsets_by_8;
   } else {
     a.w = arena;
@@ -198,7 +210,7 @@ ar_status_t run(ar_experts *ex, Which which, const RowsArg &r1, const RowsArg &r
     a.outs = static_cast<int64_t>(r2.stride);
     (which == kForward ? a.x : a.dy) = r1.p;
     (which == kForward ? a.xs : a.dys) = static_cast<int64_t>(r1.stride);
-    a.aligned = rows16 && on(arena, 16) && ex->offsets_by_8 && ex->in % 8 == 0 && ex->out % 8 == 0;
+    a.aligned = rows16(r1) && on(arena, 16) && ex->offsets_by_8 && by16;
     a.vec_out = on(r2.p, 4 * elem) && r2.stride % 4 == 0;
   }
   hipStream_t s = static_cast<hipStream_t>(stream);
@@ -754,6 +766,8 @@ ar_experts_t *ar_experts_create(int nexperts, size_t in_features, size_t out_fea
       ex->arena = std::max(ex->arena, at + size);
       ex->offsets_by_8 = ex->offsets_by_8 && at % 8 == 0;
     }
+    ex->slot_bytes =
+        static_cast<size_t>(ar_dev::experts_weight_slots(nexperts, ex->in, ex->out)) * ar_dev::kExpertSlot * 4;
     std::vector<int64_t> sorted = ex->offsets;
     std::sort(sorted.begin(), sorted.end());
     for (int e = 1; e < nexperts; ++e)
@@ -785,6 +799,7 @@ ar_experts_stats_t ar_experts_stats(const ar_experts_t *ex) {
   s.elem_bytes = ex->bf16 ? 2 : 4;
   s.grad_bytes = ex->grad_bf16 ? 2 : 4;
   s.arena_count = static_cast<uint64_t>(ex->arena);
+  s.workspace_bytes = ex->offsets.size() * sizeof(int64_t) + ex->slot_bytes;
   return s;
 }
 

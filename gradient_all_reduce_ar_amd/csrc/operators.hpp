@@ -25,11 +25,16 @@ struct ExpertArgs {
   bool accumulate;
   bool aligned;            // every row and matrix starts on 16 bytes
   bool vec_out;            // four consecutive outputs can be stored as one
+  float *slots;            // weight gradient: partial tiles (experts_weight_slots)
 };
 
 hipError_t experts_forward(const ExpertArgs &a, hipStream_t s);
 hipError_t experts_input_grad(const ExpertArgs &a, hipStream_t s);
 hipError_t experts_weight_grad(const ExpertArgs &a, hipStream_t s);
+// Partial tiles, of kExpertSlot sums, that the weight gradient of such experts
+// may use: 0 where its tiles are enough for the device.
+int64_t experts_weight_slots(int64_t experts, int64_t in, int64_t outf);
+constexpr int kExpertSlot = 64 * 128;
 
 // ---- Newton-Schulz and Muon (muon.hip)
 

@@ -2,24 +2,31 @@
 // Newton-Schulz products share (gfx950, device code).
 //
 // One workgroup computes a BM x BN tile of C = A B over a contraction of
-// length k, both operands 16-bit floats (bf16 or fp16), sums in fp32.  Each
-// operand lies in memory in one of two orders:
+// length k, both operands bf16, fp16 or fp32, sums in fp32.  Each operand lies
+// in memory in one of two orders:
 //   kMajorK   row r of the tile is contiguous along the contraction
 //             (A[r][k]; for B: B given as its transpose, [n][k])
 //   kMajorMN  step k of the contraction is contiguous along the tile
 //             (A given as [k][m]; B as [k][n])
-// and is staged in LDS in that order, kStepK = 64 contraction elements at a
-// time, in two stages: the loads of one stage are in flight while the matrix
-// instructions read the other.  MFMA wants 8 consecutive contraction elements
-// of one row in each lane: a kMajorK tile gives them with one 16-byte LDS
-// read, a kMajorMN tile with two transposing reads (ds_read_b64_tr_b16, which
-// hands each lane of a group of 16 one column of a 4 x 16 block).
+// and is staged in LDS in that order, 128 bytes of contraction elements at a
+// time (64 of 16 bits, 32 of fp32), in two or more stages: the loads of a
+// stage are in flight while the matrix instructions read another.  A lane
+// takes 16 bytes of consecutive contraction elements of one row: 8 of 16 bits
+// are one operand of a 16x16x32 matrix instruction, 4 of fp32 those of four
+// 16x16x4 (element j of every lane to the j-th: which contraction element
+// meets which lane does not matter as long as both operands agree).  A kMajorK
+// tile gives them with one 16-byte LDS read; a kMajorMN tile of 16-bit
+// elements with two transposing reads (ds_read_b64_tr_b16, which hands each
+// lane of a group of 16 one column of a 4 x 16 block), of fp32 with four
+// 4-byte reads.
 //
 // LDS banks.  A kMajorK row holds 128 bytes, so 16 lanes that read the same
 // 16-byte column of 16 rows would meet in 4 banks: column c of row r is kept
-// at c ^ (r & 7).  A kMajorMN row holds 2 BN bytes and half a wave reads one
-// 32-byte block of 8 rows (k, k+1, k+2, k+3 and the same plus 8): block b of
-// row k is kept at b ^ mn_swizzle(k), which takes 8 values over these rows.
+// at c ^ (r & 7).  A kMajorMN row holds W elements.  16 bits: half a wave
+// reads one 32-byte block of 8 rows (k, k+1, k+2, k+3 and the same plus 8);
+// block b of row k is kept at b ^ mn_swizzle(k), which takes 8 values over
+// these rows.  fp32: half a wave reads 64 bytes of rows k and k + 4, which are
+// kept 64 bytes apart (16-byte column c at c ^ (k & 4)).
 //
 // Aligned operands (16-byte rows and starts) go from memory to LDS without
 // passing through registers (buffer_load ... lds: lane l of the wave writes
@@ -31,6 +38,7 @@
 
 #include <cstdint>
 #include <cstring>
+#include <type_traits>
 
 namespace ar_dev {
 
@@ -42,9 +50,14 @@ typedef float fx4 __attribute__((ext_vector_type(4)));
 typedef uint32_t ux4 __attribute__((ext_vector_type(4)));
 typedef uint32_t ux2 __attribute__((ext_vector_type(2)));
 
-enum Elem16 { kBF16, kF16 };
+enum Elem { kBF16, kF16, kF32 };
 enum Major { kMajorK, kMajorMN };
-constexpr int kStepK = 64;
+template <Elem E>
+using ElemOf = std::conditional_t<E == kF32, float, uint16_t>;
+// 16 bytes of contraction elements.
+template <Elem E>
+using Frag = std::conditional_t<E == kF32, fx4, s16x8>;
+constexpr int kStepK = 64;  // contraction elements of a stage, 16 bits
 
 __device__ __forceinline__ uint32_t lds_offset(const void *p) {
   return static_cast<uint32_t>(
@@ -75,23 +88,24 @@ __device__ __forceinline__ void loads_done_and_meet() {
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
-template <int W>  // tile width in elements
+template <int W>  // tile width in 16-bit elements
 __device__ __forceinline__ constexpr int mn_swizzle(int k) {
   return W >= 128 ? ((k & 3) | ((k >> 3) & 1) << 2) : (((k >> 1) & 1) | ((k >> 3) & 1) << 1);
 }
 
-// Byte of the 16-byte chunk that holds, in a kMajorK tile, contraction
-// elements 8 c .. 8 c + 7 of row r.
-__device__ __forceinline__ constexpr int chunk_k(int r, int c) { return r * (kStepK * 2) + ((c ^ (r & 7)) << 4); }
-
-template <Elem16 E>
-__device__ __forceinline__ fx4 mfma16(s16x8 a, s16x8 b, fx4 c) {
-  if constexpr (E == kBF16)
+template <Elem E>
+__device__ __forceinline__ fx4 mfma16(Frag<E> a, Frag<E> b, fx4 c) {
+  if constexpr (E == kBF16) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
                                                    0, 0);
-  else
+  } else if constexpr (E == kF16) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0,
                                                   0);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[j], b[j], c, 0, 0, 0);
+    return c;
+  }
 }
 
 // One operand of a tile: W rows (kMajorK) or columns (kMajorMN) of it, loaded
@@ -100,35 +114,38 @@ __device__ __forceinline__ fx4 mfma16(s16x8 a, s16x8 b, fx4 c) {
 //   ld      elements between rows (kMajorK) or contraction steps (kMajorMN)
 //   valid   rows/columns of the tile that exist (>= 1); what lies beyond is
 //           loaded from the last one that exists (its products are not stored)
-template <Major MJ, int W, int NT, bool ALIGNED>
+template <Elem E, Major MJ, int W, int NT, bool ALIGNED>
 struct Operand {
-  static constexpr int kChunks = W * kStepK / 8;  // 16-byte chunks of a stage
-  static constexpr int kPer = kChunks / NT;       // per thread
-  static constexpr int kBytes = W * kStepK * 2;
+  using T = ElemOf<E>;
+  static constexpr int ES = sizeof(T), kVec = 16 / ES, kStep = 128 / ES;
+  static constexpr int kChunks = W * 8;      // 16-byte chunks of a stage
+  static constexpr int kPer = kChunks / NT;  // per thread
+  static constexpr int kBytes = W * 128;
+  static constexpr int kRow = W * ES / 16;   // chunks of a kMajorMN row
   static_assert(kPer * NT == kChunks, "whole chunks per thread");
 
-  const uint16_t *base;
+  const T *base;
   int64_t ld;
   int valid;
   uint32_t off[ALIGNED ? kPer : 1];  // bytes from base, contraction step 0
-  s16x8 reg[ALIGNED ? 1 : kPer];
+  ux4 reg[ALIGNED ? 1 : kPer];
 
   // Chunk j of this thread: its row in LDS, and which 16 bytes of that row
   // in memory land there.
   __device__ __forceinline__ void where(int j, int &row, int &col) const {
-    const int c = (threadIdx.x >> 6) * (64 * kPer) + j * 64 + (threadIdx.x & 63);
+    const int c = ALIGNED ? (threadIdx.x >> 6) * (64 * kPer) + j * 64 + (threadIdx.x & 63) : j * NT + threadIdx.x;
     if constexpr (MJ == kMajorK) {
       row = c >> 3;
       col = (c & 7) ^ (row & 7);
     } else {
-      constexpr int kRow = W / 8;  // chunks of a row
       row = c / kRow;
       const int p = c % kRow;
-      col = (((p >> 1) ^ mn_swizzle<W>(row)) << 1) | (p & 1);
+      if constexpr (E == kF32) col = p ^ (row & 4);
+      else col = (((p >> 1) ^ mn_swizzle<W>(row)) << 1) | (p & 1);
     }
   }
 
-  __device__ __forceinline__ void init(const uint16_t *b, int64_t l, int v) {
+  __device__ __forceinline__ void init(const T *b, int64_t l, int v) {
     base = b;
     ld = l;
     valid = v;
@@ -138,14 +155,15 @@ struct Operand {
         int row, col;
         where(j, row, col);
         if constexpr (MJ == kMajorK)
-          off[j] = static_cast<uint32_t>(min(row, valid - 1)) * static_cast<uint32_t>(ld * 2) + col * 16;
+          off[j] = static_cast<uint32_t>(min(row, valid - 1)) * static_cast<uint32_t>(ld * ES) + col * 16;
         else
-          off[j] = static_cast<uint32_t>(row) * static_cast<uint32_t>(ld * 2) + min(col * 8, (valid - 1) & ~7) * 2;
+          off[j] = static_cast<uint32_t>(row) * static_cast<uint32_t>(ld * ES) +
+                   min(col * kVec, (valid - 1) & ~(kVec - 1)) * ES;
       }
     }
   }
 
-  __device__ __forceinline__ void advance() { base += MJ == kMajorK ? kStepK : kStepK * ld; }
+  __device__ __forceinline__ void advance() { base += MJ == kMajorK ? kStep : kStep * ld; }
 
   // For the last stage, of whose contraction elements the first `left` exist:
   // the loads of the others give zeros.
@@ -155,7 +173,7 @@ struct Operand {
       for (int j = 0; j < kPer; ++j) {
         int row, col;
         where(j, row, col);
-        if ((MJ == kMajorK ? col * 8 : row) >= left) off[j] = kOutOfRange;
+        if ((MJ == kMajorK ? col * kVec : row) >= left) off[j] = kOutOfRange;
       }
     }
   }
@@ -168,22 +186,24 @@ struct Operand {
     } else {
       int row, col;
       where(j, row, col);
-      const uint16_t *p;
+      const T *p;
       int n;  // elements that exist
       if constexpr (MJ == kMajorK) {
-        p = base + static_cast<int64_t>(min(row, valid - 1)) * ld + col * 8;
-        n = left - col * 8;
+        p = base + static_cast<int64_t>(min(row, valid - 1)) * ld + col * kVec;
+        n = left - col * kVec;
       } else {
-        p = base + static_cast<int64_t>(row) * ld + col * 8;
-        n = row < left ? valid - col * 8 : 0;
+        p = base + static_cast<int64_t>(row) * ld + col * kVec;
+        n = row < left ? valid - col * kVec : 0;
       }
-      s16x8 v = {};
-      if (n >= 8) {
+      ux4 v = {};
+      if (n >= kVec) {
         __builtin_memcpy(&v, p, 16);
       } else if (n > 0) {
+        T h[kVec] = {};
 #pragma unroll
-        for (int i = 0; i < 7; ++i)
-          if (i < n) v[i] = static_cast<short>(p[i]);
+        for (int i = 0; i < kVec - 1; ++i)
+          if (i < n) h[i] = p[i];
+        __builtin_memcpy(&v, h, 16);
       }
       reg[j] = v;
     }
@@ -196,18 +216,25 @@ struct Operand {
   // The register path's second half: what load() read goes to LDS.
   __device__ __forceinline__ void land(char *stage) {
     if constexpr (!ALIGNED) {
-      char *w = stage + (threadIdx.x >> 6) * (1024 * kPer) + (threadIdx.x & 63) * 16;
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) *reinterpret_cast<s16x8 *>(w + j * 1024) = reg[j];
+      for (int j = 0; j < kPer; ++j) *reinterpret_cast<ux4 *>(stage + (j * NT + threadIdx.x) * 16) = reg[j];
     }
   }
 
-  // The 8 contraction elements 32 ks + 8 (lane / 16) .. of row/column
-  // r + lane % 16 of the stage.
-  static __device__ __forceinline__ s16x8 fragment(const char *stage, int r, int ks) {
+  // The 16 bytes of contraction elements from (ks * 4 + lane / 16) kVec on, of
+  // row/column r + lane % 16 of the stage.
+  static __device__ __forceinline__ Frag<E> fragment(const char *stage, int r, int ks) {
     const int lane = threadIdx.x & 63;
     if constexpr (MJ == kMajorK) {
-      return *reinterpret_cast<const s16x8 *>(stage + chunk_k(r + (lane & 15), ks * 4 + (lane >> 4)));
+      const int row = r + (lane & 15), c = ks * 4 + (lane >> 4);
+      return *reinterpret_cast<const Frag<E> *>(stage + row * 128 + ((c ^ (row & 7)) << 4));
+    } else if constexpr (E == kF32) {
+      const int i = r + (lane & 15);
+      const char *p = stage + (ks * 16 + (lane >> 4) * 4) * (W * 4) + (((i >> 2) ^ (lane >> 2 & 4)) << 4) + (i & 3) * 4;
+      fx4 v;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const float *>(p + j * (W * 4));
+      return v;
     } else {
       const int k = ks * 32 + (lane >> 4) * 8 + ((lane & 15) >> 2);
       s16x4 h[2];
@@ -332,12 +359,13 @@ struct TileOut {
 // the second, 0.99 with the first.  (16 waves with the second loop: 1.27; 4
 // waves of 128 x 128 with the first: 0.96; two wave groups that alternate
 // between LDS reads and matrix instructions: 1.24.)
-template <Elem16 E, class S, Major AM, Major BMJ, bool ALIGNED>
+template <Elem E, class S, Major AM, Major BMJ, bool ALIGNED>
 struct TileProduct {
-  using Elem = uint16_t;
+  using T = ElemOf<E>;
   using Sh = S;
-  using OpA = Operand<AM, S::BM, S::kThreads, ALIGNED>;
-  using OpB = Operand<BMJ, S::BN, S::kThreads, ALIGNED>;
+  using OpA = Operand<E, AM, S::BM, S::kThreads, ALIGNED>;
+  using OpB = Operand<E, BMJ, S::BN, S::kThreads, ALIGNED>;
+  static constexpr int kStep = OpA::kStep;
   static constexpr int kStage = OpA::kBytes + OpB::kBytes;
   static constexpr int kStages = ALIGNED ? S::kStages : 2;
   static constexpr int kLds = kStages * kStage;
@@ -346,13 +374,13 @@ struct TileProduct {
   OpA oa;
   OpB ob;
   // what is loaded next: stage `at` of `per` of pair `pair`
-  const uint16_t *a0, *b0;
+  const T *a0, *b0;
   int64_t lo_a, lo_b;  // elements from a hi plane to its lo plane
   int64_t k, at, per;
   int pair, pairs;
 
   __device__ __forceinline__ int left() const {
-    return static_cast<int>(min(k - at * kStepK, static_cast<int64_t>(kStepK)));
+    return static_cast<int>(min(k - at * kStep, static_cast<int64_t>(kStep)));
   }
   __device__ __forceinline__ void next() {
     if (++at < per) {
@@ -367,7 +395,7 @@ struct TileProduct {
   // Only a list of one pair may end inside a stage: the masks of cut() stay.
   __device__ __forceinline__ int existing() {
     const int n = left();
-    if (n < kStepK) {
+    if (n < kStep) {
       oa.cut(n);
       ob.cut(n);
     }
@@ -384,7 +412,7 @@ struct TileProduct {
     ob.land(stage + OpA::kBytes);
   }
 
-  __device__ __forceinline__ void run(char *lds, const uint16_t *a, const uint16_t *b, int64_t lda, int64_t ldb,
+  __device__ __forceinline__ void run(char *lds, const T *a, const T *b, int64_t lda, int64_t ldb,
                                       int validm, int validn, int64_t length, int npairs = 1, int64_t plane_a = 0,
                                       int64_t plane_b = 0) {
 #pragma unroll
@@ -400,7 +428,7 @@ struct TileProduct {
     k = length;
     pair = 0;
     at = 0;
-    per = (k + kStepK - 1) / kStepK;
+    per = (k + kStep - 1) / kStep;
     oa.init(a, lda, validm);
     ob.init(b + (pairs > 1 ? lo_b : 0), ldb, validn);
     if constexpr (kTwoSets) two_sets(lds, per * pairs);
@@ -428,8 +456,8 @@ struct TileProduct {
       if (more) load(lds0 + to * kStage);
       const char *sa = lds + buf * kStage, *sb = sa + OpA::kBytes;
 #pragma unroll
-      for (int ks = 0; ks < kStepK / 32; ++ks) {
-        s16x8 fa[S::FM], fb[S::FN];
+      for (int ks = 0; ks < 2; ++ks) {
+        Frag<E> fa[S::FM], fb[S::FN];
 #pragma unroll
         for (int i = 0; i < S::FM; ++i) fa[i] = OpA::fragment(sa, rm + i * 16, ks);
 #pragma unroll
@@ -446,9 +474,9 @@ struct TileProduct {
     __syncthreads();
   }
 
-  // Stage t lies in half t & 1 of the LDS.  Its first 32 contraction elements
-  // are in register set 0 when step t begins.  Step t: matrix instructions on
-  // set 0 while set 1 reads the stage's other 32; then every wave is done
+  // Stage t lies in half t & 1 of the LDS.  The first half of its contraction
+  // elements is in register set 0 when step t begins.  Step t: matrix instructions on
+  // set 0 while set 1 reads the stage's other half; then every wave is done
   // with the stage, and stage t + 1 has landed (its loads began a step ago):
   // matrix instructions on set 1 while set 0 reads stage t + 1 and stage
   // t + 2's loads start into the half that stage t leaves.
@@ -457,7 +485,7 @@ struct TileProduct {
     const int rm = wave / S::WN * (S::BM / S::WM), rn = wave % S::WN * (S::BN / S::WN);
     const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_offset(lds));
     constexpr int kReads = S::FM + S::FN, kLoads = OpA::kPer + OpB::kPer;
-    s16x8 fa[2][S::FM], fb[2][S::FN];
+    Frag<E> fa[2][S::FM], fb[2][S::FN];
     auto read = [&](int set, const char *stage, int ks, int r) {
       if (r < S::FN) fb[set][r] = OpB::fragment(stage + OpA::kBytes, rn + r * 16, ks);
       else fa[set][r - S::FN] = OpA::fragment(stage, rm + (r - S::FN) * 16, ks);
@@ -485,7 +513,7 @@ struct TileProduct {
       loads_done_and_meet();
       const bool more = t + 2 < steps;
       const uint32_t da = lds0 + buf * kStage, db = da + OpA::kBytes;
-      const int n = more ? existing() : kStepK;
+      const int n = more ? existing() : kStep;
 #pragma unroll
       for (int i = 0; i < S::FM; ++i) {
         if (more) {

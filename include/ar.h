@@ -679,6 +679,7 @@ typedef struct {
   uint64_t elem_bytes;    /* of x, y, dx, dy and the weights */
   uint64_t grad_bytes;    /* of the weight gradients         */
   uint64_t arena_count;   /* elements an arena holds at least */
+  uint64_t workspace_bytes; /* device memory the plan owns once prepared */
 } ar_experts_stats_t;
 
 /*
@@ -690,17 +691,21 @@ typedef struct {
  */
 ar_experts_t *ar_experts_create(int nexperts, size_t in_features, size_t out_features, ar_dtype_t dtype,
                                 ar_dtype_t grad_dtype, const size_t *weight_offsets);
-/* Uploads the offset table to the current device (the first product does it
- * otherwise; call it before capturing one into a HIP graph).  The plan is
- * bound to that device. */
+/* Uploads the offset table to the current device and allocates the plan's
+ * workspace, at most 16 MiB (the first product does it otherwise; call it
+ * before capturing one into a HIP graph).  The plan is bound to that device.
+ * AR_ERR_OOM / AR_ERR_HIP on failure. */
 ar_status_t ar_experts_prepare(ar_experts_t *plan);
 ar_experts_stats_t ar_experts_stats(const ar_experts_t *plan);
 /*
  * The products.  Row strides are in elements (at least the features, at most
  * 2^22); pointers are aligned to their elements (the fast path needs rows
  * and matrices that start on 16 bytes, and feature counts that are multiples
- * of 8).  The output overlaps no input.  Calls of one plan have no workspace:
- * they may be in flight together on several streams, captured or not.
+ * of 16 bytes).  The output overlaps no input.  forward and input_grad use no
+ * workspace: calls of one plan may be in flight together on several streams,
+ * captured or not.  weight_grad may (few experts of few features, many rows:
+ * the rows are cut into parts whose sums are added in a fixed order): no two
+ * of one plan may overlap in time, replays of captured ones included.
  * ntokens = 0: forward and input_grad do nothing.  AR_ERR_INVALID_ARG for bad
  * arguments or another device than the plan's; AR_ERR_UNSUPPORTED for a
  * product beyond one launch grid; AR_ERR_HIP if the launch fails.

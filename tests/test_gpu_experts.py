@@ -122,6 +122,16 @@ def test_products(inf, outf, counts, dtype, grad):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype,grad", [("bf16", "fp32"), ("bf16", "bf16"), ("fp32", "fp32")])
+@pytest.mark.parametrize("inf,outf,counts", [(128, 64, [4000]), (72, 136, [2100, 0, 700]), (71, 135, [3001, 5]),
+                                             (512, 768, [8001]), (64, 64, [0, 0, 0, 4099, 1])])
+def test_long_weight_gradients(inf, outf, counts, dtype, grad):
+    """Few tiles and many rows: the rows are cut into parts and joined; experts of none, one and many rows."""
+    print("case", inf, outf, counts, dtype, grad, flush=True)
+    Case(inf, outf, counts, dtype, grad, extra=3).check_all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("pad,shift", [((8, 16), 0), ((1, 3), 0), ((0, 0), 1), ((8, 8), 3), ((5, 0), 8), ((4, 4), 4)])
 def test_strides_and_alignment(pad, shift, dtype):
@@ -197,7 +207,7 @@ def test_infinities_stay_in_their_rows(inf, dtype, rows):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("counts", [[1, 2, 0, 1], [100, 300, 0, 77]])
+@pytest.mark.parametrize("counts", [[1, 2, 0, 1], [100, 300, 0, 77], [1000, 3000, 0, 700]])
 def test_graph_replays(counts):
     """A captured forward, input gradient and weight gradient, replayed with new rows and new ends between
     eager calls."""

@@ -54,7 +54,7 @@ def test_experts_stats():
     s = B.ar_experts_stats(p)
     B.ar_experts_destroy(p)
     assert s == {"nexperts": 3, "device": -1, "in_features": 5, "out_features": 7, "elem_bytes": 2, "grad_bytes": 4,
-                 "arena_count": 135}
+                 "arena_count": 135, "workspace_bytes": 3 * 8 + 3 * 16 * 64 * 128 * 4}
 
 
 def test_experts_null_plan():
@@ -204,6 +204,6 @@ def test_muon_offsets_from_a_bucket_plan():
 
 def test_c_struct_sizes():
     """The ctypes mirrors have the C layout."""
-    assert ctypes.sizeof(B.ar_experts_stats_t) == 48
+    assert ctypes.sizeof(B.ar_experts_stats_t) == 56
     assert ctypes.sizeof(B.ar_muon_stats_t) == 48
     assert ctypes.sizeof(B.ar_muon_params_t) == 40
