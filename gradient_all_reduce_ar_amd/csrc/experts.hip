@@ -185,9 +185,9 @@ __global__ __launch_bounds__(P::Sh::kThreads) void experts_rows(ExpertArgs a) {
   const int64_t n0 = static_cast<int64_t>(t.tile_n) * S::BN, ldx = GRAD ? a.dys : a.xs;
   const int validn = static_cast<int>(min(static_cast<int64_t>(S::BN), n - n0));
   const T *x = static_cast<const T *>(GRAD ? a.dy : a.x) + t.row * ldx;
-  const T *w = static_cast<const T *>(a.w) + a.offsets[t.e] + (GRAD ? n0 : n0 * a.in);
+  const T *w = static_cast<const T *>(a.w) + table_entry(a.offsets + t.e) + (GRAD ? n0 : n0 * a.in);
   P p;
-  p.run(lds, x, w, ldx, a.in, t.rows, validn, k);
+  p.run(lds, x, w, ldx, a.in, t.rows, validn, static_cast<int>(k));
   using Out = TileOut<S, P::kLds>;
   Out::all(lds, p.acc, [&](int pass, int tid) {
     Out::rows(lds, pass, tid, [&](int m, int c, fx4 v) {
@@ -254,7 +254,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void experts_few(ExpertArgs a) {
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, r = lane & 15;
   const int64_t n0 = static_cast<int64_t>(t.tile_n) * kFewCols, own = (lane >> 4) * 2 * F::kVec;
   // rows and columns that do not exist repeat the last one; not stored
-  const T *w = static_cast<const T *>(a.w) + a.offsets[t.e] + min(n0 + r, a.outf - 1) * a.in + own;
+  const T *w = static_cast<const T *>(a.w) + table_entry(a.offsets + t.e) + min(n0 + r, a.outf - 1) * a.in + own;
   const T *x0 = static_cast<const T *>(a.x) + (t.row + min(r, t.rows - 1)) * a.xs + own;
   const T *x1 = static_cast<const T *>(a.x) + (t.row + min(r + 16, t.rows - 1)) * a.xs + own;
   const bool two = t.rows > 16;
@@ -332,7 +332,7 @@ __device__ __forceinline__ WeightTile weight_tile(const ExpertArgs &a, int64_t i
 // One pass of the tile's way into the arena.
 template <class Out, bool GBF>
 __device__ __forceinline__ void store_weights(const ExpertArgs &a, const WeightTile &t, char *lds, int pass, int tid) {
-  const int64_t out = a.offsets[t.e] + t.m0 * a.in + t.n0;
+  const int64_t out = table_entry(a.offsets + t.e) + t.m0 * a.in + t.n0;
   Out::rows(lds, pass, tid, [&](int m, int c, fx4 v) {
     if (m >= t.validm || c >= t.validn) return;
     const int64_t at = out + m * a.in + c;

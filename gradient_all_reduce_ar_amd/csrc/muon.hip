@@ -80,8 +80,8 @@ __device__ __forceinline__ float update_of(const MuonArgs &a, float g, float m1)
 // Momentum, and the sum of squares of U over one part of a matrix (fp64).
 template <bool GBF, bool STEP>
 __global__ __launch_bounds__(kThreads) void muon_norm(MuonArgs a) {
-  const MuonTile t = a.parts[blockIdx.x];
-  const MuonMat &mat = a.mats[t.mat];
+  const MuonTile t = table_entry(a.parts + blockIdx.x);
+  const MuonMat mat = table_entry(a.mats + t.mat);
   const int64_t size = static_cast<int64_t>(mat.rows) * mat.cols;
   const int64_t lo = static_cast<int64_t>(t.m) * mat.chunk, hi = min(lo + mat.chunk, size);
   double sum = 0;
@@ -143,8 +143,8 @@ __device__ __forceinline__ void store_pair4(uint16_t *hi, uint16_t *lo, fx4 v, b
 // the matrix is tall, zeros in the padding.
 template <bool GBF, bool STEP>
 __global__ __launch_bounds__(kThreads) void muon_scale(MuonArgs a, int ex, bool pair) {
-  const MuonTile t = a.blocks[blockIdx.x];
-  const MuonMat &mat = a.mats[t.mat];
+  const MuonTile t = table_entry(a.blocks + blockIdx.x);
+  const MuonMat mat = table_entry(a.mats + t.mat);
   double sum = 0;
   for (int i = threadIdx.x; i < mat.parts; i += kThreads) sum += a.partials[mat.part0 + i];
 #pragma unroll
@@ -275,7 +275,7 @@ struct FinishMul {
   int mp, np, ld;
   bool pair;
   __device__ __forceinline__ FinishMul(const MuonArgs &a, const MuonStep &k, const MuonMat &mat, bool)
-      : out(a.ws + mat.x[k.from ^ 1]), plane(static_cast<int64_t>(mat.mp) * mat.np),
+      : out(a.ws + (k.from ? mat.x[0] : mat.x[1])), plane(static_cast<int64_t>(mat.mp) * mat.np),
         f(pow2(k.ex_next - k.eb - k.ex)), mp(mat.mp), np(mat.np), ld(mat.np), pair(k.pair_next) {}
   __device__ __forceinline__ bool along_rows() const { return true; }
   __device__ __forceinline__ bool along_columns() const { return false; }
@@ -362,12 +362,13 @@ __global__ __launch_bounds__(S::kThreads) void muon_product(MuonArgs a, MuonStep
   static_assert(S::BM == S::BN, "square tiles");
   extern __shared__ __align__(16) char lds[];
   const MuonWork &w = work_of<PR>(a);
-  for (int it = w.first[blockIdx.x]; it < w.first[blockIdx.x + 1]; ++it) {
-    const MuonItem t = w.items[it];
-    const MuonMat &mat = a.mats[t.mat];
+  const int last = table_entry(w.first + blockIdx.x + 1);
+  for (int it = table_entry(w.first + blockIdx.x); it < last; ++it) {
+    const MuonItem t = table_entry(w.items + it);
+    const MuonMat mat = table_entry(a.mats + t.mat);
     const int mp = mat.mp, cols = kSym ? mp : mat.np, m0 = t.m * S::BM, n0 = t.n * S::BN;
     const int64_t lda = PR == kGram ? mat.np : mat.mp, ldb = PR == kPoly ? mat.mp : mat.np;
-    const uint16_t *x = a.ws + mat.x[k.from] + t.k0 * (kSym ? 1 : ldb), *sq = a.ws + (PR == kPoly ? mat.a : mat.b) + t.k0;
+    const uint16_t *x = a.ws + (k.from ? mat.x[1] : mat.x[0]) + t.k0 * (kSym ? 1 : ldb), *sq = a.ws + (PR == kPoly ? mat.a : mat.b) + t.k0;
     const uint16_t *pa = (PR == kGram ? x : sq) + m0 * lda;
     const uint16_t *pb = PR == kPoly ? sq + n0 * ldb : PR == kGram ? x + n0 * ldb : x + n0;
     // X X^T for a single A takes X's hi alone: lo lies below A's rounding
@@ -397,9 +398,9 @@ __global__ __launch_bounds__(S::kThreads) void muon_join(MuonArgs a, MuonStep k)
   using Out = TileOut<S, kJoinLds>;
   extern __shared__ __align__(16) char lds[];
   const MuonWork &w = work_of<PR>(a);
-  const MuonJoin t = w.joins[blockIdx.x / Out::kPasses];
+  const MuonJoin t = table_entry(w.joins + blockIdx.x / Out::kPasses);
   const int pass = blockIdx.x % Out::kPasses;
-  const MuonMat &mat = a.mats[t.mat];
+  const MuonMat mat = table_entry(a.mats + t.mat);
   const fx4 *slot = reinterpret_cast<const fx4 *>(a.slots + static_cast<int64_t>(t.slot) * kMuonSlot) +
                     static_cast<int64_t>(pass) * Out::IP * S::FN * S::kThreads + threadIdx.x;
   fx4 v[Out::IP][S::FN];
@@ -527,7 +528,7 @@ __global__ __launch_bounds__(Small<TINY>::kThreads) void muon_small_kernel(MuonA
   using Sm = Small<TINY>;
   extern __shared__ __align__(16) char lds[];
   __shared__ double sums[Sm::kWaves];
-  const MuonMat &mat = a.mats[blockIdx.x];
+  const MuonMat mat = table_entry(a.mats + blockIdx.x);
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int mp = static_cast<int>(pad32(mat.m)), np = static_cast<int>(pad32(mat.n));
   const int px = np * 2 + 32, pq = mp * 2 + 32, lx = mp * px, lq = mp * pq;

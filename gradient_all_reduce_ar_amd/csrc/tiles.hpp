@@ -64,20 +64,48 @@ __device__ __forceinline__ uint32_t lds_offset(const void *p) {
       reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const char *)static_cast<const char *>(p)));
 }
 
-// 64 lanes x 16 bytes from base + off (per lane) to LDS at lds_base + 16 lane;
-// a lane whose off is at or over 2^31 - 1 writes zeros (the buffer's range
-// check).  Asynchronous: loads_done() waits.  In asm because the compiler
-// would wait for every such load before each transposing LDS read; the
-// instruction has no output register.  s_nop 4: the wait states that a
-// scalar register written by the vector unit needs before a buffer load.
+// A value that is the same in all lanes, in scalar registers.
+__device__ __forceinline__ int32_t uniform(int32_t v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+  const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<int32_t>(v));
+  const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<int32_t>(v >> 32));
+  return static_cast<int64_t>(static_cast<uint64_t>(hi) << 32 | lo);
+}
+
+// An entry of a plan's table, which nothing writes while a kernel runs, at a
+// uniform address: read with scalar loads, so that what is computed from it
+// (a contraction's addresses and loop counts) stays in the scalar unit.  The
+// compiler would read it into vector registers, since the kernel stores.
+template <class T>
+__device__ __forceinline__ T table_entry(const T *p) {
+  static_assert(sizeof(T) % 4 == 0, "whole words");
+  const auto *w = (const __attribute__((address_space(4))) uint32_t *)reinterpret_cast<uintptr_t>(p);
+  uint32_t h[sizeof(T) / 4];
+#pragma unroll
+  for (size_t i = 0; i < sizeof(T) / 4; ++i) h[i] = w[i];
+  T v;
+  __builtin_memcpy(&v, h, sizeof(T));
+  return v;
+}
+
+// A buffer resource at a uniform address: 48-bit base, 2^31 - 1 bytes, 32-bit
+// data format.  s_nop 4: the wait states between a scalar register that the
+// vector unit wrote and a buffer load, which asm hides from the compiler.
+__device__ __forceinline__ ux4 resource(const void *base) {
+  const uint64_t b = static_cast<uint64_t>(uniform(static_cast<int64_t>(reinterpret_cast<uintptr_t>(base))));
+  ux4 r = {static_cast<uint32_t>(b), static_cast<uint32_t>(b >> 32) & 0xffffu, 0x7fffffffu, 0x00020000u};
+  asm volatile("s_nop 4" : "+s"(r));
+  return r;
+}
+
+// 64 lanes x 16 bytes from the resource's base + off (per lane) to LDS at
+// lds_base + 16 lane; a lane whose off is at or over 2^31 - 1 writes zeros
+// (the buffer's range check).  Asynchronous: loads_done_and_meet() waits.  In
+// asm because the compiler would wait for every such load before each
+// transposing LDS read; the instruction has no output register.
 constexpr uint32_t kOutOfRange = 0x80000000u;
-__device__ __forceinline__ void load_to_lds(const void *base, uint32_t off, uint32_t lds_base) {
-  const uint64_t b = reinterpret_cast<uint64_t>(base);
-  // a buffer resource in scalar registers: 48-bit base, 2^31 - 1 bytes, 32-bit data format
-  const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(b));
-  const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(b >> 32)) & 0xffffu;
-  const ux4 r = {lo, hi, 0x7fffffffu, 0x00020000u};
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds_base), "v"(off),
+__device__ __forceinline__ void load_to_lds(ux4 r, uint32_t off, uint32_t lds_base) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds_base), "v"(off),
                "s"(r)
                : "memory");
 }
@@ -128,7 +156,14 @@ struct Operand {
   int64_t ld;
   int valid;
   uint32_t off[ALIGNED ? kPer : 1];  // bytes from base, contraction step 0
+  ux4 res;                           // resource at base
+  uint32_t mine;                     // LDS bytes of a stage before this wave's
   ux4 reg[ALIGNED ? 1 : kPer];
+
+  __device__ __forceinline__ void point(const T *b) {
+    base = b;
+    if constexpr (ALIGNED) res = resource(base);
+  }
 
   // Chunk j of this thread: its row in LDS, and which 16 bytes of that row
   // in memory land there.
@@ -146,9 +181,10 @@ struct Operand {
   }
 
   __device__ __forceinline__ void init(const T *b, int64_t l, int v) {
-    base = b;
+    point(b);
     ld = l;
     valid = v;
+    mine = uniform(static_cast<int32_t>(threadIdx.x >> 6)) * (1024 * kPer);
     if constexpr (ALIGNED) {
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
@@ -163,7 +199,7 @@ struct Operand {
     }
   }
 
-  __device__ __forceinline__ void advance() { base += MJ == kMajorK ? kStep : kStep * ld; }
+  __device__ __forceinline__ void advance() { point(base + (MJ == kMajorK ? kStep : kStep * ld)); }
 
   // For the last stage, of whose contraction elements the first `left` exist:
   // the loads of the others give zeros.
@@ -182,7 +218,7 @@ struct Operand {
   // aligned form has called before if that is less than a stage.
   __device__ __forceinline__ void load_one(int j, int left, uint32_t lds) {
     if constexpr (ALIGNED) {
-      load_to_lds(base, off[j], lds + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * (1024 * kPer) + j * 1024);
+      load_to_lds(res, off[j], lds + mine + j * 1024);
     } else {
       int row, col;
       where(j, row, col);
@@ -376,11 +412,12 @@ struct TileProduct {
   // what is loaded next: stage `at` of `per` of pair `pair`
   const T *a0, *b0;
   int64_t lo_a, lo_b;  // elements from a hi plane to its lo plane
-  int64_t k, at, per;
+  // (32 bits: ordered 64-bit comparisons would go to the vector unit)
+  int k, at, per;
   int pair, pairs;
 
   __device__ __forceinline__ int left() const {
-    return static_cast<int>(min(k - at * kStep, static_cast<int64_t>(kStep)));
+    return min(k - at * kStep, kStep);
   }
   __device__ __forceinline__ void next() {
     if (++at < per) {
@@ -388,8 +425,8 @@ struct TileProduct {
       ob.advance();
     } else if (++pair < pairs) {
       at = 0;
-      oa.base = a0 + (pair + 2 == pairs ? lo_a : 0);
-      ob.base = b0;
+      oa.point(a0 + (pair + 2 == pairs ? lo_a : 0));
+      ob.point(b0);
     }
   }
   // Only a list of one pair may end inside a stage: the masks of cut() stay.
@@ -413,7 +450,7 @@ struct TileProduct {
   }
 
   __device__ __forceinline__ void run(char *lds, const T *a, const T *b, int64_t lda, int64_t ldb,
-                                      int validm, int validn, int64_t length, int npairs = 1, int64_t plane_a = 0,
+                                      int validm, int validn, int length, int npairs = 1, int64_t plane_a = 0,
                                       int64_t plane_b = 0) {
 #pragma unroll
     for (int i = 0; i < S::FM; ++i)
@@ -428,14 +465,14 @@ struct TileProduct {
     k = length;
     pair = 0;
     at = 0;
-    per = (k + kStep - 1) / kStep;
+    per = k / kStep + (k % kStep != 0);
     oa.init(a, lda, validm);
     ob.init(b + (pairs > 1 ? lo_b : 0), ldb, validn);
     if constexpr (kTwoSets) two_sets(lds, per * pairs);
     else one_set(lds, per * pairs);
   }
 
-  __device__ __forceinline__ void one_set(char *lds, int64_t steps) {
+  __device__ __forceinline__ void one_set(char *lds, int steps) {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int rm = wave / S::WN * (S::BM / S::WM), rn = wave % S::WN * (S::BN / S::WN);
     const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_offset(lds));
@@ -444,7 +481,7 @@ struct TileProduct {
     for (int i = 0; i < kAhead && i < steps; ++i) load(lds0 + i * kStage);
     land(lds);
     int buf = 0, to = kAhead;  // stage read, stage loaded
-    for (int64_t t = 0; t < steps; ++t) {
+    for (int t = 0; t < steps; ++t) {
       if constexpr (!ALIGNED) {
         __syncthreads();
       } else if (kAhead > 1 && t + kAhead <= steps) {  // all but the newest kAhead - 1 stages have landed
@@ -480,7 +517,7 @@ struct TileProduct {
   // with the stage, and stage t + 1 has landed (its loads began a step ago):
   // matrix instructions on set 1 while set 0 reads stage t + 1 and stage
   // t + 2's loads start into the half that stage t leaves.
-  __device__ __forceinline__ void two_sets(char *lds, int64_t steps) {
+  __device__ __forceinline__ void two_sets(char *lds, int steps) {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int rm = wave / S::WN * (S::BM / S::WM), rn = wave % S::WN * (S::BN / S::WN);
     const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_offset(lds));
@@ -499,8 +536,8 @@ struct TileProduct {
     }
 #pragma unroll
     for (int r = 0; r < kReads; ++r) read(0, lds, 0, r);
-    for (int64_t t = 0; t < steps; ++t) {
-      const int buf = static_cast<int>(t & 1);
+    for (int t = 0; t < steps; ++t) {
+      const int buf = t & 1;
       const char *stage = lds + buf * kStage, *other = lds + (buf ^ 1) * kStage;
 #pragma unroll
       for (int i = 0; i < S::FM; ++i) {
