@@ -516,8 +516,11 @@ struct TileProduct {
   // set 0 while set 1 reads the stage's other half; then every wave is done
   // with the stage, and stage t + 1 has landed (its loads began a step ago):
   // matrix instructions on set 1 while set 0 reads stage t + 1 and stage
-  // t + 2's loads start into the half that stage t leaves.
+  // t + 2's loads start into the half that stage t leaves.  The steps without
+  // such a load, and the one before them, whose stage may be cut, are apart, so
+  // that the others are free of branches.
   __device__ __forceinline__ void two_sets(char *lds, int steps) {
+    enum { kWhole, kLast, kNone };
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int rm = wave / S::WN * (S::BM / S::WM), rn = wave % S::WN * (S::BN / S::WN);
     const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_offset(lds));
@@ -536,7 +539,9 @@ struct TileProduct {
     }
 #pragma unroll
     for (int r = 0; r < kReads; ++r) read(0, lds, 0, r);
-    for (int t = 0; t < steps; ++t) {
+    // kind: kWhole / kLast where a stage t + 2 exists and is whole / may be cut
+    auto step = [&](int t, auto kind) {
+      constexpr bool more = decltype(kind)::value != kNone;
       const int buf = t & 1;
       const char *stage = lds + buf * kStage, *other = lds + (buf ^ 1) * kStage;
 #pragma unroll
@@ -548,12 +553,11 @@ struct TileProduct {
         __builtin_amdgcn_sched_barrier(0);  // keeps the reads spread among the products
       }
       loads_done_and_meet();
-      const bool more = t + 2 < steps;
       const uint32_t da = lds0 + buf * kStage, db = da + OpA::kBytes;
-      const int n = more ? existing() : kStep;
+      const int n = decltype(kind)::value == kLast ? existing() : kStep;
 #pragma unroll
       for (int i = 0; i < S::FM; ++i) {
-        if (more) {
+        if constexpr (more) {
 #pragma unroll
           for (int r = i * kLoads / S::FM; r < (i + 1) * kLoads / S::FM; ++r) {
             if (r < OpA::kPer) oa.load_one(r, n, da);
@@ -567,8 +571,12 @@ struct TileProduct {
         for (int j = 0; j < S::FN; ++j) acc[i][j] = mfma16<E>(fb[1][j], fa[1][i], acc[i][j]);
         __builtin_amdgcn_sched_barrier(0);
       }
-      if (more) next();
-    }
+      if constexpr (more) next();
+    };
+    int t = 0;
+    for (; t + 3 < steps; ++t) step(t, std::integral_constant<int, kWhole>{});
+    if (t + 2 < steps) step(t++, std::integral_constant<int, kLast>{});
+    for (; t < steps; ++t) step(t, std::integral_constant<int, kNone>{});
     loads_done_and_meet();
   }
 };
