@@ -404,8 +404,9 @@ struct TileProduct {
   static constexpr int kStep = OpA::kStep;
   static constexpr int kStage = OpA::kBytes + OpB::kBytes;
   static constexpr int kStages = ALIGNED ? S::kStages : 2;
-  static constexpr int kLds = kStages * kStage;
   static constexpr bool kTwoSets = ALIGNED && S::BM * S::BN >= 256 * 256;
+  static constexpr int kLds = kTwoSets ? kStage * 5 / 2 : kStages * kStage;
+  static_assert(!kTwoSets || OpA::kBytes == OpB::kBytes, "a ring of operand stages");
   fx4 acc[S::FM][S::FN];
   OpA oa;
   OpB ob;
@@ -511,14 +512,18 @@ struct TileProduct {
     __syncthreads();
   }
 
-  // Stage t lies in half t & 1 of the LDS.  The first half of its contraction
-  // elements is in register set 0 when step t begins.  Step t: matrix instructions on
-  // set 0 while set 1 reads the stage's other half; then every wave is done
-  // with the stage, and stage t + 1 has landed (its loads began a step ago):
-  // matrix instructions on set 1 while set 0 reads stage t + 1 and stage
-  // t + 2's loads start into the half that stage t leaves.  The steps without
-  // such a load, and the one before them, whose stage may be cut, are apart, so
-  // that the others are free of branches.
+  // The LDS is a ring of five parts, each one operand's stage: A of stage t in
+  // part 2t % 5, B in the next.  The first half of stage t's contraction
+  // elements is in register set 0 when step t begins.  Step t: matrix
+  // instructions on set 0 while set 1 reads the stage's other half and A of
+  // stage t + 2 starts on its way to the part that B of stage t - 1 left; then
+  // every wave is done with stage t, and stage t + 1 has landed (its loads
+  // began a step ago): matrix instructions on set 1 while set 0 reads stage
+  // t + 1 and B of stage t + 2 starts into the part of A of stage t.  So one
+  // load goes out for every two rows of fragments: all in the second half of
+  // the step (two stages of LDS do for that), they take 2% longer, and in its
+  // first quarter 8%.  The steps without such loads, and the one before them,
+  // whose stage may be cut, are apart, so that the others are free of branches.
   __device__ __forceinline__ void two_sets(char *lds, int steps) {
     enum { kWhole, kLast, kNone };
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -526,57 +531,63 @@ struct TileProduct {
     const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_offset(lds));
     constexpr int kReads = S::FM + S::FN, kLoads = OpA::kPer + OpB::kPer;
     Frag<E> fa[2][S::FM], fb[2][S::FN];
-    auto read = [&](int set, const char *stage, int ks, int r) {
-      if (r < S::FN) fb[set][r] = OpB::fragment(stage + OpA::kBytes, rn + r * 16, ks);
-      else fa[set][r - S::FN] = OpA::fragment(stage, rm + (r - S::FN) * 16, ks);
+    auto read = [&](int set, const char *sa, const char *sb, int ks, int r) {
+      if (r < S::FN) fb[set][r] = OpB::fragment(sb, rn + r * 16, ks);
+      else fa[set][r - S::FN] = OpA::fragment(sa, rm + (r - S::FN) * 16, ks);
     };
     load(lds0);
     if (steps > 1) {
-      load(lds0 + kStage);
+      load(lds0 + kStage);  // (parts 2 and 3)
       asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(kLoads) : "memory");
     } else {
       loads_done_and_meet();
     }
 #pragma unroll
-    for (int r = 0; r < kReads; ++r) read(0, lds, 0, r);
+    for (int r = 0; r < kReads; ++r) read(0, lds, lds + OpA::kBytes, 0, r);
     // kind: kWhole / kLast where a stage t + 2 exists and is whole / may be cut
-    auto step = [&](int t, auto kind) {
+    constexpr int kPart = OpA::kBytes;
+    const auto part = [](int p) { return p >= 5 * kPart ? p - 5 * kPart : p; };
+    int at_a = 0;  // where A of stage t is
+    auto step = [&](auto kind) {
       constexpr bool more = decltype(kind)::value != kNone;
-      const int buf = t & 1;
-      const char *stage = lds + buf * kStage, *other = lds + (buf ^ 1) * kStage;
-#pragma unroll
-      for (int i = 0; i < S::FM; ++i) {
-#pragma unroll
-        for (int r = i * kReads / S::FM; r < (i + 1) * kReads / S::FM; ++r) read(1, stage, 1, r);
-#pragma unroll
-        for (int j = 0; j < S::FN; ++j) acc[i][j] = mfma16<E>(fb[0][j], fa[0][i], acc[i][j]);
-        __builtin_amdgcn_sched_barrier(0);  // keeps the reads spread among the products
-      }
-      loads_done_and_meet();
-      const uint32_t da = lds0 + buf * kStage, db = da + OpA::kBytes;
+      const char *sa = lds + at_a, *sb = lds + part(at_a + kPart);
+      const char *na = lds + part(at_a + 2 * kPart), *nb = lds + part(at_a + 3 * kPart);
+      const uint32_t da = lds0 + part(at_a + 4 * kPart), db = lds0 + at_a;
       const int n = decltype(kind)::value == kLast ? existing() : kStep;
 #pragma unroll
       for (int i = 0; i < S::FM; ++i) {
         if constexpr (more) {
 #pragma unroll
-          for (int r = i * kLoads / S::FM; r < (i + 1) * kLoads / S::FM; ++r) {
-            if (r < OpA::kPer) oa.load_one(r, n, da);
-            else ob.load_one(r - OpA::kPer, n, db);
-          }
+          for (int r = i * OpA::kPer / S::FM; r < (i + 1) * OpA::kPer / S::FM; ++r) oa.load_one(r, n, da);
+        }
+#pragma unroll
+        for (int r = i * kReads / S::FM; r < (i + 1) * kReads / S::FM; ++r) read(1, sa, sb, 1, r);
+#pragma unroll
+        for (int j = 0; j < S::FN; ++j) acc[i][j] = mfma16<E>(fb[0][j], fa[0][i], acc[i][j]);
+        __builtin_amdgcn_sched_barrier(0);  // keeps the reads spread among the products
+      }
+      // A of stage t + 2 may still be on its way
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(more ? OpA::kPer : 0) : "memory");
+#pragma unroll
+      for (int i = 0; i < S::FM; ++i) {
+        if constexpr (more) {
+#pragma unroll
+          for (int r = i * OpB::kPer / S::FM; r < (i + 1) * OpB::kPer / S::FM; ++r) ob.load_one(r, n, db);
         }
         // (behind the last stage: what another tile or stage left, not used)
 #pragma unroll
-        for (int r = i * kReads / S::FM; r < (i + 1) * kReads / S::FM; ++r) read(0, other, 0, r);
+        for (int r = i * kReads / S::FM; r < (i + 1) * kReads / S::FM; ++r) read(0, na, nb, 0, r);
 #pragma unroll
         for (int j = 0; j < S::FN; ++j) acc[i][j] = mfma16<E>(fb[1][j], fa[1][i], acc[i][j]);
         __builtin_amdgcn_sched_barrier(0);
       }
       if constexpr (more) next();
+      at_a = part(at_a + 2 * kPart);
     };
     int t = 0;
-    for (; t + 3 < steps; ++t) step(t, std::integral_constant<int, kWhole>{});
-    if (t + 2 < steps) step(t++, std::integral_constant<int, kLast>{});
-    for (; t < steps; ++t) step(t, std::integral_constant<int, kNone>{});
+    for (; t + 3 < steps; ++t) step(std::integral_constant<int, kWhole>{});
+    if (t + 2 < steps) step(std::integral_constant<int, kLast>{}), ++t;
+    for (; t < steps; ++t) step(std::integral_constant<int, kNone>{});
     loads_done_and_meet();
   }
 };
