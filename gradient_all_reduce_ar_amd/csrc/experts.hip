@@ -453,12 +453,13 @@ hipError_t launch_rows(const ExpertArgs &a, hipStream_t s) {
 
 template <class S, bool GRAD>
 hipError_t launch_rows(const ExpertArgs &a, hipStream_t s) {
-  if (a.aligned)
-    return a.bf16 ? launch_rows<kBF16, S, GRAD, true>(a, s) : launch_rows<kF32, S, GRAD, true>(a, s);
-  if constexpr (S::BM < 256)  // the largest tile is for aligned operands
+  if constexpr (S::BM >= 256) {  // aligned bf16 alone
+    return launch_rows<kBF16, S, GRAD, true>(a, s);
+  } else {
+    if (a.aligned)
+      return a.bf16 ? launch_rows<kBF16, S, GRAD, true>(a, s) : launch_rows<kF32, S, GRAD, true>(a, s);
     return a.bf16 ? launch_rows<kBF16, S, GRAD, false>(a, s) : launch_rows<kF32, S, GRAD, false>(a, s);
-  else
-    return hipErrorInvalidValue;
+  }
 }
 
 // Which tile: the least of modelled times.  A tile's time is that of its
@@ -466,20 +467,22 @@ hipError_t launch_rows(const ExpertArgs &a, hipStream_t s) {
 // workgroup on a CU goes faster than several (`alone`, launches of up to 256
 // tiles).  The model against measured times, bf16 (rows, experts, in x out:
 // Big / Square / Half / Small, microseconds):
-//   16384, 8, 4096 x 12288:  1570 / 1920 / 2370 / 4700   measured 1590 / 1890 / 2370 / 4690
-//   16384, 4, 2048 x 2048:    199 /  180 /  210 /  410             191 /  178 /  196 /  402
-//   8192, 32, 2048 x 2048:    133 /  130 /  131 /  210             138 /  129 /  140 /  213
-//   4096, 8, 1024 x 1024:      35 /   24 /   22 /   33              35 /   21 /   20 /   32
-//   64, 32, 4096 x 1536:      190 /   82 /   76 /   40                - /   82 /   82 /   73
-// fp32:
-//   8192, 4, 2048 x 2048:    1000 / 670 / 595 / 760   measured 984 / 647 / 589 / 718
-//   3001, 8, 1024 x 1536:     500 / 131 /  95 / 127            254 / 135 / 109 / 125
-//   500, 4, 1000 x 1000:      250 /  77 /  44 /  36            250 /  72 /  43 /  28
+//   16384, 8, 4096 x 12288:  1362 / 1823 / 2206 / 4184   measured 1403 / 1777 / 2227 / 4196
+//   16384, 4, 2048 x 2048:    175 /  176 /  209 /  395             159 /  162 /  176 /  324
+//   8192, 32, 2048 x 2048:    117 /  116 /  124 /  212             118 /  120 /  124 /  192
+//   4096, 8, 1024 x 1024:      33 /   22 /   20 /   35              32 /   21 /   20 /   30
+//   64, 32, 4096 x 1536:       95 /   72 /   67 /   32             106 /   93 /   91 /   77
+// fp32 (Big, the matrix instructions' rate being a sixteenth, only lost: 4690
+// in the first of these):
+//   16384, 8, 4096 x 4096:       - / 4468 / 4180 / 5720   measured 4187 / 4120 / 5129
+//   8192, 4, 2048 x 2048:        - /  661 /  598 /  759             632 /  574 /  678
+//   3001, 8, 1024 x 1536:        - /  131 /   95 /  126             130 /  102 /  112
+//   500, 4, 1000 x 1000:         - /   77 /   44 /   36              72 /   42 /   27
 struct TileCost {
   double slots, alone, full, rest;
 };
-constexpr TileCost kBF16Cost[4] = {{256, 1.45, 1.7, 12}, {512, 0.65, 1.2, 5}, {768, 0.55, 1.12, 4}, {768, 0.4, 0.57, 3.5}};
-constexpr TileCost kF32Cost[4] = {{256, 15, 15, 12}, {512, 4.5, 7.9, 5}, {768, 2.5, 5.7, 4}, {768, 0.9, 2.0, 3.5}};
+constexpr TileCost kBF16Cost[4] = {{256, 1.3, 1.45, 12}, {512, 0.65, 1.05, 5}, {768, 0.55, 0.98, 4}, {768, 0.4, 0.45, 3.5}};
+constexpr TileCost kF32Cost[4] = {{}, {512, 4.5, 7.9, 5}, {768, 2.5, 5.7, 4}, {768, 0.9, 2.0, 3.5}};
 
 template <class S, bool GRAD>
 double rows_time(const ExpertArgs &a, const TileCost &c) {
@@ -509,7 +512,7 @@ hipError_t rows(const ExpertArgs &a, hipStream_t s) {
     }
   }
   const TileCost *c = a.bf16 ? kBF16Cost : kF32Cost;
-  const double big = a.aligned ? rows_time<Big, GRAD>(a, c[0]) : 1e300;
+  const double big = a.aligned && a.bf16 ? rows_time<Big, GRAD>(a, c[0]) : 1e300;
   const double square = rows_time<Square, GRAD>(a, c[1]), half = rows_time<Half, GRAD>(a, c[2]);
   const double small = rows_time<Small, GRAD>(a, c[3]);
   if (big <= std::min({square, half, small})) return launch_rows<Big, GRAD>(a, s);
@@ -550,16 +553,17 @@ hipError_t launch_weights(const ExpertArgs &a, hipStream_t s) {
 
 template <class S>
 hipError_t launch_weights(const ExpertArgs &a, hipStream_t s) {
-  if (a.aligned)
-    return !a.bf16       ? launch_weights<kF32, S, false, true>(a, s)
-           : a.grad_bf16 ? launch_weights<kBF16, S, true, true>(a, s)
-                         : launch_weights<kBF16, S, false, true>(a, s);
-  if constexpr (S::BM < 256)
+  if constexpr (S::BM * S::BN > kExpertSlot) {  // aligned bf16 alone
+    return a.grad_bf16 ? launch_weights<kBF16, S, true, true>(a, s) : launch_weights<kBF16, S, false, true>(a, s);
+  } else {
+    if (a.aligned)
+      return !a.bf16       ? launch_weights<kF32, S, false, true>(a, s)
+             : a.grad_bf16 ? launch_weights<kBF16, S, true, true>(a, s)
+                           : launch_weights<kBF16, S, false, true>(a, s);
     return !a.bf16       ? launch_weights<kF32, S, false, false>(a, s)
            : a.grad_bf16 ? launch_weights<kBF16, S, true, false>(a, s)
                          : launch_weights<kBF16, S, false, false>(a, s);
-  else
-    return hipErrorInvalidValue;
+  }
 }
 
 }  // namespace

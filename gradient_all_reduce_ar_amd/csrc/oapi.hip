@@ -368,29 +368,35 @@ struct Tile {
 
 // Tile shapes: workgroups that run at once, and the microseconds of a tile's
 // contraction step where every CU has one workgroup at most (`alone`, a launch
-// of up to 256 tiles) and where the launch is full, and of the rest of a
-// tile's work.  Measured, e.g. alone: X X^T of 512 x 2048 with pairs 150, 68
-// and 42 us with the three shapes; full: of 12288 x 4096 831, 982, 1232.
+// of up to 256 tiles) and where the launch is full, of the rest of a tile's
+// work, and of that which a square product adds (`mirror`: its tiles leave
+// twice).  Measured with the three shapes, pairs: the product with X of
+// 512 x 2048 (alone) 37, 21 and 12 us, of 12288 x 4096 (full) 891, 1123 and
+// 2022; X X^T of 512 x 2048 65 and 33 with the smaller two, of eight matrices
+// of 1024 x 1024 and 1024 x 2048 84 (split) and 107 with the largest and the
+// smallest.
 struct ShapeCost {
   int32_t slots;
-  double alone, full, rest;
+  double alone, full, rest, mirror;
 };
-constexpr ShapeCost kCost[ar_dev::kMuonShapes] = {{256, 1.45, 1.7, 12.0}, {512, 0.65, 1.2, 5.0}, {512, 0.42, 0.8, 3.5}};
-// A split launch also writes and reads its partial tiles (256 KiB each, at
-// the rate of a large copy) and launches the join.
-constexpr double kJoinLaunch = 6.0, kJoinSlot = 2 * 262144 / 4.7e6;
+constexpr ShapeCost kCost[ar_dev::kMuonShapes] = {
+    {256, 1.15, 1.48, 12.0, 17.0}, {512, 0.6, 0.97, 5.0, 8.0}, {512, 0.31, 0.6, 3.5, 1.5}};
+// A split launch also writes and reads its partial tiles (256 KiB each; 5.5
+// TB/s, 402 pieces of a 4096 x 4096 and a 1024 x 4096 matrix 42 us with the
+// launch) and launches the join.
+constexpr double kJoinLaunch = 6.0, kJoinSlot = 2 * 262144 / 5.5e6;
 constexpr int32_t kMinPiece = 4;  // steps of a piece at least
 
 // The time until the last tile is done if each goes, in order, to the
 // workgroup with the least to do.  pairs: planes' products of a step.
-double list_time(const std::vector<Tile> &tiles, const ShapeCost &c, int pairs) {
+double list_time(const std::vector<Tile> &tiles, const ShapeCost &c, int pairs, double rest) {
   std::vector<double> heap(c.slots, 0.0);  // the least on top
   const auto more = [](double x, double y) { return x > y; };
   const double step = pairs * (tiles.size() <= 256 ? c.alone : c.full);
   double last = 0;
   for (const Tile &t : tiles) {
     std::pop_heap(heap.begin(), heap.end(), more);
-    heap.back() += t.steps * step + c.rest;
+    heap.back() += t.steps * step + rest;
     last = std::max(last, heap.back());
     std::push_heap(heap.begin(), heap.end(), more);
   }
@@ -470,7 +476,7 @@ void split_tiles(const std::vector<Tile> &tiles, int32_t groups, ar_muon_plan::W
 // Chooses the tile shape, whole or split, with the least modelled time, and
 // makes the launch's lists.
 template <class List>
-void plan_product(List list, int pairs, ar_muon_plan::Work &w) {
+void plan_product(List list, int pairs, bool sym, ar_muon_plan::Work &w) {
   w = ar_muon_plan::Work{};
   double best = 0;
   bool split = false;
@@ -478,7 +484,7 @@ void plan_product(List list, int pairs, ar_muon_plan::Work &w) {
   for (int i = 0; i < ar_dev::kMuonShapes; ++i) {
     std::vector<Tile> t = list(ar_dev::muon_tile(i));
     const ShapeCost &c = kCost[i];
-    const double whole = list_time(t, c, pairs);
+    const double rest = c.rest + (sym ? c.mirror : 0), whole = list_time(t, c, pairs, rest);
     double time = whole;
     bool cut = false;
     if (i == 0) {
@@ -572,10 +578,10 @@ void lay_out(ar_muon_plan *p) {
     return t;
   };
   longest([](const MuonMat &m) { return m.np; });
-  plan_product([&](int64_t bt) { return tiles(bt, true, true); }, pair_ab ? 3 : 1, p->gram);
+  plan_product([&](int64_t bt) { return tiles(bt, true, true); }, pair_ab ? 3 : 1, true, p->gram);
   longest([](const MuonMat &m) { return m.mp; });
-  plan_product([&](int64_t bt) { return tiles(bt, true, false); }, pair_ab ? 3 : 1, p->poly);
-  plan_product([&](int64_t bt) { return tiles(bt, false, false); }, pair_ab ? 3 : 2, p->mul);
+  plan_product([&](int64_t bt) { return tiles(bt, true, false); }, pair_ab ? 3 : 1, true, p->poly);
+  plan_product([&](int64_t bt) { return tiles(bt, false, false); }, pair_ab ? 3 : 2, false, p->mul);
   int64_t slots = 0;
   for (const ar_muon_plan::Work *w : {&p->gram, &p->poly, &p->mul})
     for (const ar_dev::MuonJoin &j : w->joins) slots = std::max<int64_t>(slots, j.slot + j.count);
