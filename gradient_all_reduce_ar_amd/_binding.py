@@ -10,6 +10,7 @@ with a ``cuda_stream`` attribute (torch streams).
 """
 import ctypes
 import os
+import sys
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 # AR_LIB names another build of the same sources (the sanitizer build of the
@@ -674,6 +675,16 @@ def ar_bucket_plan_destroy(bp):
 
 # ------------------------------------------- products grouped by expert
 
+def _bound(plan, stats, prepare):
+    """Device of a plan, which is prepared if it was not (not while the caller captures a graph)."""
+    if stats(plan).device < 0:
+        torch = sys.modules.get("torch")  # the tensors' own
+        if torch is not None and torch.cuda.is_current_stream_capturing():
+            raise ValueError("the plan has to be prepared before it is captured")
+        _check(prepare(plan))
+    return stats(plan).device
+
+
 class _ExpertsInfo:
     """What the checks of a call need of a plan, read once; `device` is the one the plan is bound to (None
     before its first call with tensors, which prepares it)."""
@@ -687,8 +698,7 @@ class _ExpertsInfo:
         self.device = None
 
     def bind(self):
-        _check(lib().ar_experts_prepare(self.plan))
-        self.device = lib().ar_experts_stats(self.plan).device
+        self.device = _bound(self.plan, lib().ar_experts_stats, lib().ar_experts_prepare)
 
 
 _experts_info = {}  # by handle, until the plan is destroyed
@@ -864,7 +874,6 @@ def ar_muon_plan_set_scales(plan, scales=None):
         if len(scales) != n:
             raise ValueError(f"{len(scales)} scales for {n} matrices")
         arr = (ctypes.c_double * max(n, 1))(*[float(v) for v in scales])
-    _muon_info.pop(plan, None)  # the plan is no longer bound to a device
     _check(lib().ar_muon_plan_set_scales(plan, arr))
 
 
@@ -887,8 +896,7 @@ class _MuonInfo:
         self.device = None
 
     def bind(self):
-        _check(lib().ar_muon_plan_prepare(self.plan))
-        self.device = lib().ar_muon_plan_stats(self.plan).device
+        self.device = _bound(self.plan, lib().ar_muon_plan_stats, lib().ar_muon_plan_prepare)
 
 
 _muon_info = {}

@@ -47,8 +47,12 @@ class CallMarks {
   std::vector<Mark> marks_;
 };
 
-// Allocates `bytes` on the current device and fills them from src (if not
-// NULL) on a non-blocking stream of its own, which it waits for.
+// Copies `bytes` to the current device's memory on a non-blocking stream of
+// its own, which it waits for.
+hipError_t upload(void *dst, const void *src, size_t bytes);
+// Allocates `bytes` on the current device and fills them from src, if not NULL.
 hipError_t device_table(void **dst, const void *src, size_t bytes);
+// AR_ERR_INVALID_ARG while the caller captures s: a plan cannot be prepared then.
+ar_status_t refuse_capture(hipStream_t s);
 
 }  // namespace ar_host

@@ -56,6 +56,29 @@ void CallMarks::release() {
   marks_.clear();
 }
 
+ar_status_t refuse_capture(hipStream_t s) {
+  hipStreamCaptureStatus cs = hipStreamCaptureStatusNone;
+  const hipError_t e = hipStreamIsCapturing(s, &cs);
+  if (e != hipSuccess) return hip_fail(e, "hipStreamIsCapturing");
+  return cs == hipStreamCaptureStatusNone ? AR_OK
+                                          : fail(AR_ERR_INVALID_ARG, "the plan has to be prepared before it is captured");
+}
+
+hipError_t upload(void *dst, const void *src, size_t bytes) {
+  // a non-blocking stream and an event: a synchronous copy would go through
+  // the default stream, which ends a capture that another thread has open
+  hipStream_t s = nullptr;
+  hipEvent_t done = nullptr;
+  hipError_t e = hipStreamCreateWithFlags(&s, hipStreamNonBlocking);
+  if (e == hipSuccess) e = hipEventCreateWithFlags(&done, hipEventDisableTiming);
+  if (e == hipSuccess) e = hipMemcpyAsync(dst, src, bytes, hipMemcpyHostToDevice, s);
+  if (e == hipSuccess) e = hipEventRecord(done, s);
+  if (e == hipSuccess) e = hipEventSynchronize(done);
+  if (done) (void)hipEventDestroy(done);
+  if (s) (void)hipStreamDestroy(s);
+  return e;
+}
+
 hipError_t device_table(void **dst, const void *src, size_t bytes) {
   hipError_t e = hipMalloc(dst, bytes);
   if (e != hipSuccess) {
@@ -64,17 +87,7 @@ hipError_t device_table(void **dst, const void *src, size_t bytes) {
     return e;
   }
   if (!src) return hipSuccess;
-  // a non-blocking stream and an event: a synchronous copy would go through
-  // the default stream, which ends a capture that another thread has open
-  hipStream_t s = nullptr;
-  hipEvent_t done = nullptr;
-  e = hipStreamCreateWithFlags(&s, hipStreamNonBlocking);
-  if (e == hipSuccess) e = hipEventCreateWithFlags(&done, hipEventDisableTiming);
-  if (e == hipSuccess) e = hipMemcpyAsync(*dst, src, bytes, hipMemcpyHostToDevice, s);
-  if (e == hipSuccess) e = hipEventRecord(done, s);
-  if (e == hipSuccess) e = hipEventSynchronize(done);
-  if (done) (void)hipEventDestroy(done);
-  if (s) (void)hipStreamDestroy(s);
+  e = upload(*dst, src, bytes);
   if (e != hipSuccess) {
     (void)hipFree(*dst);
     *dst = nullptr;
@@ -177,7 +190,8 @@ ar_status_t run(ar_experts *ex, Which which, const RowsArg &r1, const RowsArg &r
   if (out_is_rows ? overlap(r2.p, b2, r1.p, b1) || overlap(r2.p, b2, arena, ab) || overlap(r2.p, b2, ends, eb)
                   : overlap(arena, ab, r1.p, b1) || overlap(arena, ab, r2.p, b2) || overlap(arena, ab, ends, eb))
     return fail(AR_ERR_INVALID_ARG, "the output overlaps an input");
-  st = prepare(ex);
+  if (!ex->d_offsets) st = ar_host::refuse_capture(static_cast<hipStream_t>(stream));
+  if (st == AR_OK) st = prepare(ex);
   if (st != AR_OK) return st;
   if (t == 0 && which != kWeightGrad) return AR_OK;
   ar_dev::ExpertArgs a{};
@@ -688,7 +702,8 @@ ar_status_t run(ar_muon_plan *p, const MuonCall &c, void *stream) {
     a.keep = f[2];
     a.lr = f[3];
   }
-  ar_status_t st = prepare(p);
+  ar_status_t st = p->device >= 0 ? AR_OK : ar_host::refuse_capture(static_cast<hipStream_t>(stream));
+  if (st == AR_OK) st = prepare(p);
   if (st != AR_OK || p->mats.empty()) return st;
   const char *t = static_cast<const char *>(p->d_table);
   a.mats = reinterpret_cast<const MuonMat *>(t);
@@ -789,7 +804,7 @@ ar_experts_t *ar_experts_create(int nexperts, size_t in_features, size_t out_fea
 
 ar_status_t ar_experts_prepare(ar_experts_t *ex) {
   if (!ex) return fail(AR_ERR_INVALID_ARG, "expert plan is NULL");
-  return prepare(ex);
+  return guarded([&] { return prepare(ex); });
 }
 
 ar_experts_stats_t ar_experts_stats(const ar_experts_t *ex) {
@@ -908,7 +923,6 @@ ar_status_t ar_muon_plan_set_iterations(ar_muon_plan_t *p, int n, const double *
     int32_t ex0 = 0;
     if (!make_steps(n, abc, !p->w_bf16, steps, ex0))
       return fail(AR_ERR_INVALID_ARG, "the coefficients let singular values or a factor grow beyond bounds");
-    p->marks.wait();
     p->steps = std::move(steps);
     p->ex0 = ex0;
     return AR_OK;
@@ -921,16 +935,26 @@ ar_status_t ar_muon_plan_set_scales(ar_muon_plan_t *p, const double *scales) {
     for (int i = 0; i < p->nmatrices; ++i)
       if (!std::isfinite(static_cast<float>(scales[i])))
         return fail(AR_ERR_INVALID_ARG, "scale of matrix " + std::to_string(i) + " is not a finite fp32 number");
-  p->release();
+  const bool held = p->d_table != nullptr;
+  int dev = 0;
+  if (held) {
+    const hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess) return hip_fail(e, "hipGetDevice");
+    if (dev != p->device) return fail(AR_ERR_INVALID_ARG, "Muon plan was prepared on another device");
+  }
   if (!scales) default_scales(p);
   else
     for (size_t i = 0; i < p->mats.size(); ++i) p->mats[i].scale = static_cast<float>(scales[p->index[i]]);
-  return AR_OK;
+  if (!held) return AR_OK;
+  // in place: captured graphs hold the table's address
+  p->marks.wait();
+  const hipError_t e = ar_host::upload(p->d_table, p->mats.data(), p->mats.size() * sizeof(MuonMat));
+  return e == hipSuccess ? AR_OK : hip_fail(e, "Muon tables");
 }
 
 ar_status_t ar_muon_plan_prepare(ar_muon_plan_t *p) {
   if (!p) return fail(AR_ERR_INVALID_ARG, "Muon plan is NULL");
-  return prepare(p);
+  return guarded([&] { return prepare(p); });
 }
 
 ar_muon_stats_t ar_muon_plan_stats(const ar_muon_plan_t *p) {

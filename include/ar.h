@@ -692,8 +692,8 @@ typedef struct {
 ar_experts_t *ar_experts_create(int nexperts, size_t in_features, size_t out_features, ar_dtype_t dtype,
                                 ar_dtype_t grad_dtype, const size_t *weight_offsets);
 /* Uploads the offset table to the current device and allocates the plan's
- * workspace, at most 16 MiB (the first product does it otherwise; call it
- * before capturing one into a HIP graph).  The plan is bound to that device.
+ * workspace, at most 16 MiB (the first product does it otherwise; one that is
+ * captured into a HIP graph before is refused with AR_ERR_INVALID_ARG).  The plan is bound to that device.
  * AR_ERR_OOM / AR_ERR_HIP on failure. */
 ar_status_t ar_experts_prepare(ar_experts_t *plan);
 ar_experts_stats_t ar_experts_stats(const ar_experts_t *plan);
@@ -786,15 +786,16 @@ ar_muon_plan_t *ar_muon_plan_create(int nmatrices, const size_t *rows, const siz
                                     ar_dtype_t grad_dtype, ar_dtype_t weight_dtype);
 /* n (1 to 32) steps with coefficients abc[3 k .. 3 k + 2]; abc = NULL: the
  * default ones in every step.  AR_ERR_INVALID_ARG where singular values in
- * [0, 1] could grow past 2^10 or a factor past 2^14 on the way.  Waits for
- * the plan's calls in flight.  Host only. */
+ * [0, 1] could grow past 2^10 or a factor past 2^14 on the way.  Concerns the
+ * calls that follow (a captured graph keeps its steps).  Host only. */
 ar_status_t ar_muon_plan_set_iterations(ar_muon_plan_t *plan, int n, const double *abc);
-/* scale[i] of matrix i (NULL: the default ones).  Finite.  Drops the plan's
- * device tables after waiting for its calls in flight; the next call (or
- * prepare) uploads new ones. */
+/* scale[i] of matrix i (NULL: the default ones).  Finite.  Concerns the calls
+ * that follow and the later replays of captured ones; waits for the plan's
+ * calls in flight (captured ones are the caller's to finish). */
 ar_status_t ar_muon_plan_set_scales(ar_muon_plan_t *plan, const double *scales);
 /* Allocates the plan's workspace and tables on the current device (the first
- * call does it otherwise; call it before capturing one into a HIP graph). */
+ * call does it otherwise; one that is captured into a HIP graph before is
+ * refused with AR_ERR_INVALID_ARG). */
 ar_status_t ar_muon_plan_prepare(ar_muon_plan_t *plan);
 ar_muon_stats_t ar_muon_plan_stats(const ar_muon_plan_t *plan);
 /*

@@ -238,6 +238,32 @@ def test_graph_replays(counts):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("address", [False, True])
+def test_capture_needs_a_prepared_plan(address):
+    c = Case(64, 32, [5, 0, 20], "bf16")
+    y, other = c.rows(32, 0, 0), torch.zeros(4, device=DEV)
+    t = [c.x, c.w, y, c.ends]
+    if address:
+        t, more = [v.data_ptr() for v in t], dict(ntokens=c.x.shape[0], x_stride=c.x.stride(0), y_stride=y.stride(0))
+    else:
+        more = {}
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        with pytest.raises(B.ArError if address else ValueError):
+            B.ar_experts_forward(c.plan, *t, stream=s, **more)
+        other.add_(1)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert other.tolist() == [1] * 4 and B.ar_experts_stats(c.plan)["device"] == -1
+    B.ar_experts_forward(c.plan, *t, **more)
+    torch.cuda.synchronize()
+    c.check_rows(y, c.x, False)
+    B.ar_experts_destroy(c.plan)
+
+
+@pytest.mark.gpu
 def test_two_streams_at_once():
     """One plan's calls have no workspace: two streams may run them together."""
     c = Case(256, 512, [700, 100, 0, 900], "bf16")

@@ -297,6 +297,51 @@ def test_graph_replays(shapes):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("shapes", [[(64, 64), (32, 32)], [(160, 224), (96, 64)]])
+def test_captured_step_takes_new_scales(shapes):
+    offs, n = back_to_back(shapes)
+    plan = B.ar_muon_plan_create(shapes, "fp32", "fp32")
+    B.ar_muon_plan_prepare(plan)
+    g, m, w = torch.randn(n, device=DEV), torch.zeros(n, device=DEV), torch.zeros(n, device=DEV)
+    m2, w2 = m.clone(), w.clone()
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        B.ar_muon_step(plan, g, m, w, 0.1, stream=s)
+    for scales in (None, [0.5, 3.0], [2.0, 0.25], None):
+        B.ar_muon_plan_set_scales(plan, scales)
+        graph.replay()
+        torch.cuda.synchronize()
+        B.ar_muon_step(plan, g, m2, w2, 0.1)
+        torch.cuda.synchronize()
+        assert torch.equal(m, m2) and torch.equal(w, w2)
+    B.ar_muon_plan_destroy(plan)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("address", [False, True])
+def test_capture_needs_a_prepared_plan(address):
+    plan = B.ar_muon_plan_create([(96, 64)], "fp32", "fp32")
+    g, out, other = torch.randn(96 * 64, device=DEV), torch.zeros(96 * 64, device=DEV), torch.zeros(4, device=DEV)
+    args = (g.data_ptr(), out.data_ptr()) if address else (g, out)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        with pytest.raises(B.ArError if address else ValueError):
+            B.ar_orthogonalize(plan, *args, stream=s)
+        other.add_(1)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert other.tolist() == [1] * 4 and not out.any() and B.ar_muon_plan_stats(plan)["device"] == -1
+    B.ar_orthogonalize(plan, *args)
+    torch.cuda.synchronize()
+    assert out.any()
+    B.ar_muon_plan_destroy(plan)
+
+
+@pytest.mark.gpu
 def test_arena_past_32_bits():
     shapes, at = [(40, 64), (64, 40)], (1 << 32) + 5
     plan = B.ar_muon_plan_create(shapes, "bf16", "bf16", [1, at])
