@@ -419,8 +419,11 @@ double list_time(const std::vector<Tile> &tiles, const ShapeCost &c, int pairs, 
 
 // Splits a launch of the largest tiles over its workgroups: each gets whole
 // tiles while they fit into an equal share of the steps; the other tiles are
-// cut along the contraction to fill what is left of the shares.
-void split_tiles(const std::vector<Tile> &tiles, int32_t groups, ar_muon_plan::Work &w) {
+// cut along the contraction to fill what is left of the shares.  Returns the
+// time until the joined tiles are out.
+double split_tiles(const std::vector<Tile> &tiles, const ShapeCost &c, int pairs, double rest_time,
+                   ar_muon_plan::Work &w) {
+  const int32_t groups = c.slots;
   int64_t total = 0;
   for (const Tile &t : tiles) total += t.steps;
   const int64_t share = (total + groups - 1) / groups + kMinPiece;
@@ -477,6 +480,13 @@ void split_tiles(const std::vector<Tile> &tiles, int32_t groups, ar_muon_plan::W
     for (const Piece &x : pieces[i])
       of[x.group].push_back({t.mat, t.m, t.n, x.k0 * kStep, x.k1 * kStep, n > 1 ? slot++ : -1});
   }
+  double last = 0;
+  for (const auto &items : of) {
+    double time = 0;
+    for (const ar_dev::MuonItem &x : items)
+      time += (x.k1 - x.k0) / kStep * (pairs * c.full) + (x.slot >= 0 ? c.rest : rest_time);
+    last = std::max(last, time);
+  }
   // workgroup b runs on XCD b % 8: neighbouring shares go to one XCD, whose
   // L2 then holds the operands that their tiles share
   for (int32_t b = 0; b < groups; ++b) {
@@ -485,13 +495,13 @@ void split_tiles(const std::vector<Tile> &tiles, int32_t groups, ar_muon_plan::W
     w.items.insert(w.items.end(), of[s].begin(), of[s].end());
   }
   w.first.push_back(static_cast<int32_t>(w.items.size()));
+  return last + (slot > 0 ? kJoinLaunch + slot * kJoinSlot : 0);
 }
 
 // Chooses the tile shape, whole or split, with the least modelled time, and
 // makes the launch's lists.
 template <class List>
 void plan_product(List list, int pairs, bool sym, ar_muon_plan::Work &w) {
-  w = ar_muon_plan::Work{};
   double best = 0;
   bool split = false;
   std::vector<Tile> tiles;
@@ -499,26 +509,25 @@ void plan_product(List list, int pairs, bool sym, ar_muon_plan::Work &w) {
     std::vector<Tile> t = list(ar_dev::muon_tile(i));
     const ShapeCost &c = kCost[i];
     const double rest = c.rest + (sym ? c.mirror : 0), whole = list_time(t, c, pairs, rest);
-    double time = whole;
-    bool cut = false;
     if (i == 0) {
-      int64_t total = 0;
-      for (const Tile &x : t) total += x.steps;
-      // pieces: about one per workgroup and one per split tile
-      const double n = static_cast<double>(t.size()), pieces = c.slots + std::min<double>(n, c.slots);
-      const double even = (static_cast<double>(total) / c.slots + kMinPiece) * pairs * c.full +
-                          std::ceil(n / c.slots) * c.rest + kJoinLaunch + pieces * kJoinSlot;
-      cut = even < whole;
-      time = std::min(even, whole);
+      ar_muon_plan::Work cut;
+      const double even = split_tiles(t, c, pairs, rest, cut);
+      if (even < whole) {
+        best = even;
+        split = true;
+        w = std::move(cut);
+        continue;
+      }
     }
-    if (tiles.empty() || time < best) {
-      best = time;
-      split = cut;
+    if (i == 0 || whole < best) {
+      best = whole;
+      split = false;
+      w = ar_muon_plan::Work{};
       w.shape = i;
       tiles = std::move(t);
     }
   }
-  if (split) return split_tiles(tiles, kCost[w.shape].slots, w);
+  if (split) return;
   // one workgroup per tile, neighbours on one XCD
   const int32_t n = static_cast<int32_t>(tiles.size()), q = n / 8, r = n % 8;
   for (int32_t b = 0; b < n; ++b) {
