@@ -357,7 +357,7 @@ __global__ __launch_bounds__(P::Sh::kThreads) void experts_weights(ExpertArgs a)
   extern __shared__ __align__(16) char lds[];
   // Tiles in the order of the workgroups, which go round the XCDs: all of the
   // device then writes one neighbourhood of the arena at a time (16384 rows,
-  // 64 experts, 2048 x 1408: 272 us; 323 with a run of tiles per XCD).
+  // 64 experts, 2048 x 1408: 227 us; 231 with a run of tiles per XCD).
   WeightTile t = weight_tile<S>(a, blockIdx.x);
   if (a.accumulate && t.rows == 0) return;
   const bool split = gridDim.y > 1;
@@ -432,7 +432,7 @@ hipError_t launch(K kernel, int64_t grid, int parts, int threads, int lds, hipSt
   return hipGetLastError();
 }
 
-// Tiles.  Big runs one workgroup on a CU at 1.2 to 1.36 PFLOP/s, the others
+// Tiles.  Big runs one workgroup on a CU at 1.2 to 1.4 PFLOP/s, the others
 // several.
 using Big = Shape<256, 256, 2, 4>;
 using Square = Shape<128, 128, 2, 2>;
@@ -536,7 +536,7 @@ hipError_t launch_weights(const ExpertArgs &a, hipStream_t s) {
   const int64_t tiles = weight_tiles<S>(a);
   if constexpr (S::BM * S::BN == kExpertSlot) {
     // 8001 rows of one expert, 512 x 768 (48 tiles): 73 us whole, 26 us in
-    // parts; 16000, 2, 1024 x 1024 (256 tiles): 96 and 67
+    // parts; 16000, 2, 1024 x 1024 (256 tiles): 96 and 71
     const int64_t parts = std::min(most_parts(tiles), a.tokens / a.experts / kPartRows);
     if (parts > 1 && a.slots) {
       const LaunchEvents ev = t_launch_events;  // the call's mark goes on its last kernel
@@ -574,10 +574,10 @@ hipError_t experts_input_grad(const ExpertArgs &a, hipStream_t s) { return rows<
 // Big where its tiles give every CU one and an expert's rows fill a few
 // steps; Half where Square's would leave CUs idle, and for operands that are
 // not aligned.  Microseconds Big / Square / Half (rows, experts, in x out):
-//   16384, 64, 2048 x 1408:         264 / 272 / 300
-//   16384, 8, 4096 x 2048:          295 / 346 /   -
-//   4096, 32, 2048 x 1024 (128 rows each, bf16 gradients): 68 / 65 / -
-//   16384, 2, 512 x 512 (32 square tiles):  245 / 120 / 100
+//   16384, 64, 2048 x 1408:         228 / 226 / 232
+//   16384, 8, 4096 x 2048:          285 / 338 / 616
+//   4096, 32, 2048 x 1024 (128 rows each, bf16 gradients): 68 / 64 / 66
+//   16384, 2, 512 x 512 (32 square tiles):  212 / 118 / 36 (in parts)
 //   8192, 8, 2047 x 2047:             - / 546 / 485
 //   fp32, 8192, 4, 2048 x 2048:       - / 582 / 548
 hipError_t experts_weight_grad(const ExpertArgs &a, hipStream_t s) {

@@ -296,8 +296,8 @@ struct Shape {
 
 // The way out of a tile.  A lane's four sums lie in one row, 16 rows to an
 // instruction: stored from there, memory would see 32- or 64-byte pieces (a
-// weight gradient of 64 experts, 738 MB of fp32: 346 us; with whole lines and
-// non-temporal stores 196).  So the sums pass through the LDS, which the
+// weight gradient of 64 experts, 738 MB of fp32: 346 us; with whole lines 270,
+// with non-temporal stores of them 227).  So the sums pass through the LDS, which the
 // contraction no longer needs, IP rows of fragments of each wave at a time,
 // and leave it along rows or along columns, four sums to a lane.
 // Banks: 16-byte chunk c of row r is kept at c ^ ((r >> 2 ^ r << 2) & 15),
@@ -390,11 +390,14 @@ struct TileOut {
 // loads are issued between them, so that a stage costs one meeting and no
 // wait for the LDS.  Smaller tiles leave room for several workgroups on a CU,
 // which cover each other's waits, and read each fragment right before its
-// use.  bf16, 8192^3, both operands kMajorK: 1.36 PFLOP/s with the first loop
-// and this tile, 1.19 with the second; 128 x 128 tiles of 4 waves 1.05 with
-// the second, 0.99 with the first.  (16 waves with the second loop: 1.27; 4
-// waves of 128 x 128 with the first: 0.96; two wave groups that alternate
-// between LDS reads and matrix instructions: 1.24.)
+// use.  bf16, 8192^3, both operands kMajorK: 1.40 PFLOP/s with the first loop
+// and this tile (a large library product: 1.44), 1.22 with the second; 128 x
+// 128 tiles of 4 waves 1.08 with the second; a bucket of 1024-sized matrices,
+// whose launches these share, takes 1178 us with the second for them and 1214
+// with the first.  (16 waves with the second loop: 1.27; 4 waves of 128 x 128
+// with the first: 0.96; two wave groups that alternate between LDS reads and
+// matrix instructions: 1.24; stages of 32 elements, five of them in the LDS: 9%
+// slower, its loads being half lines.)
 template <Elem E, class S, Major AM, Major BMJ, bool ALIGNED>
 struct TileProduct {
   using T = ElemOf<E>;
