@@ -123,6 +123,8 @@ struct ar_experts {
 namespace {
 
 constexpr int64_t kMaxFeatures = 1 << 22, kMaxStride = 1 << 22;
+// rows are counted in int32, rounded up to whole tiles and parts
+constexpr size_t kMaxTokens = (size_t{1} << 31) - 65536;
 
 // [p, p + n) and [q, q + m) share a byte.
 bool overlap(const void *p, int64_t n, const void *q, int64_t m) {
@@ -173,7 +175,7 @@ enum Which { kForward, kInputGrad, kWeightGrad };
 
 ar_status_t run(ar_experts *ex, Which which, const RowsArg &r1, const RowsArg &r2, const void *arena, bool out_is_rows,
                 bool accumulate, const int32_t *ends, size_t ntokens, void *stream) {
-  if (ntokens > static_cast<size_t>(INT32_MAX)) return fail(AR_ERR_INVALID_ARG, "more than 2^31 - 1 tokens");
+  if (ntokens > kMaxTokens) return fail(AR_ERR_INVALID_ARG, "more than 2^31 - 65536 tokens");
   const int64_t t = static_cast<int64_t>(ntokens), elem = ex->bf16 ? 2 : 4;
   int64_t b1 = 0, b2 = 0;
   ar_status_t st = check_rows(r1, t, elem, &b1);

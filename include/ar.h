@@ -706,7 +706,8 @@ ar_experts_stats_t ar_experts_stats(const ar_experts_t *plan);
  * captured or not.  weight_grad may (few experts of few features, many rows:
  * the rows are cut into parts whose sums are added in a fixed order): no two
  * of one plan may overlap in time, replays of captured ones included.
- * ntokens = 0: forward and input_grad do nothing.  AR_ERR_INVALID_ARG for bad
+ * ntokens: up to 2^31 - 65536; 0: forward and input_grad do nothing (but
+ * prepare the plan).  AR_ERR_INVALID_ARG for bad
  * arguments or another device than the plan's; AR_ERR_UNSUPPORTED for a
  * product beyond one launch grid; AR_ERR_HIP if the launch fails.
  */
@@ -780,7 +781,8 @@ typedef struct {
  * grad_dtype (of the gradients) and weight_dtype (of the weights and of
  * ar_orthogonalize's output): AR_FLOAT32 or AR_BFLOAT16.  rows and cols up to
  * 2^20; a matrix with none of either is skipped.  Returns NULL on error
- * (AR_ERR_INVALID_ARG, also where matrices overlap).  Host only.
+ * (AR_ERR_INVALID_ARG, also where matrices overlap, or where they are more
+ * than one plan takes: about 400 GB of workspace).  Host only.
  */
 ar_muon_plan_t *ar_muon_plan_create(int nmatrices, const size_t *rows, const size_t *cols, const size_t *offsets,
                                     ar_dtype_t grad_dtype, ar_dtype_t weight_dtype);

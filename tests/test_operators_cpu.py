@@ -95,6 +95,15 @@ def test_experts_weight_grad_refuses(experts, change, word):
     assert word in msg
 
 
+def test_experts_rows_end_below_32_bits(experts):
+    """Rows rounded up to whole tiles and parts stay inside int32."""
+    n = (1 << 31) - 65535
+    for call in (lambda: B.ar_experts_forward(experts, far(0), far(1), far(2), far(3), ntokens=n),
+                 lambda: B.ar_experts_input_grad(experts, far(0), far(1), far(2), far(3), ntokens=n),
+                 lambda: B.ar_experts_weight_grad(experts, far(0), far(1), far(2), far(3), ntokens=n)):
+        assert "tokens" in refused(B.AR_ERR_INVALID_ARG, call)
+
+
 def test_experts_binding_checks_tensors(experts):
     x = torch.zeros(8, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="not a device tensor"):
