@@ -151,6 +151,10 @@ struct Operand {
   static constexpr int kBytes = W * 128;
   static constexpr int kRow = W * ES / 16;   // chunks of a kMajorMN row
   static_assert(kPer * NT == kChunks, "whole chunks per thread");
+  // Unaligned: stages on their way in registers.  Three for small tiles (64 rows,
+  // 8 experts, 2047 -> 1023: 24 us, with one 28), one for those whose workgroups
+  // share a CU (weight gradients of 8192 rows, 2047 x 2047: 207 us, 229).
+  static constexpr int kSets = ALIGNED ? 0 : kPer <= 2 ? 3 : 1;
 
   const T *base;
   int64_t ld;
@@ -158,7 +162,7 @@ struct Operand {
   uint32_t off[ALIGNED ? kPer : 1];  // bytes from base, contraction step 0
   ux4 res;                           // resource at base
   uint32_t mine;                     // LDS bytes of a stage before this wave's
-  ux4 reg[ALIGNED ? 1 : kPer];
+  ux4 reg[ALIGNED ? 1 : 3][ALIGNED ? 1 : kPer];
 
   __device__ __forceinline__ void point(const T *b) {
     base = b;
@@ -214,12 +218,26 @@ struct Operand {
     }
   }
 
-  // Starts load j of the stage at `base`.  left: as for cut(), which the
-  // aligned form has called before if that is less than a stage.
-  __device__ __forceinline__ void load_one(int j, int left, uint32_t lds) {
-    if constexpr (ALIGNED) {
-      load_to_lds(res, off[j], lds + mine + j * 1024);
-    } else {
+  // Aligned: starts load j of the stage at `base`.
+  __device__ __forceinline__ void load_one(int j, uint32_t lds) {
+    load_to_lds(res, off[j], lds + mine + j * 1024);
+  }
+  __device__ __forceinline__ void load(uint32_t lds) {
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) load_one(j, lds);
+  }
+
+  // Unaligned: starts the loads of the stage at `base`, from where on `rest`
+  // contraction elements exist, into register set `set`; land() takes them to
+  // the LDS.  What lies beyond the contraction's end is zero.  Beyond the last
+  // row/column anything will do, so a kMajorMN piece that ends there is read
+  // whole, into the rows that follow, where these exist: element by element,
+  // the tiles at the edge would be slower than all others together (weight
+  // gradients of 8192 rows, 8 experts, 2047 x 2047: 459 us, so 207).
+  __device__ __forceinline__ void fetch(int set, int rest) {
+    const int left = min(rest, kStep), follow = ld >= kVec ? 1 : kVec;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
       int row, col;
       where(j, row, col);
       const T *p;
@@ -230,6 +248,7 @@ struct Operand {
       } else {
         p = base + static_cast<int64_t>(row) * ld + col * kVec;
         n = row < left ? valid - col * kVec : 0;
+        if (n > 0 && row + follow < rest) n = kVec;
       }
       ux4 v = {};
       if (n >= kVec) {
@@ -241,20 +260,12 @@ struct Operand {
           if (i < n) h[i] = p[i];
         __builtin_memcpy(&v, h, 16);
       }
-      reg[j] = v;
+      reg[set][j] = v;
     }
   }
-  __device__ __forceinline__ void load(int left, uint32_t lds) {
+  __device__ __forceinline__ void land(int set, char *stage) {
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) load_one(j, left, lds);
-  }
-
-  // The register path's second half: what load() read goes to LDS.
-  __device__ __forceinline__ void land(char *stage) {
-    if constexpr (!ALIGNED) {
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) *reinterpret_cast<ux4 *>(stage + (j * NT + threadIdx.x) * 16) = reg[j];
-    }
+    for (int j = 0; j < kPer; ++j) *reinterpret_cast<ux4 *>(stage + (j * NT + threadIdx.x) * 16) = reg[set][j];
   }
 
   // The 16 bytes of contraction elements from (ks * 4 + lane / 16) kVec on, of
@@ -434,23 +445,27 @@ struct TileProduct {
     }
   }
   // Only a list of one pair may end inside a stage: the masks of cut() stay.
-  __device__ __forceinline__ int existing() {
+  __device__ __forceinline__ void existing() {
     const int n = left();
     if (n < kStep) {
       oa.cut(n);
       ob.cut(n);
     }
-    return n;
   }
   __device__ __forceinline__ void load(uint32_t stage) {
-    const int n = existing();
-    oa.load(n, stage);
-    ob.load(n, stage + OpA::kBytes);
+    existing();
+    oa.load(stage);
+    ob.load(stage + OpA::kBytes);
     next();
   }
-  __device__ __forceinline__ void land(char *stage) {
-    oa.land(stage);
-    ob.land(stage + OpA::kBytes);
+  __device__ __forceinline__ void fetch(int set) {
+    oa.fetch(set, k - at * kStep);
+    ob.fetch(set, k - at * kStep);
+    next();
+  }
+  __device__ __forceinline__ void land(int set, char *stage) {
+    oa.land(set, stage);
+    ob.land(set, stage + OpA::kBytes);
   }
 
   __device__ __forceinline__ void run(char *lds, const T *a, const T *b, int64_t lda, int64_t ldb,
@@ -473,7 +488,25 @@ struct TileProduct {
     oa.init(a, lda, validm);
     ob.init(b + (pairs > 1 ? lo_b : 0), ldb, validn);
     if constexpr (kTwoSets) two_sets(lds, per * pairs);
-    else one_set(lds, per * pairs);
+    else if constexpr (ALIGNED) one_set(lds, per * pairs);
+    else through_registers(lds, per * pairs);
+  }
+
+  // The products of the stage at sa.
+  __device__ __forceinline__ void multiply(const char *sa, int rm, int rn) {
+    const char *sb = sa + OpA::kBytes;
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      Frag<E> fa[S::FM], fb[S::FN];
+#pragma unroll
+      for (int i = 0; i < S::FM; ++i) fa[i] = OpA::fragment(sa, rm + i * 16, ks);
+#pragma unroll
+      for (int j = 0; j < S::FN; ++j) fb[j] = OpB::fragment(sb, rn + j * 16, ks);
+#pragma unroll
+      for (int i = 0; i < S::FM; ++i)
+#pragma unroll
+        for (int j = 0; j < S::FN; ++j) acc[i][j] = mfma16<E>(fb[j], fa[i], acc[i][j]);
+    }
   }
 
   __device__ __forceinline__ void one_set(char *lds, int steps) {
@@ -483,34 +516,45 @@ struct TileProduct {
     constexpr int kAhead = kStages - 1;  // stages in flight when a step begins
     constexpr int kLoads = OpA::kPer + OpB::kPer;
     for (int i = 0; i < kAhead && i < steps; ++i) load(lds0 + i * kStage);
-    land(lds);
     int buf = 0, to = kAhead;  // stage read, stage loaded
     for (int t = 0; t < steps; ++t) {
-      if constexpr (!ALIGNED) {
-        __syncthreads();
-      } else if (kAhead > 1 && t + kAhead <= steps) {  // all but the newest kAhead - 1 stages have landed
+      if (kAhead > 1 && t + kAhead <= steps) {  // all but the newest kAhead - 1 stages have landed
         asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((kAhead - 1) * kLoads) : "memory");
       } else {
         loads_done_and_meet();
       }
-      const bool more = t + kAhead < steps;
-      if (more) load(lds0 + to * kStage);
-      const char *sa = lds + buf * kStage, *sb = sa + OpA::kBytes;
-#pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {
-        Frag<E> fa[S::FM], fb[S::FN];
-#pragma unroll
-        for (int i = 0; i < S::FM; ++i) fa[i] = OpA::fragment(sa, rm + i * 16, ks);
-#pragma unroll
-        for (int j = 0; j < S::FN; ++j) fb[j] = OpB::fragment(sb, rn + j * 16, ks);
-#pragma unroll
-        for (int i = 0; i < S::FM; ++i)
-#pragma unroll
-          for (int j = 0; j < S::FN; ++j) acc[i][j] = mfma16<E>(fb[j], fa[i], acc[i][j]);
-      }
-      if (more) land(lds + to * kStage);
+      if (t + kAhead < steps) load(lds0 + to * kStage);
+      multiply(lds + buf * kStage, rm, rn);
       buf = buf + 1 == kStages ? 0 : buf + 1;
       to = to + 1 == kStages ? 0 : to + 1;
+    }
+    __syncthreads();
+  }
+
+  // Operands that are not aligned.  Step t: stage t + kSets starts on its way
+  // to the registers that stage t left for the LDS; after the products stage
+  // t + 1, whose loads began kSets - 1 steps ago, goes to the LDS's other half.
+  __device__ __forceinline__ void through_registers(char *lds, int steps) {
+    constexpr int kSets = OpA::kSets < OpB::kSets ? OpA::kSets : OpB::kSets;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int rm = wave / S::WN * (S::BM / S::WM), rn = wave % S::WN * (S::BN / S::WN);
+#pragma unroll
+    for (int i = 0; i < kSets; ++i)
+      if (i < steps) fetch(i);
+    land(0, lds);
+    auto step = [&](int t, auto set) {
+      constexpr int cur = decltype(set)::value, nxt = (cur + 1) % kSets;
+      __syncthreads();
+      if (t + kSets < steps) fetch(cur);
+      multiply(lds + (t & 1) * kStage, rm, rn);
+      if (t + 1 < steps) land(nxt, lds + (t + 1 & 1) * kStage);
+    };
+    for (int t = 0; t < steps; t += kSets) {
+      step(t, std::integral_constant<int, 0>{});
+      if constexpr (kSets == 3) {
+        if (t + 1 < steps) step(t + 1, std::integral_constant<int, 1>{});
+        if (t + 2 < steps) step(t + 2, std::integral_constant<int, 2>{});
+      }
     }
     __syncthreads();
   }
@@ -556,12 +600,12 @@ struct TileProduct {
       const char *sa = lds + at_a, *sb = lds + part(at_a + kPart);
       const char *na = lds + part(at_a + 2 * kPart), *nb = lds + part(at_a + 3 * kPart);
       const uint32_t da = lds0 + part(at_a + 4 * kPart), db = lds0 + at_a;
-      const int n = decltype(kind)::value == kLast ? existing() : kStep;
+      if constexpr (decltype(kind)::value == kLast) existing();
 #pragma unroll
       for (int i = 0; i < S::FM; ++i) {
         if constexpr (more) {
 #pragma unroll
-          for (int r = i * OpA::kPer / S::FM; r < (i + 1) * OpA::kPer / S::FM; ++r) oa.load_one(r, n, da);
+          for (int r = i * OpA::kPer / S::FM; r < (i + 1) * OpA::kPer / S::FM; ++r) oa.load_one(r, da);
         }
 #pragma unroll
         for (int r = i * kReads / S::FM; r < (i + 1) * kReads / S::FM; ++r) read(1, sa, sb, 1, r);
@@ -575,7 +619,7 @@ struct TileProduct {
       for (int i = 0; i < S::FM; ++i) {
         if constexpr (more) {
 #pragma unroll
-          for (int r = i * OpB::kPer / S::FM; r < (i + 1) * OpB::kPer / S::FM; ++r) ob.load_one(r, n, db);
+          for (int r = i * OpB::kPer / S::FM; r < (i + 1) * OpB::kPer / S::FM; ++r) ob.load_one(r, db);
         }
         // (behind the last stage: what another tile or stage left, not used)
 #pragma unroll

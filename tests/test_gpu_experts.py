@@ -133,6 +133,23 @@ def test_long_weight_gradients(inf, outf, counts, dtype, grad):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("inf,outf", [(1, 1), (3, 2), (7, 5), (2, 131), (129, 3), (257, 263), (1031, 67)])
+@pytest.mark.parametrize("counts", [[70, 0, 65, 1], [300, 129, 64, 2]])
+def test_narrow_and_odd_rows(inf, outf, counts, dtype):
+    """Rows of a few elements, and tiles whose last columns end inside a load, over several stages; what lies
+    behind the last row and in the gaps is NaN."""
+    print("case", inf, outf, counts, dtype, flush=True)
+    c = Case(inf, outf, counts, dtype, extra=2)
+    c.x[sum(counts):], c.dy[sum(counts):] = float("nan"), float("nan")
+    c.check_all()
+    c = Case(inf, outf, counts, dtype, extra=2, pad=(1, 2))
+    for t, n, pad in ((c.x, inf, 1), (c.dy, outf, 2)):
+        t.as_strided((c.t, n + pad), (n + pad, 1))[:, n:] = float("nan")
+    c.check_all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("pad,shift", [((8, 16), 0), ((1, 3), 0), ((0, 0), 1), ((8, 8), 3), ((5, 0), 8), ((4, 4), 4)])
 def test_strides_and_alignment(pad, shift, dtype):
     """Rows with gaps, and rows, weights and gradients that start off 16 bytes; the gaps stay as they were."""
