@@ -114,57 +114,63 @@ __device__ __forceinline__ bool find_row_tile(const ExpertArgs &a, int nt, RowTi
   return false;
 }
 
+// Four elements at any element's address: the hardware takes such 8- and
+// 16-byte loads and stores (weight gradients of 515 rows, 24 experts, 1025 x
+// 511, bf16: 15.7 us; 20.3 with rows off 8 bytes stored by the element).
+typedef ux2 ux2_any __attribute__((aligned(2)));
+typedef fx4 fx4_any __attribute__((aligned(4)));
+
 // Stores v to p[0 .. n) (n in 1 .. 4), rounding once to the output's type.
 // NT: non-temporal, for what the next kernel will hardly find in a cache.
 template <bool BF, bool NT = false>
-__device__ __forceinline__ void store4(void *base, int64_t at, fx4 v, int n, bool vec) {
+__device__ __forceinline__ void store4(void *base, int64_t at, fx4 v, int n) {
   if constexpr (BF) {
     uint16_t h[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) h[i] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(v[i]));
     uint16_t *p = static_cast<uint16_t *>(base) + at;
-    if (vec && n >= 4) {
-      const ux2 u = {h[0] | static_cast<uint32_t>(h[1]) << 16, h[2] | static_cast<uint32_t>(h[3]) << 16};
-      if constexpr (NT) __builtin_nontemporal_store(u, reinterpret_cast<ux2 *>(p));
-      else *reinterpret_cast<ux2 *>(p) = u;
+    if (n >= 4) {
+      const ux2_any u = {h[0] | static_cast<uint32_t>(h[1]) << 16, h[2] | static_cast<uint32_t>(h[3]) << 16};
+      if constexpr (NT) __builtin_nontemporal_store(u, reinterpret_cast<ux2_any *>(p));
+      else *reinterpret_cast<ux2_any *>(p) = u;
     } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < 3; ++i)
         if (i < n) p[i] = h[i];
     }
   } else {
     float *p = static_cast<float *>(base) + at;
-    if (vec && n >= 4) {
-      if constexpr (NT) __builtin_nontemporal_store(v, reinterpret_cast<fx4 *>(p));
-      else *reinterpret_cast<fx4 *>(p) = v;
+    if (n >= 4) {
+      if constexpr (NT) __builtin_nontemporal_store(v, reinterpret_cast<fx4_any *>(p));
+      else *reinterpret_cast<fx4_any *>(p) = v;
     } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < 3; ++i)
         if (i < n) p[i] = v[i];
     }
   }
 }
 template <bool BF>
-__device__ __forceinline__ fx4 load4(const void *base, int64_t at, int n, bool vec) {
+__device__ __forceinline__ fx4 load4(const void *base, int64_t at, int n) {
   fx4 v = {};
   if constexpr (BF) {
     const uint16_t *p = static_cast<const uint16_t *>(base) + at;
-    if (vec && n >= 4) {
-      const ux2 u = *reinterpret_cast<const ux2 *>(p);
+    if (n >= 4) {
+      const ux2 u = *reinterpret_cast<const ux2_any *>(p);
       v = fx4{__uint_as_float(u[0] << 16), __uint_as_float(u[0] & 0xffff0000u), __uint_as_float(u[1] << 16),
               __uint_as_float(u[1] & 0xffff0000u)};
     } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < 3; ++i)
         if (i < n) v[i] = __uint_as_float(static_cast<uint32_t>(p[i]) << 16);
     }
   } else {
     const float *p = static_cast<const float *>(base) + at;
-    if (vec && n >= 4) {
-      v = *reinterpret_cast<const fx4 *>(p);
+    if (n >= 4) {
+      v = *reinterpret_cast<const fx4_any *>(p);
     } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < 3; ++i)
         if (i < n) v[i] = p[i];
     }
   }
@@ -192,7 +198,7 @@ __global__ __launch_bounds__(P::Sh::kThreads) void experts_rows(ExpertArgs a) {
   Out::all(lds, p.acc, [&](int pass, int tid) {
     Out::rows(lds, pass, tid, [&](int m, int c, fx4 v) {
       if (m < t.rows && c < validn)
-        store4<sizeof(T) == 2>(a.out, (t.row + m) * a.outs + n0 + c, v, validn - c, a.vec_out);
+        store4<sizeof(T) == 2>(a.out, (t.row + m) * a.outs + n0 + c, v, validn - c);
     });
   });
 }
@@ -301,7 +307,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void experts_few(ExpertArgs a) {
     for (int e = 0; e < 4; ++e) v[e] += u[e];
   }
   const int m = wave * 16 + r, left = static_cast<int>(min(static_cast<int64_t>(4), a.outf - n0 - (lane >> 4) * 4));
-  if (m < t.rows && left > 0) store4<BF>(a.out, (t.row + m) * a.outs + n0 + (lane >> 4) * 4, v, left, a.vec_out);
+  if (m < t.rows && left > 0) store4<BF>(a.out, (t.row + m) * a.outs + n0 + (lane >> 4) * 4, v, left);
 }
 
 // One tile of one expert's weight gradient.
@@ -337,11 +343,11 @@ __device__ __forceinline__ void store_weights(const ExpertArgs &a, const WeightT
     if (m >= t.validm || c >= t.validn) return;
     const int64_t at = out + m * a.in + c;
     if (a.accumulate) {
-      const fx4 old = load4<GBF>(a.out, at, t.validn - c, a.vec_out);
+      const fx4 old = load4<GBF>(a.out, at, t.validn - c);
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[i] += old[i];
     }
-    store4<GBF, true>(a.out, at, v, t.validn - c, a.vec_out);
+    store4<GBF, true>(a.out, at, v, t.validn - c);
   });
 }
 

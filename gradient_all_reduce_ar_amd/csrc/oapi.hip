@@ -219,7 +219,6 @@ ar_status_t run(ar_experts *ex, Which which, const RowsArg &r1, const RowsArg &r
     a.dys = static_cast<int64_t>(r2.stride);
     a.out = const_cast<void *>(arena);
     a.aligned = rows16(r1) && rows16(r2) && by16;
-    a.vec_out = on(arena, 4 * aelem) && ex->in % 4 == 0 && ex->offsets_by_8;
   } else {
     a.w = arena;
     a.out = const_cast<void *>(r2.p);
@@ -227,7 +226,6 @@ ar_status_t run(ar_experts *ex, Which which, const RowsArg &r1, const RowsArg &r
     (which == kForward ? a.x : a.dy) = r1.p;
     (which == kForward ? a.xs : a.dys) = static_cast<int64_t>(r1.stride);
     a.aligned = rows16(r1) && on(arena, 16) && ex->offsets_by_8 && by16;
-    a.vec_out = on(r2.p, 4 * elem) && r2.stride % 4 == 0;
   }
   hipStream_t s = static_cast<hipStream_t>(stream);
   hipEvent_t mark = nullptr;

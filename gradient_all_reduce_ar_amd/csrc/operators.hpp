@@ -24,7 +24,6 @@ struct ExpertArgs {
   bool grad_bf16;          // element type of the weight gradients
   bool accumulate;
   bool aligned;            // every row and matrix starts on 16 bytes
-  bool vec_out;            // four consecutive outputs can be stored as one
   float *slots;            // weight gradient: partial tiles (experts_weight_slots)
 };
 
