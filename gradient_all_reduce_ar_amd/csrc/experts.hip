@@ -557,19 +557,10 @@ hipError_t launch_weights(const ExpertArgs &a, hipStream_t s) {
   return launch(experts_weights<P, GBF>, tiles, 1, S::kThreads, P::kLds, s, a);
 }
 
-template <class S>
-hipError_t launch_weights(const ExpertArgs &a, hipStream_t s) {
-  if constexpr (S::BM * S::BN > kExpertSlot) {  // aligned bf16 alone
-    return a.grad_bf16 ? launch_weights<kBF16, S, true, true>(a, s) : launch_weights<kBF16, S, false, true>(a, s);
-  } else {
-    if (a.aligned)
-      return !a.bf16       ? launch_weights<kF32, S, false, true>(a, s)
-             : a.grad_bf16 ? launch_weights<kBF16, S, true, true>(a, s)
-                           : launch_weights<kBF16, S, false, true>(a, s);
-    return !a.bf16       ? launch_weights<kF32, S, false, false>(a, s)
-           : a.grad_bf16 ? launch_weights<kBF16, S, true, false>(a, s)
-                         : launch_weights<kBF16, S, false, false>(a, s);
-  }
+template <Elem E, class S, bool ALIGNED>
+hipError_t launch_weights_of(const ExpertArgs &a, hipStream_t s) {
+  if constexpr (E == kF32) return launch_weights<E, S, false, ALIGNED>(a, s);
+  else return a.grad_bf16 ? launch_weights<E, S, true, ALIGNED>(a, s) : launch_weights<E, S, false, ALIGNED>(a, s);
 }
 
 }  // namespace
@@ -578,19 +569,24 @@ hipError_t experts_forward(const ExpertArgs &a, hipStream_t s) { return rows<fal
 hipError_t experts_input_grad(const ExpertArgs &a, hipStream_t s) { return rows<true>(a, s); }
 
 // Big where its tiles give every CU one and an expert's rows fill a few
-// steps; Half where Square's would leave CUs idle, and for operands that are
-// not aligned.  Microseconds Big / Square / Half (rows, experts, in x out):
+// steps; Half where Square's would leave CUs idle, for fp32, and for operands
+// that are not aligned if the rows are few.  Microseconds Big / Square / Half
+// (rows, experts, in x out):
 //   16384, 64, 2048 x 1408:         228 / 226 / 232
 //   16384, 8, 4096 x 2048:          285 / 338 / 616
 //   4096, 32, 2048 x 1024 (128 rows each, bf16 gradients): 68 / 64 / 66
 //   16384, 2, 512 x 512 (32 square tiles):  212 / 118 / 36 (in parts)
-//   8192, 8, 2047 x 2047:             - / 546 / 485
-//   fp32, 8192, 4, 2048 x 2048:       - / 582 / 548
+//   8192, 8, 2047 x 2047:             - / 147 / 175
+//   515, 24, 1025 x 511:              - / 18.6 / 16.6
+//   fp32, 8192, 4, 2048 x 2048:       - / 505 / 508
+//   fp32, 8192, 4, 2047 x 2047:       - / 600 / 608
 hipError_t experts_weight_grad(const ExpertArgs &a, hipStream_t s) {
-  if (a.bf16 && a.aligned && a.tokens >= 256 * static_cast<int64_t>(a.experts) && weight_tiles<Big>(a) >= 256)
-    return launch_weights<Big>(a, s);
-  const bool half = weight_tiles<Square>(a) < 256 || !a.bf16 || !a.aligned;
-  return half ? launch_weights<Half>(a, s) : launch_weights<Square>(a, s);
+  const bool fill = a.tokens >= 256 * static_cast<int64_t>(a.experts);
+  if (a.bf16 && a.aligned && fill && weight_tiles<Big>(a) >= 256) return launch_weights_of<kBF16, Big, true>(a, s);
+  if (!a.bf16) return a.aligned ? launch_weights_of<kF32, Half, true>(a, s) : launch_weights_of<kF32, Half, false>(a, s);
+  if (weight_tiles<Square>(a) < 256 || (!a.aligned && !fill))
+    return a.aligned ? launch_weights_of<kBF16, Half, true>(a, s) : launch_weights_of<kBF16, Half, false>(a, s);
+  return a.aligned ? launch_weights_of<kBF16, Square, true>(a, s) : launch_weights_of<kBF16, Square, false>(a, s);
 }
 
 int64_t experts_weight_slots(int64_t experts, int64_t in, int64_t outf) {

@@ -153,7 +153,8 @@ struct Operand {
   static_assert(kPer * NT == kChunks, "whole chunks per thread");
   // Unaligned: stages on their way in registers.  Three for small tiles (64 rows,
   // 8 experts, 2047 -> 1023: 24 us, with one 28), one for those whose workgroups
-  // share a CU (weight gradients of 8192 rows, 2047 x 2047: 207 us, 229).
+  // share a CU (weight gradients of 8192 rows, 8 experts, 2047 x 2047: 207 us,
+  // with three 229).
   static constexpr int kSets = ALIGNED ? 0 : kPer <= 2 ? 3 : 1;
 
   const T *base;

@@ -132,6 +132,16 @@ def test_long_weight_gradients(inf, outf, counts, dtype, grad):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype,grad", [("bf16", "fp32"), ("bf16", "bf16"), ("fp32", "fp32")])
+@pytest.mark.parametrize("inf,outf,counts", [(2048, 2056, [300, 724, 0, 77]), (1031, 1029, [300, 400, 0, 500]),
+                                             (2056, 4104, [2100]), (1000, 4000, [513, 1500, 1])])
+def test_large_tiles(inf, outf, counts, dtype, grad):
+    """Sizes that the larger tiles are for, with edges in every direction."""
+    print("case", inf, outf, counts, dtype, grad, flush=True)
+    Case(inf, outf, counts, dtype, grad, extra=5).check_all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("inf,outf", [(1, 1), (3, 2), (7, 5), (2, 131), (129, 3), (257, 263), (1031, 67)])
 @pytest.mark.parametrize("counts", [[70, 0, 65, 1], [300, 129, 64, 2]])
