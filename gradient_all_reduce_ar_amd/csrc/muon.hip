@@ -9,14 +9,16 @@
 // a list that the host made once.  A and B are symmetric: only the tiles on
 // and above the diagonal are computed, and each is stored twice.
 //
-// Numbers.  X, A and B are kept as fp16 or as a sum of two (hi + lo, 22
-// bits), scaled by a power of two.  Singular values stay inside a bound that
+// Numbers.  X, A and B are kept as a sum of two fp16 (hi + lo, 22 bits),
+// scaled by a power of two.  Singular values stay inside a bound that
 // the host follows through the steps (X_0 has Frobenius norm at most 1), and
 // no element of a matrix exceeds its largest singular value, so the scale
 // that puts the bound under 2^15 puts every element inside fp16's range, and
 // leaves elements 2^-29 of it still normal numbers.  A product of two sums is
 // three products (hi hi + hi lo + lo hi; lo lo lies 2^-22 below), added into
-// one fp32 sum.
+// one fp32 sum.  bf16 weights take the same: with A and B as one fp16, whose
+// rounding (2^-12 at most) each step amplifies, and X as one in the last step,
+// four 64 x 64 matrices came out 2.05e-3 off, 1.67e-3 being bf16's rounding.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -131,18 +133,18 @@ __device__ __forceinline__ void split(float v, _Float16 &hi, _Float16 &lo) {
   hi = static_cast<_Float16>(v);
   lo = static_cast<_Float16>(v - static_cast<float>(hi));
 }
-__device__ __forceinline__ void store_pair4(uint16_t *hi, uint16_t *lo, fx4 v, bool pair) {
+__device__ __forceinline__ void store_pair4(uint16_t *hi, uint16_t *lo, fx4 v) {
   _Float16 h[4], l[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) split(v[i], h[i], l[i]);
   __builtin_memcpy(__builtin_assume_aligned(hi, 8), h, 8);
-  if (pair) __builtin_memcpy(__builtin_assume_aligned(lo, 8), l, 8);
+  __builtin_memcpy(__builtin_assume_aligned(lo, 8), l, 8);
 }
 
 // X_0: one 64 x 64 block of U, divided by the norm, scaled by 2^ex, turned if
 // the matrix is tall, zeros in the padding.
 template <bool GBF, bool STEP>
-__global__ __launch_bounds__(kThreads) void muon_scale(MuonArgs a, int ex, bool pair) {
+__global__ __launch_bounds__(kThreads) void muon_scale(MuonArgs a, int ex) {
   const MuonTile t = table_entry(a.blocks + blockIdx.x);
   const MuonMat mat = table_entry(a.mats + t.mat);
   double sum = 0;
@@ -189,7 +191,7 @@ __global__ __launch_bounds__(kThreads) void muon_scale(MuonArgs a, int ex, bool 
       for (int k = 0; k < 4; ++k) turn[col + k][row + 16 * p] = u[k];
     } else {
       const int64_t at = static_cast<int64_t>(r) * mat.np + c;
-      store_pair4(x + at, x + plane + at, u, pair);
+      store_pair4(x + at, x + plane + at, u);
     }
   }
   if (!mat.tall) return;
@@ -201,7 +203,7 @@ __global__ __launch_bounds__(kThreads) void muon_scale(MuonArgs a, int ex, bool 
 #pragma unroll
     for (int k = 0; k < 4; ++k) u[k] = turn[m][col + k];
     const int64_t at = static_cast<int64_t>(c0 + m) * mat.np + r0 + col;
-    store_pair4(x + at, x + plane + at, u, pair);
+    store_pair4(x + at, x + plane + at, u);
   }
 }
 
@@ -221,16 +223,16 @@ struct FinishGram {
   int64_t plane;
   float f;
   int mp, ld;
-  bool pair, mirror;
+  bool mirror;
   __device__ __forceinline__ FinishGram(const MuonArgs &a, const MuonStep &k, const MuonMat &mat, bool mir)
       : out(a.ws + mat.a), plane(static_cast<int64_t>(mat.mp) * mat.mp), f(pow2(k.ea - 2 * k.ex)), mp(mat.mp),
-        ld(mat.mp), pair(k.pair_ab), mirror(mir) {}
+        ld(mat.mp), mirror(mir) {}
   __device__ __forceinline__ bool along_rows() const { return true; }
   __device__ __forceinline__ bool along_columns() const { return mirror; }
   __device__ __forceinline__ void put(int r, int c, fx4 v) const {
     if (r >= mp || c >= mp) return;
     const int64_t at = static_cast<int64_t>(r) * ld + c;
-    store_pair4(out + at, out + plane + at, times(v, f), pair);
+    store_pair4(out + at, out + plane + at, times(v, f));
   }
   __device__ __forceinline__ void row(int m, int n, fx4 v) const { put(m, n, v); }
   __device__ __forceinline__ void column(int m, int n, fx4 v) const { put(n, m, v); }
@@ -243,11 +245,11 @@ struct FinishPoly {
   int64_t plane;
   float fa, fb, fc;
   int mp, ld;
-  bool pair, mirror;
+  bool mirror;
   __device__ __forceinline__ FinishPoly(const MuonArgs &a, const MuonStep &k, const MuonMat &mat, bool mir)
       : out(a.ws + mat.b), src(a.ws + mat.a), plane(static_cast<int64_t>(mat.mp) * mat.mp),
         fa(k.coef_a * pow2(k.eb)), fb(k.coef_b * pow2(k.eb - k.ea)), fc(k.coef_c * pow2(k.eb - 2 * k.ea)), mp(mat.mp),
-        ld(mat.mp), pair(k.pair_ab), mirror(mir) {}
+        ld(mat.mp), mirror(mir) {}
   __device__ __forceinline__ bool along_rows() const { return true; }
   __device__ __forceinline__ bool along_columns() const { return mirror; }
   // B[r][c .. c + 3]: A is as symmetric as its tiles were stored, so the
@@ -255,13 +257,13 @@ struct FinishPoly {
   __device__ __forceinline__ void put(int r, int c, fx4 v) const {
     if (r >= mp || c >= mp) return;
     const int64_t at = static_cast<int64_t>(r) * ld + c;
-    _Float16 h[4], l[4] = {0, 0, 0, 0};
+    _Float16 h[4], l[4];
     __builtin_memcpy(h, __builtin_assume_aligned(src + at, 8), 8);
-    if (pair) __builtin_memcpy(l, __builtin_assume_aligned(src + plane + at, 8), 8);
+    __builtin_memcpy(l, __builtin_assume_aligned(src + plane + at, 8), 8);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       v[i] = fc * v[i] + fb * (static_cast<float>(h[i]) + static_cast<float>(l[i])) + (r == c + i ? fa : 0.0f);
-    store_pair4(out + at, out + plane + at, v, pair);
+    store_pair4(out + at, out + plane + at, v);
   }
   __device__ __forceinline__ void row(int m, int n, fx4 v) const { put(m, n, v); }
   __device__ __forceinline__ void column(int m, int n, fx4 v) const { put(n, m, v); }
@@ -273,16 +275,15 @@ struct FinishMul {
   int64_t plane;
   float f;
   int mp, np, ld;
-  bool pair;
   __device__ __forceinline__ FinishMul(const MuonArgs &a, const MuonStep &k, const MuonMat &mat, bool)
       : out(a.ws + (k.from ? mat.x[0] : mat.x[1])), plane(static_cast<int64_t>(mat.mp) * mat.np),
-        f(pow2(k.ex_next - k.eb - k.ex)), mp(mat.mp), np(mat.np), ld(mat.np), pair(k.pair_next) {}
+        f(pow2(k.ex_next - k.eb - k.ex)), mp(mat.mp), np(mat.np), ld(mat.np) {}
   __device__ __forceinline__ bool along_rows() const { return true; }
   __device__ __forceinline__ bool along_columns() const { return false; }
   __device__ __forceinline__ void row(int m, int n, fx4 v) const {
     if (m >= mp || n >= np) return;
     const int64_t at = static_cast<int64_t>(m) * ld + n;
-    store_pair4(out + at, out + plane + at, times(v, f), pair);
+    store_pair4(out + at, out + plane + at, times(v, f));
   }
   __device__ __forceinline__ void column(int, int, fx4) const {}
 };
@@ -371,11 +372,9 @@ __global__ __launch_bounds__(S::kThreads) void muon_product(MuonArgs a, MuonStep
     const uint16_t *x = a.ws + (k.from ? mat.x[1] : mat.x[0]) + t.k0 * (kSym ? 1 : ldb), *sq = a.ws + (PR == kPoly ? mat.a : mat.b) + t.k0;
     const uint16_t *pa = (PR == kGram ? x : sq) + m0 * lda;
     const uint16_t *pb = PR == kPoly ? sq + n0 * ldb : PR == kGram ? x + n0 * ldb : x + n0;
-    // X X^T for a single A takes X's hi alone: lo lies below A's rounding
-    const int pairs = k.pair_ab ? 3 : !kSym && k.pair_x ? 2 : 1;
     using P = TileProduct<kF16, S, kMajorK, kSym ? kMajorK : kMajorMN, true>;
     P p;
-    p.run(lds, pa, pb, lda, ldb, min(S::BM, mp - m0), min(S::BN, cols - n0), t.k1 - t.k0, pairs, mp * lda, mp * ldb);
+    p.run(lds, pa, pb, lda, ldb, min(S::BM, mp - m0), min(S::BN, cols - n0), t.k1 - t.k0, 3, mp * lda, mp * ldb);
     if constexpr (S::BM * S::BN == kMuonSlot) {
       if (t.slot >= 0) {
         fx4 *slot = reinterpret_cast<fx4 *>(a.slots + static_cast<int64_t>(t.slot) * kMuonSlot) + threadIdx.x;
@@ -451,11 +450,9 @@ struct SmallTask {
   fx4 acc[TX][2];
   // kRows x 32 block at (i, j) of P Q over k, a multiple of 32.  P: rows of
   // `pp` bytes along k; Q: the same with QT (Q^T in memory), else rows along
-  // the columns.  lo planes lie lp and lq bytes behind; pairs as in
-  // TileProduct::run.
+  // the columns.  lo planes lie lp and lq bytes behind.
   template <bool QT>
-  __device__ __forceinline__ void run(const char *p, int pp, int lp, const char *q, int pq, int lq, int i, int j, int k,
-                                      int pairs) {
+  __device__ __forceinline__ void run(const char *p, int pp, int lp, const char *q, int pq, int lq, int i, int j, int k) {
     const int lane = threadIdx.x & 63;
     fx4 low[TX][2];  // hi lo + lo hi, added at the end (see TileProduct)
 #pragma unroll
@@ -481,24 +478,24 @@ struct SmallTask {
       }
     };
     for (int ks = 0; ks < k / 32; ++ks) {
-      s16x8 ph[TX], qh[2], pl[TX] = {}, ql[2] = {};
+      s16x8 ph[TX], qh[2], pl[TX], ql[2];
 #pragma unroll
       for (int x = 0; x < TX; ++x) {
         ph[x] = left(0, x, ks);
-        if (pairs == 3) pl[x] = left(1, x, ks);
+        pl[x] = left(1, x, ks);
       }
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
         qh[y] = right(0, y, ks);
-        if (pairs >= 2) ql[y] = right(1, y, ks);
+        ql[y] = right(1, y, ks);
       }
 #pragma unroll
       for (int x = 0; x < TX; ++x)
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
           acc[x][y] = mfma16<kF16>(qh[y], ph[x], acc[x][y]);
-          if (pairs >= 2) low[x][y] = mfma16<kF16>(ql[y], ph[x], low[x][y]);
-          if (pairs == 3) low[x][y] = mfma16<kF16>(qh[y], pl[x], low[x][y]);
+          low[x][y] = mfma16<kF16>(ql[y], ph[x], low[x][y]);
+          low[x][y] = mfma16<kF16>(qh[y], pl[x], low[x][y]);
         }
     }
 #pragma unroll
@@ -608,26 +605,25 @@ __global__ __launch_bounds__(Small<TINY>::kThreads) void muon_small_kernel(MuonA
   const int i = wave / nm * Sm::kRows, j = wave % nm * 32, ix = wave / nn * Sm::kRows, jx = wave % nn * 32;
   auto put = [&](char *base, int pitch, int plane, int m, int n, fx4 v) {
     char *to = base + m * pitch + n * 2;
-    store_pair4(reinterpret_cast<uint16_t *>(to), reinterpret_cast<uint16_t *>(to + plane), v, true);
+    store_pair4(reinterpret_cast<uint16_t *>(to), reinterpret_cast<uint16_t *>(to + plane), v);
   };
   SmallTask<Sm::TX> task;
   for (int step = 0; step < st.n; ++step) {
     const MuonStep &k = st.k[step];
-    const int pairs = k.pair_ab ? 3 : 1;
     if (square) {  // A = X X^T
       const float f = pow2(k.ea - 2 * k.ex);
-      task.template run<true>(x, px, lx, x, px, lx, i, j, np, pairs);
+      task.template run<true>(x, px, lx, x, px, lx, i, j, np);
       task.each(i, j, [&](int m, int n, fx4 v) { put(q, pq, lq, m, n, times(v, f)); });
     }
     __syncthreads();
     if (square) {  // B = a I + b A + c A A
       const float fa = k.coef_a * pow2(k.eb), fb = k.coef_b * pow2(k.eb - k.ea), fc = k.coef_c * pow2(k.eb - 2 * k.ea);
-      task.template run<true>(q, pq, lq, q, pq, lq, i, j, mp, pairs);
+      task.template run<true>(q, pq, lq, q, pq, lq, i, j, mp);
       task.change(i, j, [&](int m, int n, fx4 &v) {
         const char *p = q + m * pq + n * 2;
-        _Float16 h[4], l[4] = {0, 0, 0, 0};
+        _Float16 h[4], l[4];
         __builtin_memcpy(h, __builtin_assume_aligned(p, 8), 8);
-        if (k.pair_ab) __builtin_memcpy(l, __builtin_assume_aligned(p + lq, 8), 8);
+        __builtin_memcpy(l, __builtin_assume_aligned(p + lq, 8), 8);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           v[e] = fc * v[e] + fb * (static_cast<float>(h[e]) + static_cast<float>(l[e])) + (m == n + e ? fa : 0.0f);
@@ -636,7 +632,7 @@ __global__ __launch_bounds__(Small<TINY>::kThreads) void muon_small_kernel(MuonA
     __syncthreads();
     if (square) task.each(i, j, [&](int m, int n, fx4 v) { put(q, pq, lq, m, n, v); });
     __syncthreads();
-    if (wide) task.template run<false>(q, pq, lq, x, px, lx, ix, jx, mp, k.pair_ab ? 3 : k.pair_x ? 2 : 1);
+    if (wide) task.template run<false>(q, pq, lq, x, px, lx, ix, jx, mp);
     if (k.last) break;
     __syncthreads();
     if (wide) {  // X <- B X
@@ -732,7 +728,7 @@ hipError_t muon_small(const MuonArgs &a, const MuonSteps &k, int32_t nmats, int3
   return tiny ? small<true>(a, k, nmats, lds, s) : small<false>(a, k, nmats, lds, s);
 }
 
-hipError_t muon_begin(const MuonArgs &a, int32_t ex0, bool pair, hipStream_t s) {
+hipError_t muon_begin(const MuonArgs &a, int32_t ex0, hipStream_t s) {
   hipError_t e;
   if (a.step)
     e = a.g_bf16 ? go(muon_norm<true, true>, a.nparts, kThreads, 0, s, a)
@@ -743,10 +739,10 @@ hipError_t muon_begin(const MuonArgs &a, int32_t ex0, bool pair, hipStream_t s) 
   if (e != hipSuccess) return e;
   const int ex = ex0;
   if (a.step)
-    return a.g_bf16 ? go(muon_scale<true, true>, a.nblocks, kThreads, 0, s, a, ex, pair)
-                    : go(muon_scale<false, true>, a.nblocks, kThreads, 0, s, a, ex, pair);
-  return a.g_bf16 ? go(muon_scale<true, false>, a.nblocks, kThreads, 0, s, a, ex, pair)
-                  : go(muon_scale<false, false>, a.nblocks, kThreads, 0, s, a, ex, pair);
+    return a.g_bf16 ? go(muon_scale<true, true>, a.nblocks, kThreads, 0, s, a, ex)
+                    : go(muon_scale<false, true>, a.nblocks, kThreads, 0, s, a, ex);
+  return a.g_bf16 ? go(muon_scale<true, false>, a.nblocks, kThreads, 0, s, a, ex)
+                  : go(muon_scale<false, false>, a.nblocks, kThreads, 0, s, a, ex);
 }
 
 hipError_t muon_gram(const MuonArgs &a, const MuonStep &k, hipStream_t s) {

@@ -338,7 +338,7 @@ double step_bound(double a, double b, double c, double s) {
 int32_t scale_exp(double bound) { return 15 - static_cast<int32_t>(std::ceil(std::log2(std::max(bound, 1e-6) * 1.0625))); }
 
 // The steps' factors; false where a bound is passed.
-bool make_steps(int n, const double *abc, bool pair_ab, std::vector<MuonStep> &steps, int32_t &ex0) {
+bool make_steps(int n, const double *abc, std::vector<MuonStep> &steps, int32_t &ex0) {
   steps.clear();
   double s = 1;  // largest singular value; X_0's Frobenius norm is at most 1
   ex0 = scale_exp(s);
@@ -360,11 +360,6 @@ bool make_steps(int n, const double *abc, bool pair_ab, std::vector<MuonStep> &s
     s = next;
     k.ex_next = scale_exp(s);
     k.last = i + 1 == n;
-    // the last step's X may be one fp16 where the others are: nothing
-    // amplifies its rounding any more
-    k.pair_ab = pair_ab;
-    k.pair_x = pair_ab || !k.last;
-    k.pair_next = pair_ab || i + 2 < n;
     k.from = i & 1;
     steps.push_back(k);
   }
@@ -384,7 +379,7 @@ struct Tile {
 // contraction step where every CU has one workgroup at most (`alone`, a launch
 // of up to 256 tiles) and where the launch is full, of the rest of a tile's
 // work, and of that which a square product adds (`mirror`: its tiles leave
-// twice).  Measured with the three shapes, pairs: the product with X of
+// twice).  Measured with the three shapes: the product with X of
 // 512 x 2048 (alone) 37, 21 and 12 us, of 12288 x 4096 (full) 891, 1123 and
 // 2022; X X^T of 512 x 2048 65 and 33 with the smaller two, of eight matrices
 // of 1024 x 1024 and 1024 x 2048 84 (split) and 107 with the largest and the
@@ -400,13 +395,14 @@ constexpr ShapeCost kCost[ar_dev::kMuonShapes] = {
 // launch) and launches the join.
 constexpr double kJoinLaunch = 6.0, kJoinSlot = 2 * 262144 / 5.5e6;
 constexpr int32_t kMinPiece = 4;  // steps of a piece at least
+constexpr int kPairs = 3;         // planes' products of a step (TileProduct)
 
 // The time until the last tile is done if each goes, in order, to the
-// workgroup with the least to do.  pairs: planes' products of a step.
-double list_time(const std::vector<Tile> &tiles, const ShapeCost &c, int pairs, double rest) {
+// workgroup with the least to do.
+double list_time(const std::vector<Tile> &tiles, const ShapeCost &c, double rest) {
   std::vector<double> heap(c.slots, 0.0);  // the least on top
   const auto more = [](double x, double y) { return x > y; };
-  const double step = pairs * (tiles.size() <= 256 ? c.alone : c.full);
+  const double step = kPairs * (tiles.size() <= 256 ? c.alone : c.full);
   double last = 0;
   for (const Tile &t : tiles) {
     std::pop_heap(heap.begin(), heap.end(), more);
@@ -421,8 +417,7 @@ double list_time(const std::vector<Tile> &tiles, const ShapeCost &c, int pairs, 
 // tiles while they fit into an equal share of the steps; the other tiles are
 // cut along the contraction to fill what is left of the shares.  Returns the
 // time until the joined tiles are out.
-double split_tiles(const std::vector<Tile> &tiles, const ShapeCost &c, int pairs, double rest_time,
-                   ar_muon_plan::Work &w) {
+double split_tiles(const std::vector<Tile> &tiles, const ShapeCost &c, double rest_time, ar_muon_plan::Work &w) {
   const int32_t groups = c.slots;
   int64_t total = 0;
   for (const Tile &t : tiles) total += t.steps;
@@ -484,7 +479,7 @@ double split_tiles(const std::vector<Tile> &tiles, const ShapeCost &c, int pairs
   for (const auto &items : of) {
     double time = 0;
     for (const ar_dev::MuonItem &x : items)
-      time += (x.k1 - x.k0) / kStep * (pairs * c.full) + (x.slot >= 0 ? c.rest : rest_time);
+      time += (x.k1 - x.k0) / kStep * (kPairs * c.full) + (x.slot >= 0 ? c.rest : rest_time);
     last = std::max(last, time);
   }
   // workgroup b runs on XCD b % 8: neighbouring shares go to one XCD, whose
@@ -501,17 +496,17 @@ double split_tiles(const std::vector<Tile> &tiles, const ShapeCost &c, int pairs
 // Chooses the tile shape, whole or split, with the least modelled time, and
 // makes the launch's lists.
 template <class List>
-void plan_product(List list, int pairs, bool sym, ar_muon_plan::Work &w) {
+void plan_product(List list, bool sym, ar_muon_plan::Work &w) {
   double best = 0;
   bool split = false;
   std::vector<Tile> tiles;
   for (int i = 0; i < ar_dev::kMuonShapes; ++i) {
     std::vector<Tile> t = list(ar_dev::muon_tile(i));
     const ShapeCost &c = kCost[i];
-    const double rest = c.rest + (sym ? c.mirror : 0), whole = list_time(t, c, pairs, rest);
+    const double rest = c.rest + (sym ? c.mirror : 0), whole = list_time(t, c, rest);
     if (i == 0) {
       ar_muon_plan::Work cut;
-      const double even = split_tiles(t, c, pairs, rest, cut);
+      const double even = split_tiles(t, c, rest, cut);
       if (even < whole) {
         best = even;
         split = true;
@@ -552,7 +547,6 @@ void lay_out(ar_muon_plan *p) {
     p->small_lds = static_cast<int32_t>(lds);
     return;
   }
-  const bool pair_ab = !p->w_bf16;
   int64_t ws = 0, part0 = 0;
   auto take = [&](int64_t n) {
     const int64_t at = ws;
@@ -564,10 +558,10 @@ void lay_out(ar_muon_plan *p) {
     MuonMat &m = p->mats[i];
     const int64_t size = static_cast<int64_t>(m.rows) * m.cols;
     const int64_t x = static_cast<int64_t>(m.mp) * m.np;
-    const int64_t sq = static_cast<int64_t>(m.mp) * m.mp * (pair_ab ? 2 : 1);
+    const int64_t sq = static_cast<int64_t>(m.mp) * m.mp;
     for (int b = 0; b < 2; ++b) m.x[b] = take(2 * x);
-    m.a = take(sq);
-    m.b = take(sq);
+    m.a = take(2 * sq);
+    m.b = take(2 * sq);
     // parts: of 4096 elements, larger where a matrix would have more than 1024
     m.chunk = static_cast<int32_t>(up(std::max<int64_t>(4096, (size + 1023) / 1024), 1024));
     m.parts = static_cast<int32_t>((size + m.chunk - 1) / m.chunk);
@@ -601,10 +595,10 @@ void lay_out(ar_muon_plan *p) {
     return t;
   };
   longest([](const MuonMat &m) { return m.np; });
-  plan_product([&](int64_t bt) { return tiles(bt, true, true); }, pair_ab ? 3 : 1, true, p->gram);
+  plan_product([&](int64_t bt) { return tiles(bt, true, true); }, true, p->gram);
   longest([](const MuonMat &m) { return m.mp; });
-  plan_product([&](int64_t bt) { return tiles(bt, true, false); }, pair_ab ? 3 : 1, true, p->poly);
-  plan_product([&](int64_t bt) { return tiles(bt, false, false); }, pair_ab ? 3 : 2, false, p->mul);
+  plan_product([&](int64_t bt) { return tiles(bt, true, false); }, true, p->poly);
+  plan_product([&](int64_t bt) { return tiles(bt, false, false); }, false, p->mul);
   int64_t slots = 0;
   for (const ar_muon_plan::Work *w : {&p->gram, &p->poly, &p->mul})
     for (const ar_dev::MuonJoin &j : w->joins) slots = std::max<int64_t>(slots, j.slot + j.count);
@@ -754,7 +748,7 @@ ar_status_t run(ar_muon_plan *p, const MuonCall &c, void *stream) {
     ar_dev::t_launch_events = ar_dev::LaunchEvents{};
     return e == hipSuccess ? AR_OK : hip_fail(e, "kernel launch");
   }
-  hipError_t e = ar_dev::muon_begin(a, p->ex0, p->steps[0].pair_x, s);
+  hipError_t e = ar_dev::muon_begin(a, p->ex0, s);
   for (const MuonStep &k : p->steps) {
     if (e == hipSuccess) e = ar_dev::muon_gram(a, k, s);
     if (e == hipSuccess) e = ar_dev::muon_poly(a, k, s);
@@ -912,7 +906,7 @@ ar_muon_plan_t *ar_muon_plan_create(int nmatrices, const size_t *rows, const siz
     for (size_t i = 1; i < ranges.size(); ++i)
       if (ranges[i].first < ranges[i - 1].second) return fail(AR_ERR_INVALID_ARG, "matrices overlap");
     default_scales(p);
-    (void)make_steps(kNsSteps, nullptr, !p->w_bf16, p->steps, p->ex0);
+    (void)make_steps(kNsSteps, nullptr, p->steps, p->ex0);
     lay_out(p);
     fill_table(p);
     return AR_OK;
@@ -930,7 +924,7 @@ ar_status_t ar_muon_plan_set_iterations(ar_muon_plan_t *p, int n, const double *
     if (n < 1 || n > ar_dev::kMuonMaxSteps) return fail(AR_ERR_INVALID_ARG, "iterations must be from 1 to 32");
     std::vector<MuonStep> steps;
     int32_t ex0 = 0;
-    if (!make_steps(n, abc, !p->w_bf16, steps, ex0))
+    if (!make_steps(n, abc, steps, ex0))
       return fail(AR_ERR_INVALID_ARG, "the coefficients let singular values or a factor grow beyond bounds");
     p->steps = std::move(steps);
     p->ex0 = ex0;

@@ -40,7 +40,7 @@ constexpr int kExpertSlot = 64 * 128;
 // One matrix.  m <= n: its smaller and larger side; tall: rows > cols, worked
 // on transposed.  mp, np: m and n rounded up to kMuonPad.  x, a, b: first
 // element (16-bit) of its buffers in the workspace: two X buffers of two
-// planes (hi, lo) of mp x np, A and B of one or two planes of mp x mp.
+// planes (hi, lo) of mp x np, A and B of two planes of mp x mp.
 struct MuonMat {
   int64_t at;  // first element in the arenas
   int64_t x[2], a, b;
@@ -97,9 +97,6 @@ struct MuonArgs {
 struct MuonStep {
   float coef_a, coef_b, coef_c;
   int32_t ex, ea, eb, ex_next;
-  bool pair_x;       // X is held as hi + lo
-  bool pair_next;    // so is the next X
-  bool pair_ab;      // so are A and B
   bool last;
   int32_t from;      // X buffer read
 };
@@ -123,7 +120,7 @@ int muon_tile(int shape);
 constexpr int kMuonShapes = 3;
 constexpr int kMuonSlot = 256 * 256;
 
-hipError_t muon_begin(const MuonArgs &a, int32_t ex0, bool pair, hipStream_t s);
+hipError_t muon_begin(const MuonArgs &a, int32_t ex0, hipStream_t s);
 hipError_t muon_gram(const MuonArgs &a, const MuonStep &k, hipStream_t s);
 hipError_t muon_poly(const MuonArgs &a, const MuonStep &k, hipStream_t s);
 hipError_t muon_apply(const MuonArgs &a, const MuonStep &k, hipStream_t s);

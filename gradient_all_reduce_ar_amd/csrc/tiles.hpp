@@ -387,10 +387,10 @@ struct TileOut {
   }
 };
 
-// The contraction over k, or over up to three pairs of planes of length k
-// (a multiple of kStepK then) added into one sum: numbers held as the sum of
-// two 16-bit planes, hi and lo, give hi lo + lo hi + hi hi (three pairs), or
-// hi lo + hi hi where A has one plane (two).  The small products come first:
+// The contraction over k, or over three pairs of planes of length k (a
+// multiple of kStepK then) added into one sum: numbers held as the sum of two
+// 16-bit planes, hi and lo, give hi lo + lo hi + hi hi.  The small products
+// come first:
 // every addition to a sum is off by a part of the sum (the matrix instruction
 // cuts), and with hi hi first the other two pairs would add to the full sum
 // (X X^T of 64 x 2432: 4.9e-6 off, in this order 2.1e-6).  Finishes with all

@@ -749,13 +749,11 @@ void ar_experts_destroy(ar_experts_t *plan);
  * Precision.  The momentum is fp32 and its update and the norm are computed
  * in fp32 and fp64.  The products run on fp16 matrix instructions with fp32
  * sums; X, A and b A + c A A + a I are scaled by powers of two that keep them
- * inside fp16's range whatever the input's size.  weight_dtype AR_FLOAT32:
- * every factor is held as a sum of two fp16 (22 bits), three products each;
- * the relative error is near that of fp32 arithmetic.  AR_BFLOAT16: X is held
- * so up to the last step (a rounding of X is amplified by up to a per step,
- * so a single fp16 costs 1e-2 and more on a matrix of few large singular
- * values), the other factors as one fp16: the error stays below the bf16
- * rounding of the result.
+ * inside fp16's range whatever the input's size.  Every factor is held as a
+ * sum of two fp16 (22 bits), three products each (a rounding of X is amplified
+ * by up to a per step, so a single fp16 costs 1e-2 and more on a matrix of few
+ * large singular values); the relative error is near that of fp32 arithmetic.
+ * weight_dtype AR_BFLOAT16 computes the same and rounds each result once.
  * A matrix that holds an infinity or NaN gives NaN in all its results (its
  * momentum as the formula says) and changes no other matrix.
  */

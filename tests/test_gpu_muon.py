@@ -425,3 +425,26 @@ def test_experts_reduce_then_step():
     B.ar_bucket_plan_destroy(bp)
     B.ar_experts_destroy(ex)
     B.ar_muon_plan_destroy(mu)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("grad", ["fp32", "bf16"])
+@pytest.mark.parametrize("shapes", [[(64, 64)] * 4, [(33, 47), (128, 128), (9, 300)], [(300, 200), (160, 224)],
+                                    [(1030, 1100)]], ids=lambda s: "+".join(f"{r}x{c}" for r, c in s[:3]))
+def test_bf16_results_are_the_fp32_ones_rounded_once(shapes, grad):
+    """bf16 weights are computed with the factors that fp32 weights have: the same numbers, rounded once."""
+    offs, n = back_to_back(shapes)
+    g = arena(matrices(shapes, "normal", 8), offs, n, grad)
+    w = arena(matrices(shapes, "normal", 9), offs, n, "bf16")
+    res = {}
+    for weight in ("fp32", "bf16"):
+        plan = B.ar_muon_plan_create(shapes, grad, weight)
+        out, m, w1 = torch.empty(n, device=DEV, dtype=T[weight]), torch.ones(n, device=DEV), w.to(T[weight])
+        B.ar_orthogonalize(plan, g, out)
+        B.ar_muon_step(plan, g, m, w1, 0.1, weight_decay=0.1)
+        torch.cuda.synchronize()
+        res[weight] = out, m, w1
+        B.ar_muon_plan_destroy(plan)
+    for wide, narrow, what in zip(res["fp32"], res["bf16"], ("orthogonalised", "momentum", "weights")):
+        differ = int((wide.to(narrow.dtype) != narrow).sum())
+        assert differ == 0, f"{what}: {differ} of {n} elements differ"
