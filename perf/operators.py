@@ -9,7 +9,6 @@ orthogonalisation alone, and the whole Muon step).
 ``exact`` is the definition in fp64.
 """
 import math
-import sys
 
 import numpy as np
 import torch
@@ -177,9 +176,8 @@ class _Plan:
     def __init__(self, handle, destroy):
         self.handle, self.destroy = handle, destroy
 
-    def __del__(self, finalizing=sys.is_finalizing):
-        if not finalizing():  # then the library's module is gone already
-            self.destroy(self.handle)
+    def __del__(self):
+        self.destroy(self.handle)
 
 
 def prepare(case, seed):
