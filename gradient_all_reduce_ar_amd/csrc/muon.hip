@@ -14,7 +14,9 @@
 // the host follows through the steps (X_0 has Frobenius norm at most 1), and
 // no element of a matrix exceeds its largest singular value, so the scale
 // that puts the bound under 2^15 puts every element inside fp16's range, and
-// leaves elements 2^-29 of it still normal numbers.  A product of two sums is
+// leaves elements 2^-29 of it still normal numbers.  (A matrix whose norm is
+// below the constant beside it has a power of two of its own on top, from
+// that norm: MuonStep.)  A product of two sums is
 // three products (hi hi + hi lo + lo hi; lo lo lies 2^-22 below), added into
 // one fp32 sum.  bf16 weights take the same: with A and B as one fp16, whose
 // rounding (2^-12 at most) each step amplifies, and X as one in the last step,
@@ -128,6 +130,13 @@ __global__ __launch_bounds__(kThreads) void muon_norm(MuonArgs a) {
   }
 }
 
+// d_0 of a matrix (MuonStep): 0 where the norm is zero, infinite or NaN.
+__device__ __forceinline__ int first_shift(double norm) {
+  const double r = norm / (norm + kEps);
+  return r > 0 && r < 0.5 ? -ilogb(r) - 1 : 0;
+}
+__device__ __forceinline__ int next_shift(int d, const MuonStep &k) { return max(0, d - k.drop); }
+
 // hi + lo of a number already scaled into fp16's range.
 __device__ __forceinline__ void split(float v, _Float16 &hi, _Float16 &lo) {
   hi = static_cast<_Float16>(v);
@@ -141,10 +150,10 @@ __device__ __forceinline__ void store_pair4(uint16_t *hi, uint16_t *lo, fx4 v) {
   __builtin_memcpy(__builtin_assume_aligned(lo, 8), l, 8);
 }
 
-// X_0: one 64 x 64 block of U, divided by the norm, scaled by 2^ex, turned if
-// the matrix is tall, zeros in the padding.
+// X_0: one 64 x 64 block of U, divided by the norm, scaled by 2^(ex0 + d_0),
+// turned if the matrix is tall, zeros in the padding; and every step's d.
 template <bool GBF, bool STEP>
-__global__ __launch_bounds__(kThreads) void muon_scale(MuonArgs a, int ex) {
+__global__ __launch_bounds__(kThreads) void muon_scale(MuonArgs a, MuonSteps st) {
   const MuonTile t = table_entry(a.blocks + blockIdx.x);
   const MuonMat mat = table_entry(a.mats + t.mat);
   double sum = 0;
@@ -157,7 +166,14 @@ __global__ __launch_bounds__(kThreads) void muon_scale(MuonArgs a, int ex) {
   __syncthreads();
   sum = 0;
   for (int w = 0; w < kThreads / 64; ++w) sum += waves[w];
-  const double inv = ldexp(1.0, ex) / (sqrt(sum) + kEps);
+  const double norm = sqrt(sum);
+  int d = first_shift(norm);
+  const double inv = ldexp(1.0, st.ex0 + d) / (norm + kEps);
+  if (t.m == 0 && t.n == 0 && threadIdx.x == 0)
+    for (int i = 0; i < st.n; ++i) {
+      a.shifts[t.mat * kMuonMaxSteps + i] = d;
+      d = next_shift(d, st.k[i]);
+    }
   const int r0 = (mat.tall ? t.n : t.m) * 64, c0 = (mat.tall ? t.m : t.n) * 64;  // of the matrix as given
   const int col = threadIdx.x % 16 * 4, row = threadIdx.x / 16;
   uint16_t *const x = a.ws + mat.x[0];
@@ -210,11 +226,15 @@ __global__ __launch_bounds__(kThreads) void muon_scale(MuonArgs a, int ex) {
 __device__ __forceinline__ float pow2(int e) { return ldexpf(1.0f, e); }
 
 __device__ __forceinline__ fx4 times(fx4 v, float f) { return fx4{v[0] * f, v[1] * f, v[2] * f, v[3] * f}; }
+__device__ __forceinline__ fx4 shifted(fx4 v, int e) {
+  return fx4{ldexpf(v[0], e), ldexpf(v[1], e), ldexpf(v[2], e), ldexpf(v[3], e)};
+}
 
 // Where the sums of a tile go: row(m, n, v) takes C[m][n .. n + 3], column(m,
 // n, v) takes C[m .. m + 3][n].  A and B are stored along rows, and off the
 // diagonal tiles along columns too, as the transposed tile; a tall matrix's
-// result, which is held transposed, along columns only.
+// result, which is held transposed, along columns only.  d: the matrix's d_k
+// (MuonStep), which A's factor does not need, as X's and A's cancel.
 enum Product { kGram, kPoly, kMul, kLast };
 
 // A = X X^T
@@ -224,7 +244,7 @@ struct FinishGram {
   float f;
   int mp, ld;
   bool mirror;
-  __device__ __forceinline__ FinishGram(const MuonArgs &a, const MuonStep &k, const MuonMat &mat, bool mir)
+  __device__ __forceinline__ FinishGram(const MuonArgs &a, const MuonStep &k, const MuonMat &mat, int, bool mir)
       : out(a.ws + mat.a), plane(static_cast<int64_t>(mat.mp) * mat.mp), f(pow2(k.ea - 2 * k.ex)), mp(mat.mp),
         ld(mat.mp), mirror(mir) {}
   __device__ __forceinline__ bool along_rows() const { return true; }
@@ -246,10 +266,10 @@ struct FinishPoly {
   float fa, fb, fc;
   int mp, ld;
   bool mirror;
-  __device__ __forceinline__ FinishPoly(const MuonArgs &a, const MuonStep &k, const MuonMat &mat, bool mir)
+  __device__ __forceinline__ FinishPoly(const MuonArgs &a, const MuonStep &k, const MuonMat &mat, int d, bool mir)
       : out(a.ws + mat.b), src(a.ws + mat.a), plane(static_cast<int64_t>(mat.mp) * mat.mp),
-        fa(k.coef_a * pow2(k.eb)), fb(k.coef_b * pow2(k.eb - k.ea)), fc(k.coef_c * pow2(k.eb - 2 * k.ea)), mp(mat.mp),
-        ld(mat.mp), mirror(mir) {}
+        fa(k.coef_a * pow2(k.eb)), fb(k.coef_b * pow2(k.eb - k.ea - 2 * d)),
+        fc(k.coef_c * pow2(k.eb - 2 * k.ea - 4 * d)), mp(mat.mp), ld(mat.mp), mirror(mir) {}
   __device__ __forceinline__ bool along_rows() const { return true; }
   __device__ __forceinline__ bool along_columns() const { return mirror; }
   // B[r][c .. c + 3]: A is as symmetric as its tiles were stored, so the
@@ -275,9 +295,9 @@ struct FinishMul {
   int64_t plane;
   float f;
   int mp, np, ld;
-  __device__ __forceinline__ FinishMul(const MuonArgs &a, const MuonStep &k, const MuonMat &mat, bool)
+  __device__ __forceinline__ FinishMul(const MuonArgs &a, const MuonStep &k, const MuonMat &mat, int d, bool)
       : out(a.ws + (k.from ? mat.x[0] : mat.x[1])), plane(static_cast<int64_t>(mat.mp) * mat.np),
-        f(pow2(k.ex_next - k.eb - k.ex)), mp(mat.mp), np(mat.np), ld(mat.np) {}
+        f(pow2(k.ex_next + next_shift(d, k) - k.eb - k.ex - d)), mp(mat.mp), np(mat.np), ld(mat.np) {}
   __device__ __forceinline__ bool along_rows() const { return true; }
   __device__ __forceinline__ bool along_columns() const { return false; }
   __device__ __forceinline__ void row(int m, int n, fx4 v) const {
@@ -294,17 +314,17 @@ struct FinishLast {
   const void *w;
   void *w_out;
   int64_t at;
-  float f, keep, lr;
-  int m_, n_, cols;
+  float keep, lr;
+  int e, m_, n_, cols;
   bool step, tall;
-  __device__ __forceinline__ FinishLast(const MuonArgs &a, const MuonStep &k, const MuonMat &mat, bool)
-      : w(a.w), w_out(a.w_out), at(mat.at), f(pow2(-k.eb - k.ex)), keep(a.keep), lr(a.lr * mat.scale), m_(mat.m),
+  __device__ __forceinline__ FinishLast(const MuonArgs &a, const MuonStep &k, const MuonMat &mat, int d, bool)
+      : w(a.w), w_out(a.w_out), at(mat.at), keep(a.keep), lr(a.lr * mat.scale), e(-k.eb - k.ex - d), m_(mat.m),
         n_(mat.n), cols(mat.cols), step(a.step), tall(mat.tall) {}
   __device__ __forceinline__ bool along_rows() const { return !tall; }
   __device__ __forceinline__ bool along_columns() const { return tall; }
   // W[r][c .. c + 3] of the matrix as given, `left` columns from c on
   __device__ __forceinline__ void put(int r, int c, int left, fx4 v) const {
-    v = times(v, f);
+    v = shifted(v, e);
     const int64_t to = at + static_cast<int64_t>(r) * cols + c;
     if (left >= 4) {
       if (step) {
@@ -355,6 +375,10 @@ __device__ __forceinline__ const MuonWork &work_of(const MuonArgs &a) {
   return PR == kGram ? a.gram : PR == kPoly ? a.poly : a.mul;
 }
 
+__device__ __forceinline__ int shift_of(const MuonArgs &a, int mat, const MuonStep &k) {
+  return table_entry(a.shifts + mat * kMuonMaxSteps + k.index);
+}
+
 // The products of one step: each workgroup works through its items.  A split
 // item's sums are stored in the order that the threads hold them.
 template <class S, Product PR, bool WBF>
@@ -385,7 +409,7 @@ __global__ __launch_bounds__(S::kThreads) void muon_product(MuonArgs a, MuonStep
         continue;
       }
     }
-    const typename FinishOf<PR, WBF>::type f(a, k, mat, t.m != t.n);
+    const typename FinishOf<PR, WBF>::type f(a, k, mat, shift_of(a, t.mat, k), t.m != t.n);
     using Out = TileOut<S, P::kLds>;
     Out::all(lds, p.acc, [&](int pass, int tid) { leave<Out>(lds, pass, tid, m0, n0, f); });
   }
@@ -420,7 +444,7 @@ __global__ __launch_bounds__(S::kThreads) void muon_join(MuonArgs a, MuonStep k)
   }
   Out::put(lds, v, threadIdx.x);
   __syncthreads();
-  const typename FinishOf<PR, WBF>::type f(a, k, mat, t.m != t.n);
+  const typename FinishOf<PR, WBF>::type f(a, k, mat, shift_of(a, t.mat, k), t.m != t.n);
   leave<Out>(lds, pass, threadIdx.x, t.m * S::BM, t.n * S::BN, f);
 }
 
@@ -566,7 +590,9 @@ __global__ __launch_bounds__(Small<TINY>::kThreads) void muon_small_kernel(MuonA
   __syncthreads();  // also: the new momentum can be read back
   sum = 0;
   for (int w = 0; w < Sm::kWaves; ++w) sum += sums[w];
-  const double inv = ldexp(1.0, st.ex0) / (sqrt(sum) + kEps);
+  const double norm = sqrt(sum);
+  int d = first_shift(norm);
+  const double inv = ldexp(1.0, st.ex0 + d) / (norm + kEps);
   auto fill = [&](int r, int c, float u) {
     _Float16 hi, lo;
     split(static_cast<float>(u * inv), hi, lo);
@@ -617,7 +643,8 @@ __global__ __launch_bounds__(Small<TINY>::kThreads) void muon_small_kernel(MuonA
     }
     __syncthreads();
     if (square) {  // B = a I + b A + c A A
-      const float fa = k.coef_a * pow2(k.eb), fb = k.coef_b * pow2(k.eb - k.ea), fc = k.coef_c * pow2(k.eb - 2 * k.ea);
+      const float fa = k.coef_a * pow2(k.eb), fb = k.coef_b * pow2(k.eb - k.ea - 2 * d);
+      const float fc = k.coef_c * pow2(k.eb - 2 * k.ea - 4 * d);
       task.template run<true>(q, pq, lq, q, pq, lq, i, j, mp);
       task.change(i, j, [&](int m, int n, fx4 &v) {
         const char *p = q + m * pq + n * 2;
@@ -635,14 +662,16 @@ __global__ __launch_bounds__(Small<TINY>::kThreads) void muon_small_kernel(MuonA
     if (wide) task.template run<false>(q, pq, lq, x, px, lx, ix, jx, mp);
     if (k.last) break;
     __syncthreads();
+    const int next = next_shift(d, k);
     if (wide) {  // X <- B X
-      const float f = pow2(k.ex_next - k.eb - k.ex);
+      const float f = pow2(k.ex_next + next - k.eb - k.ex - d);
       task.each(ix, jx, [&](int m, int n, fx4 v) { put(x, px, lx, m, n, times(v, f)); });
     }
+    d = next;
     __syncthreads();
   }
   if (!wide) return;
-  const FinishLast<WBF> f(a, st.k[st.n - 1], mat, false);
+  const FinishLast<WBF> f(a, st.k[st.n - 1], mat, d, false);
   task.each(ix, jx, [&](int m, int n, fx4 v) {
     if (!mat.tall) {
       f.row(m, n, v);
@@ -728,7 +757,7 @@ hipError_t muon_small(const MuonArgs &a, const MuonSteps &k, int32_t nmats, int3
   return tiny ? small<true>(a, k, nmats, lds, s) : small<false>(a, k, nmats, lds, s);
 }
 
-hipError_t muon_begin(const MuonArgs &a, int32_t ex0, hipStream_t s) {
+hipError_t muon_begin(const MuonArgs &a, const MuonSteps &k, hipStream_t s) {
   hipError_t e;
   if (a.step)
     e = a.g_bf16 ? go(muon_norm<true, true>, a.nparts, kThreads, 0, s, a)
@@ -737,12 +766,11 @@ hipError_t muon_begin(const MuonArgs &a, int32_t ex0, hipStream_t s) {
     e = a.g_bf16 ? go(muon_norm<true, false>, a.nparts, kThreads, 0, s, a)
                  : go(muon_norm<false, false>, a.nparts, kThreads, 0, s, a);
   if (e != hipSuccess) return e;
-  const int ex = ex0;
   if (a.step)
-    return a.g_bf16 ? go(muon_scale<true, true>, a.nblocks, kThreads, 0, s, a, ex)
-                    : go(muon_scale<false, true>, a.nblocks, kThreads, 0, s, a, ex);
-  return a.g_bf16 ? go(muon_scale<true, false>, a.nblocks, kThreads, 0, s, a, ex)
-                  : go(muon_scale<false, false>, a.nblocks, kThreads, 0, s, a, ex);
+    return a.g_bf16 ? go(muon_scale<true, true>, a.nblocks, kThreads, 0, s, a, k)
+                    : go(muon_scale<false, true>, a.nblocks, kThreads, 0, s, a, k);
+  return a.g_bf16 ? go(muon_scale<true, false>, a.nblocks, kThreads, 0, s, a, k)
+                  : go(muon_scale<false, false>, a.nblocks, kThreads, 0, s, a, k);
 }
 
 hipError_t muon_gram(const MuonArgs &a, const MuonStep &k, hipStream_t s) {

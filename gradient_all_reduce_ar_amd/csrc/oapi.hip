@@ -277,8 +277,9 @@ struct ar_muon_plan {
   } gram, poly, mul;
   std::vector<char> table;
   size_t at_parts = 0, at_blocks = 0;
-  // workspace: sums of squares, partial tiles, then X, A and B
-  size_t partial_bytes = 0, slot_bytes = 0, ws_bytes = 0;
+  // workspace: sums of squares, shifts, partial tiles, then X, A and B
+  size_t partial_bytes = 0, shift_bytes = 0, slot_bytes = 0, ws_bytes = 0;
+  size_t work_bytes() const { return partial_bytes + shift_bytes + slot_bytes + ws_bytes; }
   int device = -1;
   void *d_table = nullptr, *d_work = nullptr;
   ar_host::CallMarks marks;
@@ -335,7 +336,8 @@ double step_bound(double a, double b, double c, double s) {
 
 // The power of two that takes a number of at most `bound` (and 1/16 more, for
 // what rounding adds) to at most 2^15.
-int32_t scale_exp(double bound) { return 15 - static_cast<int32_t>(std::ceil(std::log2(std::max(bound, 1e-6) * 1.0625))); }
+constexpr double kLeast = 1e-6;  // smaller bounds are taken for this
+int32_t scale_exp(double bound) { return 15 - static_cast<int32_t>(std::ceil(std::log2(std::max(bound, kLeast) * 1.0625))); }
 
 // The steps' factors; false where a bound is passed.
 bool make_steps(int n, const double *abc, std::vector<MuonStep> &steps, int32_t &ex0) {
@@ -357,8 +359,11 @@ bool make_steps(int n, const double *abc, std::vector<MuonStep> &steps, int32_t 
     const double terms = std::fabs(a) + std::fabs(b) * s * s + std::fabs(c) * s * s * s * s;
     if (!(terms <= 1 << 14) || !(next <= 1 << 10)) return false;
     k.eb = scale_exp(q);
-    s = next;
+    // |B X| <= q |X|, which is below `next` too once d is zero
+    k.drop = static_cast<int32_t>(std::ceil(std::log2(std::max(1.0, q * s / std::max(next, kLeast)))));
+    s = std::max(next, kLeast);
     k.ex_next = scale_exp(s);
+    k.index = i;
     k.last = i + 1 == n;
     k.from = i & 1;
     steps.push_back(k);
@@ -603,6 +608,7 @@ void lay_out(ar_muon_plan *p) {
   for (const ar_muon_plan::Work *w : {&p->gram, &p->poly, &p->mul})
     for (const ar_dev::MuonJoin &j : w->joins) slots = std::max<int64_t>(slots, j.slot + j.count);
   p->partial_bytes = static_cast<size_t>(up(part0 * 8, 256));
+  p->shift_bytes = static_cast<size_t>(up(static_cast<int64_t>(nm) * ar_dev::kMuonMaxSteps * 4, 256));
   p->slot_bytes = static_cast<size_t>(slots) * ar_dev::kMuonSlot * 4;
   p->ws_bytes = static_cast<size_t>(ws) * 2;
 }
@@ -643,7 +649,7 @@ ar_status_t prepare(ar_muon_plan *p) {
     fill_table(p);
     e = ar_host::device_table(&p->d_table, p->table.data(), p->table.size());
     if (e == hipSuccess && p->small_lds == 0)
-      e = ar_host::device_table(&p->d_work, nullptr, p->partial_bytes + p->slot_bytes + p->ws_bytes);
+      e = ar_host::device_table(&p->d_work, nullptr, p->work_bytes());
     if (e != hipSuccess) {
       p->release();
       return e == hipErrorOutOfMemory ? fail(AR_ERR_OOM, "Muon workspace allocation") : hip_fail(e, "Muon tables");
@@ -725,8 +731,9 @@ ar_status_t run(ar_muon_plan *p, const MuonCall &c, void *stream) {
   a.mul = work(p->mul);
   char *dw = static_cast<char *>(p->d_work);
   a.partials = reinterpret_cast<double *>(dw);
-  a.slots = reinterpret_cast<float *>(dw + p->partial_bytes);
-  a.ws = reinterpret_cast<uint16_t *>(dw + p->partial_bytes + p->slot_bytes);
+  a.shifts = reinterpret_cast<int32_t *>(dw + p->partial_bytes);
+  a.slots = reinterpret_cast<float *>(dw + p->partial_bytes + p->shift_bytes);
+  a.ws = reinterpret_cast<uint16_t *>(dw + p->partial_bytes + p->shift_bytes + p->slot_bytes);
   a.g = c.g;
   a.mom = c.mom;
   a.mom_out = c.mom_out;
@@ -738,17 +745,17 @@ ar_status_t run(ar_muon_plan *p, const MuonCall &c, void *stream) {
   hipEvent_t mark = nullptr;
   st = p->marks.of(s, &mark);
   if (st != AR_OK) return st;
+  ar_dev::MuonSteps steps{};
+  steps.n = static_cast<int32_t>(p->steps.size());
+  steps.ex0 = p->ex0;
+  std::copy(p->steps.begin(), p->steps.end(), steps.k);
   if (p->small_lds > 0) {
-    ar_dev::MuonSteps k{};
-    k.n = static_cast<int32_t>(p->steps.size());
-    k.ex0 = p->ex0;
-    std::copy(p->steps.begin(), p->steps.end(), k.k);
     ar_dev::t_launch_events = ar_dev::LaunchEvents{nullptr, mark};
-    const hipError_t e = ar_dev::muon_small(a, k, static_cast<int32_t>(p->mats.size()), p->small_lds, p->tiny, s);
+    const hipError_t e = ar_dev::muon_small(a, steps, static_cast<int32_t>(p->mats.size()), p->small_lds, p->tiny, s);
     ar_dev::t_launch_events = ar_dev::LaunchEvents{};
     return e == hipSuccess ? AR_OK : hip_fail(e, "kernel launch");
   }
-  hipError_t e = ar_dev::muon_begin(a, p->ex0, s);
+  hipError_t e = ar_dev::muon_begin(a, steps, s);
   for (const MuonStep &k : p->steps) {
     if (e == hipSuccess) e = ar_dev::muon_gram(a, k, s);
     if (e == hipSuccess) e = ar_dev::muon_poly(a, k, s);
@@ -974,7 +981,7 @@ ar_muon_stats_t ar_muon_plan_stats(const ar_muon_plan_t *p) {
   s.grad_bytes = p->g_bf16 ? 2 : 4;
   s.weight_bytes = p->w_bf16 ? 2 : 4;
   s.arena_count = static_cast<uint64_t>(p->arena);
-  s.workspace_bytes = p->mats.empty() ? 0 : p->table.size() + p->partial_bytes + p->slot_bytes + p->ws_bytes;
+  s.workspace_bytes = p->mats.empty() ? 0 : p->table.size() + p->work_bytes();
   return s;
 }
 

@@ -80,7 +80,8 @@ struct MuonArgs {
   int32_t nparts, nblocks;
   MuonWork gram, poly, mul;  // X X^T, A A, B X
   double *partials;
-  float *slots;  // partial tiles
+  int32_t *shifts;  // [matrix][kMuonMaxSteps]: see MuonStep::drop
+  float *slots;     // partial tiles
   uint16_t *ws;
   const void *g;
   const float *mom;
@@ -94,9 +95,17 @@ struct MuonArgs {
 
 // One step's factors: powers of two that the stored X, A and B and the next
 // X carry, and the polynomial.
+//
+// A matrix whose norm is not far above the constant that is added to it
+// starts with an X_0 far below 1.  Its X carries 2^d more, and its A 2^(2 d):
+// d_0 from the norm, so that ||X_0||_F 2^d_0 is in [1/2, 1), and d_k+1 =
+// max(0, d_k - drop_k), where 2^drop_k is what the step can make of a small X
+// beyond what the bound on the singular values grows by.
 struct MuonStep {
   float coef_a, coef_b, coef_c;
   int32_t ex, ea, eb, ex_next;
+  int32_t drop;
+  int32_t index;     // of the step
   bool last;
   int32_t from;      // X buffer read
 };
@@ -120,7 +129,7 @@ int muon_tile(int shape);
 constexpr int kMuonShapes = 3;
 constexpr int kMuonSlot = 256 * 256;
 
-hipError_t muon_begin(const MuonArgs &a, int32_t ex0, hipStream_t s);
+hipError_t muon_begin(const MuonArgs &a, const MuonSteps &k, hipStream_t s);
 hipError_t muon_gram(const MuonArgs &a, const MuonStep &k, hipStream_t s);
 hipError_t muon_poly(const MuonArgs &a, const MuonStep &k, hipStream_t s);
 hipError_t muon_apply(const MuonArgs &a, const MuonStep &k, hipStream_t s);

@@ -749,7 +749,8 @@ void ar_experts_destroy(ar_experts_t *plan);
  * Precision.  The momentum is fp32 and its update and the norm are computed
  * in fp32 and fp64.  The products run on fp16 matrix instructions with fp32
  * sums; X, A and b A + c A A + a I are scaled by powers of two that keep them
- * inside fp16's range whatever the input's size.  Every factor is held as a
+ * inside fp16's range whatever the input's size (with a power of its own for a
+ * matrix whose norm is not above the 1e-7, taken from its norm).  Every factor is held as a
  * sum of two fp16 (22 bits), three products each (a rounding of X is amplified
  * by up to a per step, so a single fp16 costs 1e-2 and more on a matrix of few
  * large singular values); the relative error is near that of fp32 arithmetic.

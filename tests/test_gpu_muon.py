@@ -448,3 +448,37 @@ def test_bf16_results_are_the_fp32_ones_rounded_once(shapes, grad):
     for wide, narrow, what in zip(res["fp32"], res["bf16"], ("orthogonalised", "momentum", "weights")):
         differ = int((wide.to(narrow.dtype) != narrow).sum())
         assert differ == 0, f"{what}: {differ} of {n} elements differ"
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("grad,weight", [("fp32", "fp32"), ("bf16", "fp32"), ("fp32", "bf16")])
+@pytest.mark.parametrize("steps", [[COEF] * 5, [COEF] * 9, [COEF], [(1.5, -0.5, 0.0)] * 6], ids=["5", "9", "1", "cubic"])
+@pytest.mark.parametrize("shapes", [[(64, 40)] * 8, [(64, 64), (33, 47), (60, 130), (128, 128)] * 2, [(128, 192), (192, 128)] * 4],
+                         ids=["tiny", "small", "tiled"])
+def test_norms_far_below_the_constant(shapes, steps, grad, weight):
+    """Matrices of norms from 1 down to 1e-33 in one plan: below 1e-7 that constant divides, X_0 is smaller than 1
+    by as much, and the results are still right relative to themselves.  The tolerance is the one above with
+    ||X_0||_F = r: ||X_k||_F is at most a^k r."""
+    offs, n = back_to_back(shapes)
+    norms = [1.0, 1e-7, 1e-9, 1e-11, 1e-13, 1e-17, 1e-25, 1e-33]
+    mats = [m * (v / float(m.double().norm())) for m, v in zip(matrices(shapes, "normal", 10), norms)]
+    g = arena(mats, offs, n, grad)
+    out, m, w = torch.full((n,), 7.0, device=DEV, dtype=T[weight]), torch.zeros(n, device=DEV), torch.zeros(n, device=DEV, dtype=T[weight])
+    plan = B.ar_muon_plan_create(shapes, grad, weight)
+    B.ar_muon_plan_set_iterations(plan, len(steps), steps)
+    assert (B.ar_muon_plan_stats(plan)["launches"] == 1) == (shapes[0] != (128, 192))
+    B.ar_orthogonalize(plan, g, out)
+    B.ar_muon_plan_set_scales(plan, [1.0] * len(shapes))
+    B.ar_muon_step(plan, g, m, w, 0.5, mu=0.0, nesterov=False)
+    torch.cuda.synchronize()
+    a, top, k = (steps[0][0], 1.21 if steps[0] == COEF else 1.0, len(steps))
+    for (r, c), at, norm in zip(shapes, offs, norms):
+        u = g[at:at + r * c].view(r, c)
+        want, x0 = orthogonalized(u, steps), float(u.double().norm())
+        x0 /= x0 + 1e-7
+        grown = sum(a ** (k - i) * min(a ** i * x0, top * math.sqrt(min(r, c))) for i in range(k + 1))
+        tol = 4 * 2.0 ** -22 * grown / float(want.norm()) + (2.0 ** -8 if weight == "bf16" else 2.0 ** -24)
+        assert tol < 0.5
+        check(out[at:at + r * c].view(r, c), want, tol, f"{r}x{c} of norm {norm}")
+        check(w[at:at + r * c].view(r, c), -0.5 * want, tol, f"step of {r}x{c} of norm {norm}")
+    B.ar_muon_plan_destroy(plan)
