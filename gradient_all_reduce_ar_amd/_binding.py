@@ -172,6 +172,7 @@ def _declare(L):
         "ar_muon_plan_set_scales": ([P, ctypes.POINTER(dbl)], ctypes.c_int),
         "ar_muon_plan_prepare": ([P], ctypes.c_int),
         "ar_muon_plan_stats": ([P], ar_muon_stats_t),
+        "ar_muon_plan_work": ([P, ctypes.c_int, pi32, pi32, pi32, pi32, pi32, pi32, pi32, pi32, i64], i64),
         "ar_orthogonalize": ([P, P, P, P], ctypes.c_int),
         "ar_muon_step": ([P, P, P, P, P, P, ctypes.POINTER(ar_muon_params_t), P], ctypes.c_int),
         "ar_muon_plan_destroy": ([P], None),
@@ -884,6 +885,20 @@ def ar_muon_plan_prepare(plan):
 def ar_muon_plan_stats(plan):
     s = lib().ar_muon_plan_stats(plan)
     return {k: getattr(s, k) for k, _ in s._fields_}
+
+
+def ar_muon_plan_work(plan, product):
+    """The items of one product of an iteration (0: X X^T, 1: b A + c A A + a I, 2: B X): dict(tile, and per item
+    group, matrix, row, col, k0, k1, slot as arrays; see ar.h)."""
+    import numpy as np
+
+    names, tile = ("group", "matrix", "row", "col", "k0", "k1", "slot"), ctypes.c_int32()
+    n = lib().ar_muon_plan_work(plan, product, ctypes.byref(tile), *[None] * 7, 0)
+    if n < 0:
+        _raise()
+    cols = {k: np.zeros(max(n, 1), np.int32) for k in names}
+    lib().ar_muon_plan_work(plan, product, None, *[cols[k].ctypes.data_as(ctypes.POINTER(ctypes.c_int32)) for k in names], n)
+    return {"tile": tile.value, **{k: v[:n] for k, v in cols.items()}}
 
 
 class _MuonInfo:

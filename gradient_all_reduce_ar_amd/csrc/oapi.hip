@@ -985,6 +985,35 @@ ar_muon_stats_t ar_muon_plan_stats(const ar_muon_plan_t *p) {
   return s;
 }
 
+int64_t ar_muon_plan_work(const ar_muon_plan_t *p, int product, int32_t *tile, int32_t *group, int32_t *matrix,
+                          int32_t *row, int32_t *col, int32_t *k0, int32_t *k1, int32_t *slot, int64_t cap) {
+  if (!p) {
+    fail(AR_ERR_INVALID_ARG, "Muon plan is NULL");
+    return -1;
+  }
+  if (product < 0 || product > 2) {
+    fail(AR_ERR_INVALID_ARG, "product must be from 0 to 2");
+    return -1;
+  }
+  const ar_muon_plan::Work &w = product == 0 ? p->gram : product == 1 ? p->poly : p->mul;
+  if (tile) *tile = w.items.empty() ? 0 : ar_dev::muon_tile(w.shape);
+  auto put = [](int32_t *to, int64_t i, int32_t v) {
+    if (to) to[i] = v;
+  };
+  for (size_t g = 0; g + 1 < w.first.size(); ++g)
+    for (int64_t i = w.first[g]; i < w.first[g + 1] && i < cap; ++i) {
+      const ar_dev::MuonItem &t = w.items[static_cast<size_t>(i)];
+      put(group, i, static_cast<int32_t>(g));
+      put(matrix, i, p->index[static_cast<size_t>(t.mat)]);
+      put(row, i, t.m);
+      put(col, i, t.n);
+      put(k0, i, t.k0);
+      put(k1, i, t.k1);
+      put(slot, i, t.slot);
+    }
+  return static_cast<int64_t>(w.items.size());
+}
+
 ar_status_t ar_orthogonalize(ar_muon_plan_t *p, const void *grads, void *out, void *stream) {
   if (!p) return fail(AR_ERR_INVALID_ARG, "Muon plan is NULL");
   return guarded([&] { return run(p, MuonCall{grads, nullptr, nullptr, nullptr, out, nullptr}, stream); });

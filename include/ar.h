@@ -800,6 +800,18 @@ ar_status_t ar_muon_plan_set_scales(ar_muon_plan_t *plan, const double *scales);
 ar_status_t ar_muon_plan_prepare(ar_muon_plan_t *plan);
 ar_muon_stats_t ar_muon_plan_stats(const ar_muon_plan_t *plan);
 /*
+ * The work of one product of an iteration (0: X X^T, 1: b A + c A A + a I, 2:
+ * B X) of a plan of more than one launch.  *tile = rows and columns of its
+ * tiles.  Per item, in the order in which a workgroup does its own: the
+ * workgroup, the matrix, the tile's row and column, the contraction elements
+ * [k0, k1), and the partial tile that the item's sums go to: -1 where the item
+ * is a whole tile; otherwise a second launch adds the tile's partial tiles in
+ * ascending order.  Returns the number of items (writes at most cap), 0 for a
+ * plan of one launch, -1 on error.  Any out pointer may be NULL.  Host only.
+ */
+int64_t ar_muon_plan_work(const ar_muon_plan_t *plan, int product, int32_t *tile, int32_t *group, int32_t *matrix,
+                          int32_t *row, int32_t *col, int32_t *k0, int32_t *k1, int32_t *slot, int64_t cap);
+/*
  * out = Newton-Schulz of every matrix of grads.  out overlaps grads only if
  * both are the same pointer and of one type (in place).  Calls of one plan
  * share its workspace: they must not overlap in time, nor with replays of

@@ -2,6 +2,7 @@
 update on a host without a GPU: every bad call is turned away before any
 device work."""
 import ctypes
+import random
 
 import pytest
 import torch
@@ -216,3 +217,84 @@ def test_c_struct_sizes():
     assert ctypes.sizeof(B.ar_experts_stats_t) == 56
     assert ctypes.sizeof(B.ar_muon_stats_t) == 48
     assert ctypes.sizeof(B.ar_muon_params_t) == 40
+
+
+# ------------------------------------------------------ Muon work lists
+
+SPLIT, WHOLE = True, False
+# matrices, and per product (X X^T, b A + c A A + a I, B X) the tile and whether tiles are cut; what the GPU tests
+# of the tiled kernels run
+TILED = {
+    "small": ([(160, 224), (300, 200), (131, 517), (5, 3)], [(64, WHOLE), (64, WHOLE), (64, WHOLE)]),
+    "wide": ([(1000, 4100)], [(64, WHOLE), (64, WHOLE), (128, WHOLE)]),
+    "tall": ([(2100, 1990)], [(256, SPLIT), (128, WHOLE), (128, WHOLE)]),
+    "equal": ([(1024, 2048)] * 8, [(128, WHOLE), (128, WHOLE), (256, WHOLE)]),
+    "large": ([(2050, 2060)] * 2 + [(2061, 2049)] * 2, [(256, WHOLE), (256, WHOLE), (256, SPLIT)]),
+    "square": ([(4001, 4100)], [(256, SPLIT), (256, SPLIT), (256, SPLIT)]),
+    "long": ([(300, 5000)] * 3 + [(5001, 299)] * 3, [(256, SPLIT), (64, WHOLE), (256, WHOLE)]),
+    "mixed": ([(4000, 520), (520, 4000), (1001, 1003), (64, 64), (2049, 2047)],
+              [(256, SPLIT), (128, WHOLE), (128, WHOLE)]),
+}
+
+
+def check_work(shapes, plan):
+    """Every tile of every matrix (the upper triangle's of the square products) is covered exactly once along its
+    contraction; whole tiles have no partial tile, the pieces of the others have consecutive ones of their own."""
+    seen = []
+    for product in range(3):
+        w = B.ar_muon_plan_work(plan, product)
+        side, tiles, slots = w["tile"], {}, []
+        assert (w["group"][1:] >= w["group"][:-1]).all() and (w["k1"] > w["k0"]).all()
+        for mat, r, c, k0, k1, slot in zip(*(w[k].tolist() for k in ("matrix", "row", "col", "k0", "k1", "slot"))):
+            tiles.setdefault((mat, r, c), []).append((slot, k0, k1))
+        want = set()
+        for i, (rows, cols) in enumerate(shapes):
+            m, n = (-(-v // 64) * 64 for v in sorted((rows, cols)))
+            if m == 0:
+                continue
+            up, across = -(-m // side), -(-(m if product < 2 else n) // side)
+            mine = {(i, r, c) for r in range(up) for c in range(r if product < 2 else 0, across)}
+            want |= mine
+            for t in mine:
+                pieces = sorted(tiles[t])
+                ranges = sorted((k0, k1) for _, k0, k1 in pieces)
+                assert ranges[0][0] == 0 and ranges[-1][1] == (n if product == 0 else m)
+                assert all(a[1] == b[0] for a, b in zip(ranges, ranges[1:]))
+                assert all(k0 % 64 == 0 and k1 % 64 == 0 for k0, k1 in ranges)
+                s = [p[0] for p in pieces]
+                assert s == [-1] if len(s) == 1 else s == list(range(s[0], s[0] + len(s))) and s[0] >= 0
+                slots += s if len(s) > 1 else []
+        assert set(tiles) == want
+        assert sorted(slots) == list(range(len(slots)))
+        seen.append((side, len(slots) > 0))
+    return seen
+
+
+@pytest.mark.parametrize("name", TILED)
+@pytest.mark.parametrize("types", [("bf16", "fp32"), ("bf16", "bf16")])
+def test_muon_work_lists(name, types):
+    shapes, want = TILED[name]
+    p = B.ar_muon_plan_create(shapes, *types)
+    assert check_work(shapes, p) == want
+    s = B.ar_muon_plan_stats(p)
+    assert s["launches"] == 2 + 5 * (3 + sum(split for _, split in want))
+    B.ar_muon_plan_destroy(p)
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_muon_work_lists_of_drawn_matrices(seed):
+    rng = random.Random(seed)
+    shapes = [(int(2 ** rng.uniform(0, 12.5)), int(2 ** rng.uniform(0, 12.5))) for _ in range(rng.randint(1, 9))]
+    shapes += [(0, 7), (257, 300)]
+    p = B.ar_muon_plan_create(shapes, "fp32", "fp32")
+    check_work(shapes, p)
+    B.ar_muon_plan_destroy(p)
+
+
+def test_muon_work_of_small_plans_and_refusals(muon):
+    for product in range(3):
+        w = B.ar_muon_plan_work(muon, product)
+        assert w["tile"] == 0 and len(w["group"]) == 0
+    refused(B.AR_ERR_INVALID_ARG, B.ar_muon_plan_work, muon, 3)
+    refused(B.AR_ERR_INVALID_ARG, B.ar_muon_plan_work, muon, -1)
+    refused(B.AR_ERR_INVALID_ARG, B.ar_muon_plan_work, None, 0)
