@@ -19,7 +19,7 @@ from ._binding import (  # noqa: F401
     ar_plan_launch_scratch, ar_plan_launch_times, ar_plan_num_launches, ar_plan_owned_range, ar_plan_prepare,
     ar_plan_set_cache_bytes, ar_plan_set_exec, ar_plan_set_graph, ar_plan_set_profiling,
     ar_plan_set_profiling_period, ar_plan_stats, ar_plan_transfers, ar_reduce_scatter, ar_select_schedule,
-    ar_experts_create, ar_experts_destroy, ar_experts_forward, ar_experts_input_grad, ar_experts_prepare,
-    ar_experts_stats, ar_experts_weight_grad, ar_muon_plan_create, ar_muon_plan_destroy, ar_muon_plan_prepare,
+    ar_experts_create, ar_experts_destroy, ar_experts_forward, ar_experts_input_grad, ar_experts_launch_shape,
+    ar_experts_prepare, ar_experts_stats, ar_experts_weight_grad, ar_muon_plan_create, ar_muon_plan_destroy, ar_muon_plan_prepare,
     ar_muon_plan_set_iterations, ar_muon_plan_set_scales, ar_muon_plan_stats, ar_muon_plan_work, ar_muon_step, ar_orthogonalize,
 )

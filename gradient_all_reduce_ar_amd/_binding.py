@@ -163,6 +163,7 @@ def _declare(L):
         "ar_experts_create": ([ctypes.c_int, sz, sz, ctypes.c_int, ctypes.c_int, psz], P),
         "ar_experts_prepare": ([P], ctypes.c_int),
         "ar_experts_stats": ([P], ar_experts_stats_t),
+        "ar_experts_launch_shape": ([P, ctypes.c_int, sz, ctypes.c_int, pi32, pi32, pi32], ctypes.c_int),
         "ar_experts_forward": ([P, P, sz, P, P, sz, P, sz, P], ctypes.c_int),
         "ar_experts_input_grad": ([P, P, sz, P, P, sz, P, sz, P], ctypes.c_int),
         "ar_experts_weight_grad": ([P, P, sz, P, sz, P, ctypes.c_int, P, sz, P], ctypes.c_int),
@@ -767,6 +768,9 @@ def _ends(info, ends):
     return ends.data_ptr()
 
 
+EXPERT_PRODUCTS = {"forward": 0, "input_grad": 1, "weight_grad": 2}
+
+
 def ar_experts_create(nexperts, in_features, out_features, dtype, grad_dtype=None, weight_offsets=None):
     """dtype, grad_dtype: "fp32" or "bf16" (grad_dtype None: dtype); weight_offsets: first element of each
     expert's [out_features, in_features] matrix in its arena (None: back to back)."""
@@ -789,6 +793,14 @@ def ar_experts_prepare(plan):
 def ar_experts_stats(plan):
     s = lib().ar_experts_stats(plan)
     return {k: getattr(s, k) for k, _ in s._fields_}
+
+
+def ar_experts_launch_shape(plan, product, ntokens, aligned=True):
+    """dict(tile_rows, tile_cols, parts) of a product ("forward", "input_grad" or "weight_grad") of ntokens rows."""
+    v = [ctypes.c_int32() for _ in range(3)]
+    _check(lib().ar_experts_launch_shape(plan, _code(EXPERT_PRODUCTS, product), int(ntokens), 1 if aligned else 0,
+                                         *[ctypes.byref(x) for x in v]))
+    return dict(zip(("tile_rows", "tile_cols", "parts"), [x.value for x in v]))
 
 
 def _experts_of(plan):

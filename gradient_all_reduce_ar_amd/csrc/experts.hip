@@ -503,27 +503,40 @@ double rows_time(const ExpertArgs &a, const TileCost &c) {
   return rounds * (std::ceil(steps) * (tiles <= 256 ? c.alone : c.full) + c.rest);
 }
 
+// What a call launches: the tiles above, or experts_few.
+enum Choice { kBig, kSquare, kHalf, kSmall, kFew };
+
 template <bool GRAD>
-hipError_t rows(const ExpertArgs &a, hipStream_t s) {
-  const int64_t e = a.experts;
+Choice rows_choice(const ExpertArgs &a) {
   if constexpr (!GRAD) {
     // Short decoding calls, where latency counts: up to 16 MiB of weights (one
     // token, 8 experts, 1024 x 512: 4.9 us, with Small 9.9; from 250 MB on
     // Small reads faster, 53 us against 62).
-    const int64_t bytes = std::min(e, a.tokens) * a.in * a.outf * (a.bf16 ? 2 : 4);
-    if (a.tokens <= 16 * e && bytes <= 16 << 20) {
-      const int64_t grid = (a.tokens / kFewRows + std::min(e, a.tokens)) * ((a.outf + kFewCols - 1) / kFewCols);
-      return a.bf16 ? launch(experts_few<true>, grid, 1, 64 * kFewWaves, 0, s, a)
-                    : launch(experts_few<false>, grid, 1, 64 * kFewWaves, 0, s, a);
-    }
+    const int64_t e = a.experts, bytes = std::min(e, a.tokens) * a.in * a.outf * (a.bf16 ? 2 : 4);
+    if (a.tokens <= 16 * e && bytes <= 16 << 20) return kFew;
   }
   const TileCost *c = a.bf16 ? kBF16Cost : kF32Cost;
   const double big = a.aligned && a.bf16 ? rows_time<Big, GRAD>(a, c[0]) : 1e300;
   const double square = rows_time<Square, GRAD>(a, c[1]), half = rows_time<Half, GRAD>(a, c[2]);
   const double small = rows_time<Small, GRAD>(a, c[3]);
-  if (big <= std::min({square, half, small})) return launch_rows<Big, GRAD>(a, s);
-  if (square <= std::min(half, small)) return launch_rows<Square, GRAD>(a, s);
-  return half <= small ? launch_rows<Half, GRAD>(a, s) : launch_rows<Small, GRAD>(a, s);
+  if (big <= std::min({square, half, small})) return kBig;
+  if (square <= std::min(half, small)) return kSquare;
+  return half <= small ? kHalf : kSmall;
+}
+
+template <bool GRAD>
+hipError_t rows(const ExpertArgs &a, hipStream_t s) {
+  switch (rows_choice<GRAD>(a)) {
+    case kBig: return launch_rows<Big, GRAD>(a, s);
+    case kSquare: return launch_rows<Square, GRAD>(a, s);
+    case kHalf: return launch_rows<Half, GRAD>(a, s);
+    case kSmall: return launch_rows<Small, GRAD>(a, s);
+    case kFew: break;
+  }
+  if constexpr (GRAD) return hipErrorInvalidValue;  // not chosen
+  const int64_t grid = (a.tokens / kFewRows + std::min<int64_t>(a.experts, a.tokens)) * ((a.outf + kFewCols - 1) / kFewCols);
+  return a.bf16 ? launch(experts_few<true>, grid, 1, 64 * kFewWaves, 0, s, a)
+                : launch(experts_few<false>, grid, 1, 64 * kFewWaves, 0, s, a);
 }
 
 template <class S>
@@ -536,15 +549,20 @@ int64_t weight_tiles(const ExpertArgs &a) {
 constexpr int64_t kMaxSlots = 512, kMaxParts = 16, kPartRows = 256;
 int64_t most_parts(int64_t tiles) { return tiles <= 0 ? 1 : std::clamp<int64_t>(kMaxSlots / tiles, 1, kMaxParts); }
 
+// Parts of the rows of a launch of Half's tiles: 8001 rows of one expert, 512 x
+// 768 (48 tiles): 73 us whole, 26 us in parts; 16000, 2, 1024 x 1024 (256
+// tiles): 96 and 71.
+int64_t weight_parts(const ExpertArgs &a) {
+  return a.slots ? std::max<int64_t>(1, std::min(most_parts(weight_tiles<Half>(a)), a.tokens / a.experts / kPartRows)) : 1;
+}
+
 template <Elem E, class S, bool GBF, bool ALIGNED>
 hipError_t launch_weights(const ExpertArgs &a, hipStream_t s) {
   using P = TileProduct<E, S, kMajorMN, kMajorMN, ALIGNED>;
   const int64_t tiles = weight_tiles<S>(a);
   if constexpr (S::BM * S::BN == kExpertSlot) {
-    // 8001 rows of one expert, 512 x 768 (48 tiles): 73 us whole, 26 us in
-    // parts; 16000, 2, 1024 x 1024 (256 tiles): 96 and 71
-    const int64_t parts = std::min(most_parts(tiles), a.tokens / a.experts / kPartRows);
-    if (parts > 1 && a.slots) {
+    const int64_t parts = weight_parts(a);
+    if (parts > 1) {
       const LaunchEvents ev = t_launch_events;  // the call's mark goes on its last kernel
       t_launch_events = LaunchEvents{};
       const hipError_t e =
@@ -563,11 +581,6 @@ hipError_t launch_weights_of(const ExpertArgs &a, hipStream_t s) {
   else return a.grad_bf16 ? launch_weights<E, S, true, ALIGNED>(a, s) : launch_weights<E, S, false, ALIGNED>(a, s);
 }
 
-}  // namespace
-
-hipError_t experts_forward(const ExpertArgs &a, hipStream_t s) { return rows<false>(a, s); }
-hipError_t experts_input_grad(const ExpertArgs &a, hipStream_t s) { return rows<true>(a, s); }
-
 // Big where its tiles give every CU one and an expert's rows fill a few
 // steps; Half where Square's would leave CUs idle, for fp32, and for operands
 // that are not aligned if the rows are few.  Microseconds Big / Square / Half
@@ -580,13 +593,44 @@ hipError_t experts_input_grad(const ExpertArgs &a, hipStream_t s) { return rows<
 //   515, 24, 1025 x 511:              - / 18.6 / 16.6
 //   fp32, 8192, 4, 2048 x 2048:       - / 505 / 508
 //   fp32, 8192, 4, 2047 x 2047:       - / 600 / 608
-hipError_t experts_weight_grad(const ExpertArgs &a, hipStream_t s) {
+Choice weight_choice(const ExpertArgs &a) {
   const bool fill = a.tokens >= 256 * static_cast<int64_t>(a.experts);
-  if (a.bf16 && a.aligned && fill && weight_tiles<Big>(a) >= 256) return launch_weights_of<kBF16, Big, true>(a, s);
+  if (!a.bf16) return kHalf;
+  if (a.aligned && fill && weight_tiles<Big>(a) >= 256) return kBig;
+  return weight_tiles<Square>(a) < 256 || (!a.aligned && !fill) ? kHalf : kSquare;
+}
+
+template <class S>
+ExpertShape shape_of(int64_t parts = 1) {
+  return {S::BM, S::BN, static_cast<int32_t>(parts)};
+}
+
+}  // namespace
+
+hipError_t experts_forward(const ExpertArgs &a, hipStream_t s) { return rows<false>(a, s); }
+hipError_t experts_input_grad(const ExpertArgs &a, hipStream_t s) { return rows<true>(a, s); }
+
+hipError_t experts_weight_grad(const ExpertArgs &a, hipStream_t s) {
+  const Choice c = weight_choice(a);
   if (!a.bf16) return a.aligned ? launch_weights_of<kF32, Half, true>(a, s) : launch_weights_of<kF32, Half, false>(a, s);
-  if (weight_tiles<Square>(a) < 256 || (!a.aligned && !fill))
+  if (c == kBig) return launch_weights_of<kBF16, Big, true>(a, s);
+  if (c == kHalf)
     return a.aligned ? launch_weights_of<kBF16, Half, true>(a, s) : launch_weights_of<kBF16, Half, false>(a, s);
   return a.aligned ? launch_weights_of<kBF16, Square, true>(a, s) : launch_weights_of<kBF16, Square, false>(a, s);
+}
+
+ExpertShape experts_shape(const ExpertArgs &a, ExpertProduct product) {
+  const Choice c = product == kExpertsForward     ? rows_choice<false>(a)
+                   : product == kExpertsInputGrad ? rows_choice<true>(a)
+                                                  : weight_choice(a);
+  switch (c) {
+    case kBig: return shape_of<Big>();
+    case kSquare: return shape_of<Square>();
+    case kHalf: return shape_of<Half>(product == kExpertsWeightGrad ? weight_parts(a) : 1);
+    case kSmall: return shape_of<Small>();
+    case kFew: break;
+  }
+  return {kFewRows, kFewCols, 1};
 }
 
 int64_t experts_weight_slots(int64_t experts, int64_t in, int64_t outf) {

@@ -171,9 +171,31 @@ ar_status_t check_rows(const RowsArg &r, int64_t rows, int64_t elem, int64_t *by
   return AR_OK;
 }
 
-enum Which { kForward, kInputGrad, kWeightGrad };
+using ar_dev::ExpertProduct;
+using ar_dev::kExpertsForward;
+using ar_dev::kExpertsInputGrad;
+using ar_dev::kExpertsWeightGrad;
 
-ar_status_t run(ar_experts *ex, Which which, const RowsArg &r1, const RowsArg &r2, const void *arena, bool out_is_rows,
+// What every call of a plan has, and whether its rows and (in the products
+// that read the weights) matrices let it read 16 bytes at a time if all
+// pointers and strides do: 16-byte rows; and offsets inside a tile of 256 rows
+// fit into 31 bits.
+size_t far_stride(const ar_experts *ex) { return (size_t{1} << 23) / (ex->bf16 ? 2 : 4); }
+ar_dev::ExpertArgs call_args(const ar_experts *ex, ExpertProduct which, int64_t tokens) {
+  ar_dev::ExpertArgs a{};
+  a.tokens = tokens;
+  a.in = ex->in;
+  a.outf = ex->out;
+  a.experts = ex->nexperts;
+  a.bf16 = ex->bf16;
+  a.grad_bf16 = ex->grad_bf16;
+  const int64_t vec = ex->bf16 ? 8 : 4;
+  a.aligned = ex->in % vec == 0 && ex->out % vec == 0 && static_cast<size_t>(ex->in) <= far_stride(ex) &&
+              (which == kExpertsWeightGrad || ex->offsets_by_8);
+  return a;
+}
+
+ar_status_t run(ar_experts *ex, ExpertProduct which, const RowsArg &r1, const RowsArg &r2, const void *arena, bool out_is_rows,
                 bool accumulate, const int32_t *ends, size_t ntokens, void *stream) {
   if (ntokens > kMaxTokens) return fail(AR_ERR_INVALID_ARG, "more than 2^31 - 65536 tokens");
   const int64_t t = static_cast<int64_t>(ntokens), elem = ex->bf16 ? 2 : 4;
@@ -181,8 +203,8 @@ ar_status_t run(ar_experts *ex, Which which, const RowsArg &r1, const RowsArg &r
   ar_status_t st = check_rows(r1, t, elem, &b1);
   if (st == AR_OK) st = check_rows(r2, t, elem, &b2);
   if (st != AR_OK) return st;
-  const int64_t aelem = which == kWeightGrad ? (ex->grad_bf16 ? 2 : 4) : elem;
-  if (t > 0 || which == kWeightGrad) {
+  const int64_t aelem = which == kExpertsWeightGrad ? (ex->grad_bf16 ? 2 : 4) : elem;
+  if (t > 0 || which == kExpertsWeightGrad) {
     if (!ends) return fail(AR_ERR_INVALID_ARG, "ends is NULL");
     if (!on(ends, 4)) return fail(AR_ERR_INVALID_ARG, "ends is not aligned to its elements");
     if (!arena) return fail(AR_ERR_INVALID_ARG, "the weight arena is NULL");
@@ -195,46 +217,37 @@ ar_status_t run(ar_experts *ex, Which which, const RowsArg &r1, const RowsArg &r
   if (!ex->d_offsets) st = ar_host::refuse_capture(static_cast<hipStream_t>(stream));
   if (st == AR_OK) st = prepare(ex);
   if (st != AR_OK) return st;
-  if (t == 0 && which != kWeightGrad) return AR_OK;
-  ar_dev::ExpertArgs a{};
+  if (t == 0 && which != kExpertsWeightGrad) return AR_OK;
+  ar_dev::ExpertArgs a = call_args(ex, which, t);
   a.offsets = static_cast<const int64_t *>(ex->d_offsets);
   a.slots = static_cast<float *>(ex->d_slots);
   a.ends = ends;
-  a.tokens = t;
-  a.in = ex->in;
-  a.outf = ex->out;
-  a.experts = ex->nexperts;
-  a.bf16 = ex->bf16;
-  a.grad_bf16 = ex->grad_bf16;
   a.accumulate = accumulate;
-  // 16-byte rows; and offsets inside a tile of 256 rows fit into 31 bits
-  const size_t vec = static_cast<size_t>(16 / elem), far = (size_t{1} << 23) / elem;
+  const size_t vec = static_cast<size_t>(16 / elem), far = far_stride(ex);
   auto rows16 = [&](const RowsArg &r) { return on(r.p, 16) && r.stride % vec == 0 && r.stride <= far; };
-  const bool by16 = static_cast<size_t>(ex->in) % vec == 0 && static_cast<size_t>(ex->out) % vec == 0 &&
-                    static_cast<size_t>(ex->in) <= far;
-  if (which == kWeightGrad) {
+  if (which == kExpertsWeightGrad) {
     a.x = r1.p;
     a.xs = static_cast<int64_t>(r1.stride);
     a.dy = r2.p;
     a.dys = static_cast<int64_t>(r2.stride);
     a.out = const_cast<void *>(arena);
-    a.aligned = rows16(r1) && rows16(r2) && by16;
+    a.aligned = a.aligned && rows16(r1) && rows16(r2);
   } else {
     a.w = arena;
     a.out = const_cast<void *>(r2.p);
     a.outs = static_cast<int64_t>(r2.stride);
-    (which == kForward ? a.x : a.dy) = r1.p;
-    (which == kForward ? a.xs : a.dys) = static_cast<int64_t>(r1.stride);
-    a.aligned = rows16(r1) && on(arena, 16) && ex->offsets_by_8 && by16;
+    (which == kExpertsForward ? a.x : a.dy) = r1.p;
+    (which == kExpertsForward ? a.xs : a.dys) = static_cast<int64_t>(r1.stride);
+    a.aligned = a.aligned && rows16(r1) && on(arena, 16);
   }
   hipStream_t s = static_cast<hipStream_t>(stream);
   hipEvent_t mark = nullptr;
   st = ex->marks.of(s, &mark);
   if (st != AR_OK) return st;
   ar_dev::t_launch_events = ar_dev::LaunchEvents{nullptr, mark};
-  const hipError_t e = which == kForward     ? ar_dev::experts_forward(a, s)
-                       : which == kInputGrad ? ar_dev::experts_input_grad(a, s)
-                                             : ar_dev::experts_weight_grad(a, s);
+  const hipError_t e = which == kExpertsForward     ? ar_dev::experts_forward(a, s)
+                       : which == kExpertsInputGrad ? ar_dev::experts_input_grad(a, s)
+                                                    : ar_dev::experts_weight_grad(a, s);
   ar_dev::t_launch_events = ar_dev::LaunchEvents{};
   if (e == hipErrorInvalidConfiguration)
     return fail(AR_ERR_UNSUPPORTED, "expert product larger than one launch grid");
@@ -834,11 +847,32 @@ ar_experts_stats_t ar_experts_stats(const ar_experts_t *ex) {
   return s;
 }
 
+ar_status_t ar_experts_launch_shape(const ar_experts_t *ex, int product, size_t ntokens, int aligned,
+                                    int32_t *tile_rows, int32_t *tile_cols, int32_t *parts) {
+  if (!ex) return fail(AR_ERR_INVALID_ARG, "expert plan is NULL");
+  if (product < kExpertsForward || product > kExpertsWeightGrad)
+    return fail(AR_ERR_INVALID_ARG, "product must be from 0 to 2");
+  if (ntokens > kMaxTokens) return fail(AR_ERR_INVALID_ARG, "more than 2^31 - 65536 tokens");
+  const ExpertProduct which = static_cast<ExpertProduct>(product);
+  ar_dev::ExpertShape s{0, 0, 0};
+  if (ntokens > 0 || which == kExpertsWeightGrad) {
+    float any = 0;
+    ar_dev::ExpertArgs a = call_args(ex, which, static_cast<int64_t>(ntokens));
+    a.aligned = a.aligned && aligned;
+    a.slots = ex->slot_bytes > 0 ? &any : nullptr;  // is there a workspace
+    s = ar_dev::experts_shape(a, which);
+  }
+  if (tile_rows) *tile_rows = s.rows;
+  if (tile_cols) *tile_cols = s.cols;
+  if (parts) *parts = s.parts;
+  return AR_OK;
+}
+
 ar_status_t ar_experts_forward(ar_experts_t *ex, const void *x, size_t x_stride, const void *weights, void *y,
                                size_t y_stride, const int32_t *ends, size_t ntokens, void *stream) {
   if (!ex) return fail(AR_ERR_INVALID_ARG, "expert plan is NULL");
   return guarded([&] {
-    return run(ex, kForward, {x, x_stride, ex->in, "x"}, {y, y_stride, ex->out, "y"}, weights, true, false, ends,
+    return run(ex, kExpertsForward, {x, x_stride, ex->in, "x"}, {y, y_stride, ex->out, "y"}, weights, true, false, ends,
                ntokens, stream);
   });
 }
@@ -847,7 +881,7 @@ ar_status_t ar_experts_input_grad(ar_experts_t *ex, const void *dy, size_t dy_st
                                   size_t dx_stride, const int32_t *ends, size_t ntokens, void *stream) {
   if (!ex) return fail(AR_ERR_INVALID_ARG, "expert plan is NULL");
   return guarded([&] {
-    return run(ex, kInputGrad, {dy, dy_stride, ex->out, "dy"}, {dx, dx_stride, ex->in, "dx"}, weights, true, false,
+    return run(ex, kExpertsInputGrad, {dy, dy_stride, ex->out, "dy"}, {dx, dx_stride, ex->in, "dx"}, weights, true, false,
                ends, ntokens, stream);
   });
 }
@@ -856,7 +890,7 @@ ar_status_t ar_experts_weight_grad(ar_experts_t *ex, const void *x, size_t x_str
                                    void *grads, int accumulate, const int32_t *ends, size_t ntokens, void *stream) {
   if (!ex) return fail(AR_ERR_INVALID_ARG, "expert plan is NULL");
   return guarded([&] {
-    return run(ex, kWeightGrad, {x, x_stride, ex->in, "x"}, {dy, dy_stride, ex->out, "dy"}, grads, false,
+    return run(ex, kExpertsWeightGrad, {x, x_stride, ex->in, "x"}, {dy, dy_stride, ex->out, "dy"}, grads, false,
                accumulate != 0, ends, ntokens, stream);
   });
 }

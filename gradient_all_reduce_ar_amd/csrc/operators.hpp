@@ -30,6 +30,13 @@ struct ExpertArgs {
 hipError_t experts_forward(const ExpertArgs &a, hipStream_t s);
 hipError_t experts_input_grad(const ExpertArgs &a, hipStream_t s);
 hipError_t experts_weight_grad(const ExpertArgs &a, hipStream_t s);
+// Rows and columns of the tiles of the product that such a call launches, and
+// the parts that a weight gradient's rows are cut into.
+enum ExpertProduct { kExpertsForward, kExpertsInputGrad, kExpertsWeightGrad };
+struct ExpertShape {
+  int32_t rows, cols, parts;
+};
+ExpertShape experts_shape(const ExpertArgs &a, ExpertProduct product);
 // Partial tiles, of kExpertSlot sums, that the weight gradient of such experts
 // may use: 0 where its tiles are enough for the device.
 int64_t experts_weight_slots(int64_t experts, int64_t in, int64_t outf);

@@ -698,14 +698,25 @@ ar_experts_t *ar_experts_create(int nexperts, size_t in_features, size_t out_fea
 ar_status_t ar_experts_prepare(ar_experts_t *plan);
 ar_experts_stats_t ar_experts_stats(const ar_experts_t *plan);
 /*
+ * Kernel shape of a product (0: forward, 1: input_grad, 2: weight_grad) of
+ * ntokens rows, with all pointers and strides on 16 bytes (aligned != 0) or
+ * not: rows and columns of the result that a workgroup makes, and the parts
+ * that weight_grad cuts each expert's rows into (more than 1: its calls use
+ * the plan's workspace).  Zeros where nothing is launched.  Any out pointer
+ * may be NULL.  Host only.
+ */
+ar_status_t ar_experts_launch_shape(const ar_experts_t *plan, int product, size_t ntokens, int aligned,
+                                    int32_t *tile_rows, int32_t *tile_cols, int32_t *parts);
+/*
  * The products.  Row strides are in elements (at least the features, at most
  * 2^22); pointers are aligned to their elements (the fast path needs rows
  * and matrices that start on 16 bytes, and feature counts that are multiples
  * of 16 bytes).  The output overlaps no input.  forward and input_grad use no
  * workspace: calls of one plan may be in flight together on several streams,
  * captured or not.  weight_grad may (few experts of few features, many rows:
- * the rows are cut into parts whose sums are added in a fixed order): no two
- * of one plan may overlap in time, replays of captured ones included.
+ * the rows are cut into parts whose sums are added in a fixed order;
+ * ar_experts_launch_shape tells): no two of one plan that do may overlap in
+ * time, replays of captured ones included.
  * ntokens: up to 2^31 - 65536; 0: forward and input_grad do nothing (but
  * prepare the plan).  AR_ERR_INVALID_ARG for bad
  * arguments or another device than the plan's; AR_ERR_UNSUPPORTED for a

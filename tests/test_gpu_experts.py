@@ -11,6 +11,7 @@ import pytest
 import torch
 
 from gradient_all_reduce_ar_amd import _binding as B
+from tests.test_operators_cpu import ROWS_OF_DISPATCH, launch_shapes
 
 DEV = "cuda:0"
 T = {"fp32": torch.float32, "bf16": torch.bfloat16}
@@ -367,3 +368,25 @@ def test_refusals_on_the_device():
         with pytest.raises(ValueError):
             B.ar_experts_forward(c.plan, a["x"], a["w"], a["y"], a["ends"])
     B.ar_experts_destroy(c.plan)
+
+
+def ragged(experts, tokens, seed=0):
+    """Rows of each expert: some none, some one, the rest uneven."""
+    rng = np.random.default_rng(seed)
+    share = rng.dirichlet(np.full(experts, 0.7))
+    counts = np.floor(share * tokens).astype(np.int64)
+    counts[int(rng.integers(experts))] += tokens - counts.sum()
+    return [int(c) for c in counts]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,inf,outf,experts,tokens,forward,input_grad,weight_grad,parts", ROWS_OF_DISPATCH)
+def test_every_tile(dtype, inf, outf, experts, tokens, forward, input_grad, weight_grad, parts):
+    """Every tile that a size of a type can take, with ragged experts and edges; the plan says that it is taken."""
+    print("case", dtype, inf, outf, experts, tokens, flush=True)
+    for grad in ("fp32", "bf16") if dtype == "bf16" else ("fp32",):
+        c = Case(inf, outf, ragged(experts, tokens), dtype, grad)
+        assert launch_shapes(c.plan, tokens, True) == [forward, input_grad, weight_grad, parts]
+        c.check_all()
+        c = Case(inf, outf, ragged(experts, tokens - 7, 1), dtype, grad, extra=7, pad=(8, 16), seed=1)
+        c.check_all()

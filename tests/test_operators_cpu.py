@@ -298,3 +298,80 @@ def test_muon_work_of_small_plans_and_refusals(muon):
     refused(B.AR_ERR_INVALID_ARG, B.ar_muon_plan_work, muon, 3)
     refused(B.AR_ERR_INVALID_ARG, B.ar_muon_plan_work, muon, -1)
     refused(B.AR_ERR_INVALID_ARG, B.ar_muon_plan_work, None, 0)
+
+
+# ------------------------------------------- which tiles a product takes
+
+# in, out, experts, rows, type: the tile of forward, input gradient and weight gradient, and its parts; what the GPU
+# tests of the products' kernels run.  The features of a type's second half are on no vector boundary.
+DISPATCH = {
+    "bf16": [
+        (4104, 1032, 8, 1500, (64, 128), (256, 256), (128, 128), 1),
+        (1000, 1200, 40, 4100, (256, 256), (64, 128), (128, 128), 1),
+        (520, 264, 1, 6000, (128, 128), (128, 128), (64, 128), 16),
+        (2048, 1408, 40, 40, (64, 128), (64, 128), (128, 128), 1),
+        (136, 72, 1, 8200, (32, 64), (64, 128), (64, 128), 16),
+        (520, 264, 40, 2500, (32, 64), (128, 128), (128, 128), 1),
+        (2056, 1000, 8, 2500, (128, 128), (64, 128), (256, 256), 1),
+        (521, 263, 1, 6000, (128, 128), (128, 128), (64, 128), 16),
+        (2047, 1409, 40, 40, (64, 128), (64, 128), (64, 128), 1),
+        (135, 71, 1, 8200, (32, 64), (64, 128), (64, 128), 16),
+        (521, 263, 40, 2500, (32, 64), (128, 128), (64, 128), 1),
+        (1025, 1001, 8, 2500, (128, 128), (128, 128), (128, 128), 1),
+        (2049, 2047, 3, 4000, (64, 128), (64, 128), (128, 128), 1),
+    ],
+    "fp32": [
+        (1000, 1200, 8, 2500, (128, 128), (32, 64), (64, 128), 1),
+        (1000, 1200, 1, 1500, (64, 128), (32, 64), (64, 128), 3),
+        (520, 264, 40, 6000, (32, 64), (64, 128), (64, 128), 1),
+        (136, 72, 1, 8200, (32, 64), (128, 128), (64, 128), 16),
+        (1001, 1201, 8, 2500, (128, 128), (32, 64), (64, 128), 1),
+        (1001, 1201, 1, 1500, (64, 128), (32, 64), (64, 128), 3),
+        (521, 263, 40, 6000, (32, 64), (64, 128), (64, 128), 1),
+        (135, 71, 1, 8200, (32, 64), (128, 128), (64, 128), 16),
+    ],
+}
+ROWS_OF_DISPATCH = [(dtype, *row) for dtype in DISPATCH for row in DISPATCH[dtype]]
+
+
+def launch_shapes(plan, tokens, aligned):
+    s = [B.ar_experts_launch_shape(plan, p, tokens, aligned) for p in ("forward", "input_grad", "weight_grad")]
+    return [(v["tile_rows"], v["tile_cols"]) for v in s] + [s[2]["parts"]]
+
+
+@pytest.mark.parametrize("dtype,inf,outf,experts,tokens,forward,input_grad,weight_grad,parts", ROWS_OF_DISPATCH)
+def test_experts_launch_shapes(dtype, inf, outf, experts, tokens, forward, input_grad, weight_grad, parts):
+    p = B.ar_experts_create(experts, inf, outf, dtype, "fp32")
+    assert launch_shapes(p, tokens, True) == [forward, input_grad, weight_grad, parts]
+    B.ar_experts_destroy(p)
+
+
+def test_every_kernel_of_the_products_is_run():
+    """The tests' sizes take every tile of every type, with and without whole vectors, that any size takes."""
+    def taken(dtype, inf, outf, experts, tokens, aligned):
+        p = B.ar_experts_create(experts, inf, outf, dtype, "fp32")
+        shapes = launch_shapes(p, tokens, aligned)
+        B.ar_experts_destroy(p)
+        vec = 8 if dtype == "bf16" else 4
+        shapes[2] += (shapes.pop() > 1,)
+        return {(dtype, aligned and inf % vec == 0 and outf % vec == 0, k, s) for k, s in enumerate(shapes)}
+
+    few = [("bf16", 64, 64, 4, 4), ("fp32", 64, 64, 4, 4), ("bf16", 71, 135, 4, 4), ("fp32", 71, 135, 4, 4),
+           ("bf16", 64, 64, 1, 40), ("fp32", 64, 64, 1, 40), ("bf16", 71, 135, 1, 40), ("fp32", 71, 135, 1, 40)]
+    run = set().union(*(taken(*r[:5], True) for r in ROWS_OF_DISPATCH + few))
+    rng = random.Random(7)
+    for _ in range(1500):
+        inf, outf, tokens = (int(2 ** rng.uniform(0, top)) for top in (13, 13, 15))
+        if rng.random() < 0.7:
+            inf, outf = max(8, inf // 8 * 8), max(8, outf // 8 * 8)
+        any_size = taken(rng.choice(["bf16", "fp32"]), inf, outf, int(2 ** rng.uniform(0, 8)), tokens, rng.random() < 0.7)
+        assert any_size <= run, any_size - run
+
+
+def test_experts_launch_shape_refusals_and_nothing(experts):
+    assert B.ar_experts_launch_shape(experts, "forward", 0) == dict(tile_rows=0, tile_cols=0, parts=0)
+    assert B.ar_experts_launch_shape(experts, "weight_grad", 0)["parts"] == 1
+    refused(B.AR_ERR_INVALID_ARG, B.ar_experts_launch_shape, experts, 3, 8)
+    refused(B.AR_ERR_INVALID_ARG, B.ar_experts_launch_shape, experts, -1, 8)
+    refused(B.AR_ERR_INVALID_ARG, B.ar_experts_launch_shape, None, 0, 8)
+    refused(B.AR_ERR_INVALID_ARG, B.ar_experts_launch_shape, experts, 0, 1 << 31)
