@@ -715,6 +715,14 @@ def _same_device(info, t, what):
         raise ValueError(f"{what} is on device {d}; the plan is on device {info.device}")
 
 
+def _typed(t, elem, what):
+    """A tensor of `elem`-byte elements holds bf16 (2) or fp32 (4): other types of that size would be misread."""
+    torch = sys.modules["torch"]  # the tensor's own
+    wanted = torch.bfloat16 if elem == 2 else torch.float32
+    if t.dtype != wanted:
+        raise ValueError(f"{what} is of {t.dtype}; wanted {wanted}")
+
+
 def _rows(info, t, stride, rows, features, what):
     """(pointer, row stride in elements) of a [rows, features] argument: a
     device tensor whose rows are contiguous, or an address with its stride."""
@@ -725,9 +733,10 @@ def _rows(info, t, stride, rows, features, what):
     if not t.is_cuda:
         raise ValueError(f"{what} is not a device tensor")
     _same_device(info, t, what)
+    _typed(t, info.elem, what)
     shape = t.shape
-    if len(shape) != 2 or shape[0] != rows or shape[1] != features or t.element_size() != info.elem:
-        raise ValueError(f"{what} is {tuple(shape)} of {t.element_size()} bytes; wanted ({rows}, {features}) of {info.elem}")
+    if len(shape) != 2 or shape[0] != rows or shape[1] != features:
+        raise ValueError(f"{what} is {tuple(shape)}; wanted ({rows}, {features})")
     st = t.stride()
     if st[1] != 1 and features > 1 and rows > 0:
         raise ValueError(f"{what}: rows are not contiguous")
@@ -744,8 +753,9 @@ def _arena(info, t, count, elem, what):
     _same_device(info, t, what)
     if not t.is_contiguous():
         raise ValueError(f"{what} is not contiguous")
-    if t.element_size() != elem or t.numel() < count:
-        raise ValueError(f"{what} holds {t.numel()} elements of {t.element_size()} bytes; wanted {count} of {elem}")
+    _typed(t, elem, what)
+    if t.numel() < count:
+        raise ValueError(f"{what} holds {t.numel()} elements; wanted {count}")
     return t.data_ptr()
 
 

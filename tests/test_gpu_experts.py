@@ -390,3 +390,17 @@ def test_every_tile(dtype, inf, outf, experts, tokens, forward, input_grad, weig
         c.check_all()
         c = Case(inf, outf, ragged(experts, tokens - 7, 1), dtype, grad, extra=7, pad=(8, 16), seed=1)
         c.check_all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("other", [torch.float16, torch.int16])
+def test_tensors_of_another_type_are_refused(other):
+    c = Case(64, 72, [3, 4], "bf16")
+    y = torch.empty(7, 72, device=DEV, dtype=torch.bfloat16)
+    for bad in (dict(x=c.x.to(other)), dict(w=c.w.to(other)), dict(y=y.to(other))):
+        a = dict(x=c.x, w=c.w, y=y) | bad
+        with pytest.raises(ValueError, match="bfloat16"):
+            B.ar_experts_forward(c.plan, a["x"], a["w"], a["y"], c.ends)
+    with pytest.raises(ValueError, match="float32"):
+        B.ar_experts_weight_grad(c.plan, c.x, c.dy, torch.empty(c.arena, device=DEV, dtype=torch.int32), c.ends)
+    B.ar_experts_destroy(c.plan)

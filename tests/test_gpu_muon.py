@@ -482,3 +482,14 @@ def test_norms_far_below_the_constant(shapes, steps, grad, weight):
         check(out[at:at + r * c].view(r, c), want, tol, f"{r}x{c} of norm {norm}")
         check(w[at:at + r * c].view(r, c), -0.5 * want, tol, f"step of {r}x{c} of norm {norm}")
     B.ar_muon_plan_destroy(plan)
+
+
+@pytest.mark.gpu
+def test_tensors_of_another_type_are_refused():
+    plan = B.ar_muon_plan_create([(8, 16)], "bf16", "fp32")
+    g, m, w = (torch.zeros(128, device=DEV, dtype=d) for d in (torch.bfloat16, torch.float32, torch.float32))
+    for bad in (dict(g=g.half()), dict(g=g.view(torch.int16)), dict(m=m.int()), dict(w=w.int()), dict(w=w.double())):
+        a = dict(g=g, m=m, w=w) | bad
+        with pytest.raises(ValueError, match="bfloat16|float32"):
+            B.ar_muon_step(plan, a["g"], a["m"], a["w"], 0.1)
+    B.ar_muon_plan_destroy(plan)

@@ -375,3 +375,79 @@ def test_experts_launch_shape_refusals_and_nothing(experts):
     refused(B.AR_ERR_INVALID_ARG, B.ar_experts_launch_shape, experts, -1, 8)
     refused(B.AR_ERR_INVALID_ARG, B.ar_experts_launch_shape, None, 0, 8)
     refused(B.AR_ERR_INVALID_ARG, B.ar_experts_launch_shape, experts, 0, 1 << 31)
+
+
+# --------------------------------------------------- tensors of a call
+
+class OnDevice:
+    """A CPU tensor that says that it lies on a device: for checks that come before anything is launched."""
+
+    def __init__(self, t, device=0):
+        self.t, self.device, self.is_cuda = t, device, True
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+    def get_device(self):
+        return self.device
+
+
+@pytest.fixture
+def one_device(monkeypatch):
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    for stats in ("_experts_info", "_muon_info"):
+        monkeypatch.setattr(B, stats, {})
+
+
+OTHER_TYPES = {"bf16": [torch.float16, torch.int16, torch.uint16, torch.float32], "fp32": [torch.int32, torch.bfloat16, torch.float64]}
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_experts_refuse_tensors_of_another_type(dtype, one_device):
+    """The type itself is checked: 16 bits may be fp16, 32 bits an integer."""
+    p = B.ar_experts_create(2, 8, 16, dtype, "fp32")
+    B._experts_of(p).device = 0
+    mine = torch.bfloat16 if dtype == "bf16" else torch.float32
+
+    def tensors(**types):
+        shapes = dict(x=(6, 8), dy=(6, 16), y=(6, 16), dx=(6, 8), w=(256,), g=(256,))
+        return {k: OnDevice(torch.zeros(s, dtype=types.get(k, torch.float32 if k == "g" else mine)))
+                for k, s in shapes.items()}
+
+    ends = OnDevice(torch.tensor([2, 6], dtype=torch.int32))
+    for other in OTHER_TYPES[dtype]:
+        for k in ("x", "w", "y"):
+            t = tensors(**{k: other})
+            with pytest.raises(ValueError, match="bfloat16|float32"):
+                B.ar_experts_forward(p, t["x"], t["w"], t["y"], ends)
+        for k in ("dy", "w", "dx"):
+            t = tensors(**{k: other})
+            with pytest.raises(ValueError, match="bfloat16|float32"):
+                B.ar_experts_input_grad(p, t["dy"], t["w"], t["dx"], ends)
+        for k in ("x", "dy"):
+            t = tensors(**{k: other})
+            with pytest.raises(ValueError, match="bfloat16|float32"):
+                B.ar_experts_weight_grad(p, t["x"], t["dy"], t["g"], ends)
+    for other in OTHER_TYPES["fp32"]:
+        t = tensors(g=other)
+        with pytest.raises(ValueError, match="float32"):
+            B.ar_experts_weight_grad(p, t["x"], t["dy"], t["g"], ends)
+    B.ar_experts_destroy(p)
+
+
+@pytest.mark.parametrize("grad,weight", [("bf16", "fp32"), ("fp32", "bf16")])
+def test_muon_refuses_tensors_of_another_type(grad, weight, one_device):
+    p = B.ar_muon_plan_create([(4, 8)], grad, weight)
+    B._muon_of(p).device = 0
+    mine = dict(g=grad, m="fp32", w=weight, mo="fp32", wo=weight)
+    name = {"bf16": torch.bfloat16, "fp32": torch.float32}
+    for k, own in mine.items():
+        for other in OTHER_TYPES[own]:
+            t = {n: OnDevice(torch.zeros(32, dtype=other if n == k else name[d])) for n, d in mine.items()}
+            with pytest.raises(ValueError, match="bfloat16|float32"):
+                B.ar_muon_step(p, t["g"], t["m"], t["w"], 0.1, momentum_out=t["mo"], weights_out=t["wo"])
+            if k in ("g", "w"):
+                with pytest.raises(ValueError, match="bfloat16|float32"):
+                    B.ar_orthogonalize(p, t["g"], t["w"])
+    B.ar_muon_plan_destroy(p)
