@@ -677,19 +677,22 @@ def ar_bucket_plan_destroy(bp):
 
 # ------------------------------------------- products grouped by expert
 
-def _bound(plan, stats, prepare):
-    """Device of a plan, which is prepared if it was not (not while the caller captures a graph)."""
-    if stats(plan).device < 0:
-        torch = sys.modules.get("torch")  # the tensors' own
-        if torch is not None and torch.cuda.is_current_stream_capturing():
-            raise ValueError("the plan has to be prepared before it is captured")
-        _check(prepare(plan))
-    return stats(plan).device
+def _device(info, stats):
+    """Device of a plan, or the one that a call will bind it to (the current one; not while the caller captures a
+    graph).  The call itself prepares the plan, when nothing refuses it any more and on its own stream's word."""
+    d = stats(info.plan).device
+    if d >= 0:
+        info.device = d
+        return d
+    torch = sys.modules["torch"]  # the tensors' own
+    if torch.cuda.is_current_stream_capturing():
+        raise ValueError("the plan has to be prepared before it is captured")
+    return torch.cuda.current_device()
 
 
 class _ExpertsInfo:
     """What the checks of a call need of a plan, read once; `device` is the one the plan is bound to (None
-    before its first call with tensors, which prepares it)."""
+    while it is not known to be)."""
     __slots__ = ("plan", "nexperts", "inf", "outf", "elem", "grad", "arena", "device")
 
     def __init__(self, plan):
@@ -699,8 +702,8 @@ class _ExpertsInfo:
         self.elem, self.grad, self.arena = s.elem_bytes, s.grad_bytes, s.arena_count
         self.device = None
 
-    def bind(self):
-        self.device = _bound(self.plan, lib().ar_experts_stats, lib().ar_experts_prepare)
+    def find_device(self):
+        return _device(self, lib().ar_experts_stats)
 
 
 _experts_info = {}  # by handle, until the plan is destroyed
@@ -708,11 +711,10 @@ _experts_info = {}  # by handle, until the plan is destroyed
 
 def _same_device(info, t, what):
     """Every tensor of a call, and of all calls of a plan, lies on one device."""
-    if info.device is None:
-        info.bind()
+    on = info.find_device() if info.device is None else info.device
     d = t.get_device()
-    if d != info.device:
-        raise ValueError(f"{what} is on device {d}; the plan is on device {info.device}")
+    if d != on:
+        raise ValueError(f"{what} is on device {d}; the plan is on device {on}")
 
 
 def _typed(t, elem, what):
@@ -932,8 +934,8 @@ class _MuonInfo:
         self.arena, self.grad, self.weight = s.arena_count, s.grad_bytes, s.weight_bytes
         self.device = None
 
-    def bind(self):
-        self.device = _bound(self.plan, lib().ar_muon_plan_stats, lib().ar_muon_plan_prepare)
+    def find_device(self):
+        return _device(self, lib().ar_muon_plan_stats)
 
 
 _muon_info = {}

@@ -11,7 +11,7 @@ import pytest
 import torch
 
 from gradient_all_reduce_ar_amd import _binding as B
-from tests.test_operators_cpu import ROWS_OF_DISPATCH, launch_shapes
+from tests.test_operators_cpu import ROWS_OF_DISPATCH, OnDevice, launch_shapes
 
 DEV = "cuda:0"
 T = {"fp32": torch.float32, "bf16": torch.bfloat16}
@@ -403,4 +403,41 @@ def test_tensors_of_another_type_are_refused(other):
             B.ar_experts_forward(c.plan, a["x"], a["w"], a["y"], c.ends)
     with pytest.raises(ValueError, match="float32"):
         B.ar_experts_weight_grad(c.plan, c.x, c.dy, torch.empty(c.arena, device=DEV, dtype=torch.int32), c.ends)
+    B.ar_experts_destroy(c.plan)
+
+
+@pytest.mark.gpu
+def test_refused_calls_leave_the_plan_unbound():
+    """Tensors of another device, or of wrong sizes: the plan can still be bound where it belongs."""
+    c = Case(64, 72, [3, 4], "bf16")
+    y = c.rows(72, 0, 0)
+    for bad in (dict(x=OnDevice(c.x, 1)), dict(w=OnDevice(c.w, 1)), dict(y=y[:5]), dict(ends=OnDevice(c.ends, 1))):
+        a = dict(x=c.x, w=c.w, y=y, ends=c.ends) | bad
+        with pytest.raises(ValueError):
+            B.ar_experts_forward(c.plan, a["x"], a["w"], a["y"], a["ends"])
+        assert B.ar_experts_stats(c.plan)["device"] == -1
+    B.ar_experts_forward(c.plan, c.x, c.w, y, c.ends)
+    torch.cuda.synchronize()
+    assert B.ar_experts_stats(c.plan)["device"] == 0
+    c.check_rows(y, c.x, False)
+    B.ar_experts_destroy(c.plan)
+
+
+@pytest.mark.gpu
+def test_an_unprepared_plan_does_not_end_a_capture_on_another_stream():
+    """The call's stream is being captured while another one is current: the call is refused before it allocates,
+    and the capture goes on."""
+    c = Case(64, 32, [5, 0, 20], "bf16")
+    y, other = c.rows(32, 0, 0), torch.zeros(4, device=DEV)
+    s, current = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        with torch.cuda.stream(current):
+            with pytest.raises((B.ArError, ValueError)):
+                B.ar_experts_forward(c.plan, c.x, c.w, y, c.ends, s)
+        other.add_(1)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert other.tolist() == [1] * 4 and B.ar_experts_stats(c.plan)["device"] == -1
     B.ar_experts_destroy(c.plan)

@@ -451,3 +451,18 @@ def test_muon_refuses_tensors_of_another_type(grad, weight, one_device):
                 with pytest.raises(ValueError, match="bfloat16|float32"):
                     B.ar_orthogonalize(p, t["g"], t["w"])
     B.ar_muon_plan_destroy(p)
+
+
+def test_refused_calls_do_not_bind_a_plan(one_device):
+    """A call whose tensors lie on another device than the current one, or do not fit, leaves the plan unbound."""
+    ex, mu = B.ar_experts_create(2, 8, 16, "fp32"), B.ar_muon_plan_create([(4, 8)], "fp32", "fp32")
+    ends = OnDevice(torch.tensor([2, 6], dtype=torch.int32))
+    for device, rows in ((1, 6), (0, 5)):
+        x, y, w, g = (OnDevice(torch.zeros(s), device) for s in ((6, 8), (rows, 16), (256,), (31 if rows < 6 else 32,)))
+        with pytest.raises(ValueError, match="device 1" if device else "wanted"):
+            B.ar_experts_forward(ex, x, w, y, ends)
+        with pytest.raises(ValueError, match="device 1" if device else "wanted"):
+            B.ar_orthogonalize(mu, g, g)
+    assert B.ar_experts_stats(ex)["device"] == -1 and B.ar_muon_plan_stats(mu)["device"] == -1
+    B.ar_experts_destroy(ex)
+    B.ar_muon_plan_destroy(mu)
