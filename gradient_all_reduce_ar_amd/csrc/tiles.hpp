@@ -107,7 +107,7 @@ constexpr uint32_t kOutOfRange = 0x80000000u;
 __device__ __forceinline__ void load_to_lds(ux4 r, uint32_t off, uint32_t lds_base) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds_base), "v"(off),
                "s"(r)
-               : "memory");
+               : "memory", "m0");
 }
 
 // Every load_to_lds of this wave has landed and its LDS reads are done, then
