@@ -484,6 +484,8 @@ hipError_t launch_rows(const ExpertArgs &a, hipStream_t s) {
 //   8192, 4, 2048 x 2048:        - /  661 /  598 /  759             632 /  574 /  678
 //   3001, 8, 1024 x 1536:        - /  131 /   95 /  126             130 /  102 /  112
 //   500, 4, 1000 x 1000:         - /   77 /   44 /   36              72 /   42 /   27
+// The fp32 input gradients of these sizes by the tile that is chosen: 3782,
+// 508, 111 and 20.
 struct TileCost {
   double slots, alone, full, rest;
 };
@@ -509,9 +511,19 @@ enum Choice { kBig, kSquare, kHalf, kSmall, kFew };
 template <bool GRAD>
 Choice rows_choice(const ExpertArgs &a) {
   if constexpr (!GRAD) {
-    // Short decoding calls, where latency counts: up to 16 MiB of weights (one
-    // token, 8 experts, 1024 x 512: 4.9 us, with Small 9.9; from 250 MB on
-    // Small reads faster, 53 us against 62).
+    // Short decoding calls, where latency counts: up to 16 MiB of weights, as
+    // counted here.  Microseconds with experts_few / Small, bf16, weights from
+    // memory (rows, active of experts, in x out: MiB):
+    //   1, 1 of 8, 1024 x 512: 1          4.7 /  7.7
+    //   8, 8 of 8, 1024 x 512: 8          5.8 /  8.4
+    //   4, 4 of 8, 2048 x 1024: 16        7.7 / 13.1
+    //   8, 8 of 8, 1024 x 1024: 16        9.8 /  8.5
+    //   16, 8 of 8, 2048 x 1024: 32      13.7 / 15.1
+    //   8, 8 of 8, 2048 x 2048: 64       25.3 / 19.0
+    //   32, 20 of 32, 2048 x 1536: 192   45.9 / 31.3
+    //   32, 20 of 32, 4096 x 1536: 384   65.1 / 56.9
+    // Long rows of few experts (2 of 8, 4096 x 4096: 64 MiB) take 17.4 / 23.2;
+    // fp32 meets at 128 MiB (8 of 8, 2048 x 2048: 37.1 / 36.8).
     const int64_t e = a.experts, bytes = std::min(e, a.tokens) * a.in * a.outf * (a.bf16 ? 2 : 4);
     if (a.tokens <= 16 * e && bytes <= 16 << 20) return kFew;
   }
@@ -593,6 +605,11 @@ hipError_t launch_weights_of(const ExpertArgs &a, hipStream_t s) {
 //   515, 24, 1025 x 511:              - / 18.6 / 16.6
 //   fp32, 8192, 4, 2048 x 2048:       - / 505 / 508
 //   fp32, 8192, 4, 2047 x 2047:       - / 600 / 608
+// Adding to the arena reads it as well: the first of these takes 487 us instead
+// of 255 (bf16 gradients 434 for 222), the fp32 one of 2048 x 2048 495 for 491.
+// The choice knows the rows of all experts together: with all of 16384 rows
+// going to one of 8 experts, 4096 x 2048 takes 329 us instead of 254, and 1024
+// x 512, whose 32 tiles of that expert leave the other CUs idle, 159 for 33.
 Choice weight_choice(const ExpertArgs &a) {
   const bool fill = a.tokens >= 256 * static_cast<int64_t>(a.experts);
   if (!a.bf16) return kHalf;
