@@ -176,13 +176,13 @@ def _quantized(v, scale_bytes):
 
 
 def _quantized_rows(x):
-    """Codes [rows, features] and scales [blocks, rows] of fp32 rows."""
+    """Codes [rows, features] and scales [rows, blocks] of fp32 rows."""
     t, n = x.shape
     blocks = -(-n // BLOCK)
     v = torch.nn.functional.pad(x, (0, blocks * BLOCK - n)).view(t, blocks, BLOCK)
     e = _scale_bytes(v.abs().amax(2))
     codes = _quantized(v, e[:, :, None]).view(t, blocks * BLOCK)[:, :n].contiguous()
-    return codes, e.to(torch.uint8).t().contiguous().view(POW2)
+    return codes, e.to(torch.uint8).view(POW2)
 
 
 def _quantized_weights(w):
@@ -254,7 +254,7 @@ def prepare(case, seed):
             d["y"] = _new((t, n), dt) if case["y"] else None
             d["rstd"] = _new(t, torch.float32) if case["y"] else None  # a training step keeps it
             d["codes"] = _new((t, n), torch.uint8).view(FP8) if case["codes"] else None
-            d["scales"] = _new((-(-n // BLOCK), t), torch.uint8).view(POW2) if case["codes"] else None
+            d["scales"] = _new((t, -(-n // BLOCK)), torch.uint8).view(POW2) if case["codes"] else None
         else:
             d["dx"], d["dgain"] = _new((t, n), dt), _new(n, torch.float32)
     else:
@@ -264,7 +264,7 @@ def prepare(case, seed):
         elif op == "input_grad":
             d["out"] = _new((t, i), dt)
             d["codes"] = _new((t, o), torch.uint8).view(FP8)
-            d["scales"] = _new((-(-o // BLOCK), t), torch.uint8).view(POW2)
+            d["scales"] = _new((t, -(-o // BLOCK)), torch.uint8).view(POW2)
         else:
             d["codes"] = _new((e, o, i), torch.uint8).view(FP8)
             d["scales"] = _new((e, -(-o // BLOCK), -(-i // BLOCK)), torch.uint8).view(POW2)
@@ -348,7 +348,7 @@ def _plain_norm_grad(s):
 
 
 def _wide_rows(codes, scales):
-    return codes.float() * scales.float().t().repeat_interleave(BLOCK, 1)[:, :codes.shape[1]]
+    return codes.float() * scales.float().repeat_interleave(BLOCK, 1)[:, :codes.shape[1]]
 
 
 def _wide_weight(codes, scales):
@@ -435,8 +435,8 @@ def _exact_codes(v, scales):
 
 def _exact_rows(x):
     blocks = torch.split(x.abs(), BLOCK, dim=1)
-    scales = _exact_scales(torch.stack([b.amax(1) for b in blocks]))  # [blocks, rows]
-    return _exact_codes(x, _spread_scales(scales, 0, x.shape[1]).t()), scales
+    scales = _exact_scales(torch.stack([b.amax(1) for b in blocks], 1))
+    return _exact_codes(x, _spread_scales(scales, 1, x.shape[1])), scales
 
 
 def _exact_clip(case, seed):
@@ -482,7 +482,7 @@ def _exact_product(case, seed):
             codes.append(_exact_codes(w, wide))
         return torch.stack(codes), torch.stack(scales)
     codes, scales = (s["x"].double(), s["x_scales"].double()) if op == "forward" else _exact_rows(s["dy"].double())
-    rows = codes * _spread_scales(scales, 0, codes.shape[1]).t()
+    rows = codes * _spread_scales(scales, 1, codes.shape[1])
     for k, n in enumerate(s["counts"]):
         w, ws = s["w"][k].double(), s["w_scales"][k].double()
         w = w * _spread_scales(_spread_scales(ws, 0, w.shape[0]), 1, w.shape[1])
