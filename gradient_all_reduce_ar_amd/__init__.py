@@ -1,8 +1,9 @@
 """MI355X-native gradient all-reduce schedules (ring, hierarchical, Rabenseifner,
 recursive doubling, binary and double binary trees; fp32, bf16 and blockwise
 INT8 with error feedback), and what stands around them in a training step: the
-products of a mixture of experts (whose weight gradients fill the arenas) and
-the Muon update of the reduced gradients.
+products of a mixture of experts (whose weight gradients fill the arenas; in
+bf16, fp32 or 8 bits), the RMS norm before them, and behind the all-reduce the
+clipping of the gradients and the Muon update.
 
 The compute path is the HIP library libar.so (csrc/), reached through the
 C ABI declared in include/ar.h; this package only marshals arguments.
@@ -22,4 +23,8 @@ from ._binding import (  # noqa: F401
     ar_experts_create, ar_experts_destroy, ar_experts_forward, ar_experts_input_grad, ar_experts_launch_shape,
     ar_experts_prepare, ar_experts_stats, ar_experts_weight_grad, ar_muon_plan_create, ar_muon_plan_destroy, ar_muon_plan_prepare,
     ar_muon_plan_set_iterations, ar_muon_plan_set_scales, ar_muon_plan_stats, ar_muon_plan_work, ar_muon_step, ar_orthogonalize,
+    ar_grad_clip, ar_grad_norm, ar_norm_plan_create, ar_norm_plan_destroy, ar_norm_plan_prepare, ar_norm_plan_stats,
+    ar_qexperts_create, ar_qexperts_destroy, ar_qexperts_forward, ar_qexperts_input_grad, ar_qexperts_launch_shape,
+    ar_qexperts_prepare, ar_qexperts_quantize, ar_qexperts_stats, ar_quantize_rows, ar_rmsnorm_backward, ar_rmsnorm_create,
+    ar_rmsnorm_destroy, ar_rmsnorm_forward, ar_rmsnorm_prepare, ar_rmsnorm_stats,
 )

@@ -70,6 +70,32 @@ class ar_muon_params_t(ctypes.Structure):
                 ("grad_scale", ctypes.c_double), ("nesterov", ctypes.c_int32)]
 
 
+class ar_norm_stats_t(ctypes.Structure):
+    _fields_ = [("ntensors", ctypes.c_int32), ("device", ctypes.c_int32), ("grad_bytes", ctypes.c_uint64),
+                ("count", ctypes.c_uint64), ("arena_count", ctypes.c_uint64), ("workspace_bytes", ctypes.c_uint64)]
+
+
+class ar_rmsnorm_stats_t(ctypes.Structure):
+    _fields_ = [("device", ctypes.c_int32), ("features", ctypes.c_uint64), ("elem_bytes", ctypes.c_uint64),
+                ("gain_bytes", ctypes.c_uint64), ("grad_bytes", ctypes.c_uint64), ("workspace_bytes", ctypes.c_uint64)]
+
+
+class ar_rmsnorm_forward_t(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_void_p) for k in ("x", "residual", "gain", "h", "y", "codes", "scales", "rstd")] + [
+        (k + "_stride", ctypes.c_size_t) for k in ("x", "residual", "h", "y", "codes", "scales")]
+
+
+class ar_rmsnorm_backward_t(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_void_p) for k in ("dy", "h", "dh", "gain", "rstd", "dx", "dgain")] + [
+        (k + "_stride", ctypes.c_size_t) for k in ("dy", "h", "dh", "dx")] + [("accumulate", ctypes.c_int32)]
+
+
+class ar_qexperts_stats_t(ctypes.Structure):
+    _fields_ = [("nexperts", ctypes.c_int32), ("device", ctypes.c_int32), ("in_features", ctypes.c_uint64),
+                ("out_features", ctypes.c_uint64), ("elem_bytes", ctypes.c_uint64), ("arena_count", ctypes.c_uint64),
+                ("scale_count", ctypes.c_uint64), ("workspace_bytes", ctypes.c_uint64)]
+
+
 class ar_stats_t(ctypes.Structure):
     _fields_ = [
         ("nranks", ctypes.c_int32), ("group_size", ctypes.c_int32),
@@ -177,6 +203,27 @@ def _declare(L):
         "ar_orthogonalize": ([P, P, P, P], ctypes.c_int),
         "ar_muon_step": ([P, P, P, P, P, P, ctypes.POINTER(ar_muon_params_t), P], ctypes.c_int),
         "ar_muon_plan_destroy": ([P], None),
+        "ar_norm_plan_create": ([ctypes.c_int, psz, psz, ctypes.c_int], P),
+        "ar_norm_plan_prepare": ([P], ctypes.c_int),
+        "ar_norm_plan_stats": ([P], ar_norm_stats_t),
+        "ar_grad_norm": ([P, P, dbl, P, P, P], ctypes.c_int),
+        "ar_grad_clip": ([P, P, P, P, dbl, P], ctypes.c_int),
+        "ar_norm_plan_destroy": ([P], None),
+        "ar_quantize_rows": ([P, ctypes.c_int, sz, P, sz, P, sz, sz, sz, P], ctypes.c_int),
+        "ar_rmsnorm_create": ([sz, ctypes.c_int, ctypes.c_int, ctypes.c_int, dbl], P),
+        "ar_rmsnorm_prepare": ([P], ctypes.c_int),
+        "ar_rmsnorm_stats": ([P], ar_rmsnorm_stats_t),
+        "ar_rmsnorm_forward": ([P, ctypes.POINTER(ar_rmsnorm_forward_t), sz, P], ctypes.c_int),
+        "ar_rmsnorm_backward": ([P, ctypes.POINTER(ar_rmsnorm_backward_t), sz, P], ctypes.c_int),
+        "ar_rmsnorm_destroy": ([P], None),
+        "ar_qexperts_create": ([ctypes.c_int, sz, sz, ctypes.c_int, psz], P),
+        "ar_qexperts_prepare": ([P], ctypes.c_int),
+        "ar_qexperts_stats": ([P], ar_qexperts_stats_t),
+        "ar_qexperts_launch_shape": ([P, ctypes.c_int, sz, ctypes.c_int, pi32, pi32], ctypes.c_int),
+        "ar_qexperts_quantize": ([P, P, ctypes.c_int, P, P, P], ctypes.c_int),
+        "ar_qexperts_forward": ([P, P, sz, P, sz, P, P, P, sz, P, sz, P], ctypes.c_int),
+        "ar_qexperts_input_grad": ([P, P, sz, P, sz, P, P, P, sz, P, sz, P], ctypes.c_int),
+        "ar_qexperts_destroy": ([P], None),
     }
     for name, (args, res) in sig.items():
         f = getattr(L, name)
@@ -975,3 +1022,378 @@ def ar_muon_step(plan, grads, momentum, weights, lr, mu=0.95, weight_decay=0.0, 
 def ar_muon_plan_destroy(plan):
     _muon_info.pop(plan, None)
     lib().ar_muon_plan_destroy(plan)
+
+
+# --------------------------------------- the global gradient norm, clipping
+
+class _NormInfo:
+    __slots__ = ("plan", "ntensors", "arena", "elem", "device")
+
+    def __init__(self, plan):
+        s = lib().ar_norm_plan_stats(plan)
+        self.plan = plan
+        self.ntensors, self.arena, self.elem = s.ntensors, s.arena_count, s.grad_bytes
+        self.device = None
+
+    def find_device(self):
+        return _device(self, lib().ar_norm_plan_stats)
+
+
+_norm_info = {}  # by handle, until the plan is destroyed
+
+
+def _info_of(table, make, prepare, plan):
+    info = table.get(plan)
+    if info is None:  # no plan, or its first call
+        if not plan:
+            _check(prepare(None))
+        info = table[plan] = make(plan)
+    return info
+
+
+def _sizes(values):
+    return (ctypes.c_size_t * max(len(values), 1))(*[int(v) for v in values])
+
+
+def ar_norm_plan_create(counts, grad_dtype, offsets=None):
+    """counts: elements of each tensor; offsets: first element of each in the arena (None: back to back)."""
+    if offsets is not None and len(offsets) != len(counts):
+        raise ValueError(f"{len(offsets)} offsets for {len(counts)} tensors")
+    p = lib().ar_norm_plan_create(len(counts), _sizes(counts), None if offsets is None else _sizes(offsets),
+                                  _code(DTYPES, grad_dtype))
+    if not p:
+        _raise()
+    return p
+
+
+def ar_norm_plan_prepare(plan):
+    _check(lib().ar_norm_plan_prepare(plan))
+
+
+def ar_norm_plan_stats(plan):
+    s = lib().ar_norm_plan_stats(plan)
+    return {k: getattr(s, k) for k, _ in s._fields_}
+
+
+def ar_grad_norm(plan, grads, norm, tensor_norms=None, scale=1.0, stream=None):
+    """norm[0] = scale times the norm of all tensors of the arena (fp32, on the device); tensor_norms: each tensor's."""
+    i = _info_of(_norm_info, _NormInfo, lib().ar_norm_plan_prepare, plan)
+    g = _arena(i, grads, i.arena, i.elem, "grads")
+    n = _arena(i, norm, 1, 4, "norm")
+    t = None if tensor_norms is None else _arena(i, tensor_norms, i.ntensors, 4, "tensor_norms")
+    if _lib.ar_grad_norm(plan, g, scale, n, t, _stream(stream)) != AR_OK:
+        _raise()
+
+
+def ar_grad_clip(plan, grads, norm, max_norm, out=None, stream=None):
+    """out = min(1, max_norm / (norm[0] + 1e-6)) grads; in place without out."""
+    i = _info_of(_norm_info, _NormInfo, lib().ar_norm_plan_prepare, plan)
+    g = _arena(i, grads, i.arena, i.elem, "grads")
+    o = None if out is None else _arena(i, out, i.arena, i.elem, "out")
+    if _lib.ar_grad_clip(plan, g, o, _arena(i, norm, 1, 4, "norm"), max_norm, _stream(stream)) != AR_OK:
+        _raise()
+
+
+def ar_norm_plan_destroy(plan):
+    _norm_info.pop(plan, None)
+    lib().ar_norm_plan_destroy(plan)
+
+
+# ------------------------------------------- 8-bit rows, and the RMS norm
+
+QBLOCK8 = 128  # elements of a scale
+
+
+def _blocks(n):
+    return -(-n // QBLOCK8)
+
+
+def _types(kind):
+    """The tensor types that hold codes ("codes"), scales ("scales") or elements of 2 or 4 bytes."""
+    torch = sys.modules["torch"]  # the tensors' own
+    return {"codes": (torch.float8_e4m3fn, torch.uint8), "scales": (torch.float8_e8m0fnu, torch.uint8),
+            2: (torch.bfloat16,), 4: (torch.float32,)}[kind]
+
+
+_kinds = {}
+
+
+def _matrix(info, t, stride, rows, cols, kind, what):
+    """(pointer, row stride in elements) of a [rows, cols] argument: a device tensor whose rows are contiguous, or
+    an address (dense without a stride); (None, cols) without one."""
+    if t is None:
+        return None, cols
+    if not hasattr(t, "data_ptr"):
+        return int(t), cols if stride is None else int(stride)
+    if stride is not None:
+        raise ValueError(f"{what}: a tensor brings its own stride")
+    d = t.get_device()
+    if d < 0:
+        raise ValueError(f"{what} is not a device tensor")
+    if d != info.device:
+        _same_device(info, t, what)
+    types = _kinds.get(kind)
+    if types is None:
+        types = _kinds[kind] = _types(kind)
+    if t.dtype not in types:
+        raise ValueError(f"{what} is of {t.dtype}; wanted {types[0]}")
+    shape = t.shape
+    if len(shape) != 2 or shape[0] != rows or shape[1] != cols:
+        raise ValueError(f"{what} is {tuple(shape)}; wanted ({rows}, {cols})")
+    st = t.stride()
+    if st[1] != 1 and cols > 1 and rows > 0:
+        raise ValueError(f"{what}: rows are not contiguous")
+    return t.data_ptr(), st[0] if rows > 1 else cols
+
+
+def _vector(info, t, count, kind, what):
+    """Pointer of at least count contiguous elements: a device tensor or an address; None without one."""
+    if t is None:
+        return None
+    if not hasattr(t, "data_ptr"):
+        return int(t)
+    d = t.get_device()
+    if d < 0:
+        raise ValueError(f"{what} is not a device tensor")
+    if d != info.device:
+        _same_device(info, t, what)
+    types = _kinds.get(kind)
+    if types is None:
+        types = _kinds[kind] = _types(kind)
+    if t.dtype not in types:
+        raise ValueError(f"{what} is of {t.dtype}; wanted {types[0]}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what} is not contiguous")
+    if t.numel() < count:
+        raise ValueError(f"{what} holds {t.numel()} elements; wanted {count}")
+    return t.data_ptr()
+
+
+class _CurrentDevice:
+    """The checks of a call without a plan: its tensors lie on the current device."""
+
+    def __init__(self):
+        self.device = sys.modules["torch"].cuda.current_device()
+
+    def find_device(self):
+        return self.device
+
+
+def ar_quantize_rows(x, codes, scales, stream=None, dtype=None, features=None, ntokens=None, x_stride=None,
+                     codes_stride=None, scales_stride=None):
+    """codes, scales = the rows of x in 8 bits.  x [tokens, features], codes the same in bytes, scales [tokens,
+    ceil(features / 128)] bytes: tensors with contiguous rows, or addresses (then dtype, features and ntokens, and
+    the strides if rows are not dense)."""
+    L = lib()
+    tensor = hasattr(x, "data_ptr")
+    if tensor:
+        if x.get_device() < 0:
+            raise ValueError("x is not a device tensor")
+        if len(x.shape) != 2:
+            raise ValueError(f"x is {tuple(x.shape)}; wanted rows")
+        torch = sys.modules["torch"]
+        elem = {torch.float32: 4, torch.bfloat16: 2}.get(x.dtype)
+        if elem is None:
+            raise ValueError(f"x is of {x.dtype}; wanted {torch.bfloat16} or {torch.float32}")
+        n, f, d = int(x.shape[0]), int(x.shape[1]), AR_BFLOAT16 if elem == 2 else AR_FLOAT32
+        if (dtype, features, ntokens) != (None, None, None):
+            raise ValueError("x: a tensor brings its own type and sizes")
+    else:
+        if dtype is None or features is None or ntokens is None:
+            raise ValueError("x is an address: dtype, features and ntokens are needed")
+        n, f, d = int(ntokens), int(features), _code(DTYPES, dtype)
+        elem = 2 if d == AR_BFLOAT16 else 4
+    info = _CurrentDevice() if any(hasattr(t, "data_ptr") for t in (x, codes, scales)) else None
+    xp, xs = _matrix(info, x, x_stride, n, f, elem, "x")
+    cp, cs = _matrix(info, codes, codes_stride, n, f, "codes", "codes")
+    sp, ss = _matrix(info, scales, scales_stride, n, _blocks(f), "scales", "scales")
+    if L.ar_quantize_rows(xp, d, xs, cp, cs, sp, ss, f, n, _stream(stream)) != AR_OK:
+        _raise()
+
+
+class _RmsInfo:
+    __slots__ = ("plan", "features", "elem", "gain", "grad", "device")
+
+    def __init__(self, plan):
+        s = lib().ar_rmsnorm_stats(plan)
+        self.plan = plan
+        self.features, self.elem, self.gain, self.grad = s.features, s.elem_bytes, s.gain_bytes, s.grad_bytes
+        self.device = None
+
+    def find_device(self):
+        return _device(self, lib().ar_rmsnorm_stats)
+
+
+_rms_info = {}
+
+
+def ar_rmsnorm_create(features, dtype, gain_dtype=None, grad_dtype=None, eps=1e-6):
+    """dtype (of the rows), gain_dtype, grad_dtype (of the gain's gradient): "fp32" or "bf16" (None: dtype)."""
+    d = _code(DTYPES, dtype)
+    p = lib().ar_rmsnorm_create(features, d, d if gain_dtype is None else _code(DTYPES, gain_dtype),
+                                d if grad_dtype is None else _code(DTYPES, grad_dtype), eps)
+    if not p:
+        _raise()
+    return p
+
+
+def ar_rmsnorm_prepare(plan):
+    _check(lib().ar_rmsnorm_prepare(plan))
+
+
+def ar_rmsnorm_stats(plan):
+    s = lib().ar_rmsnorm_stats(plan)
+    return {k: getattr(s, k) for k, _ in s._fields_}
+
+
+def ar_rmsnorm_forward(plan, x, gain, residual=None, h=None, y=None, codes=None, scales=None, rstd=None, stream=None,
+                       ntokens=None, strides=None):
+    """h = x + residual; y, or codes and scales, or both = h / rms(h) gain; rstd = 1 / rms(h).  Rows are tensors
+    [tokens, features] with contiguous rows, or addresses (x one: then ntokens; strides: {"x": elements between
+    rows, ...} of those that are not dense)."""
+    i = _info_of(_rms_info, _RmsInfo, lib().ar_rmsnorm_prepare, plan)
+    n, f, e, st = _tokens(x, ntokens, "x"), i.features, i.elem, strides or {}
+    a = ar_rmsnorm_forward_t()
+    a.x, a.x_stride = _matrix(i, x, st.get("x"), n, f, e, "x")
+    a.gain = _vector(i, gain, f, i.gain, "gain")
+    if residual is not None:
+        a.residual, a.residual_stride = _matrix(i, residual, st.get("residual"), n, f, e, "residual")
+    if h is not None:
+        a.h, a.h_stride = _matrix(i, h, st.get("h"), n, f, e, "h")
+    if y is not None:
+        a.y, a.y_stride = _matrix(i, y, st.get("y"), n, f, e, "y")
+    if codes is not None:
+        a.codes, a.codes_stride = _matrix(i, codes, st.get("codes"), n, f, "codes", "codes")
+    if scales is not None:
+        a.scales, a.scales_stride = _matrix(i, scales, st.get("scales"), n, _blocks(f), "scales", "scales")
+    if rstd is not None:
+        a.rstd = _vector(i, rstd, n, 4, "rstd")
+    if _lib.ar_rmsnorm_forward(plan, ctypes.byref(a), n, _stream(stream)) != AR_OK:
+        _raise()
+
+
+def ar_rmsnorm_backward(plan, dy, h, gain, rstd, dx, dgain, dh=None, accumulate=False, stream=None, ntokens=None,
+                        strides=None):
+    """dx = the gradient of x (and of residual) for the gradients dy of y and dh of h; dgain = (the old dgain +) the
+    gain's.  Arguments as ar_rmsnorm_forward's; rstd is the forward pass's."""
+    i = _info_of(_rms_info, _RmsInfo, lib().ar_rmsnorm_prepare, plan)
+    n, f, e, st = _tokens(dy, ntokens, "dy"), i.features, i.elem, strides or {}
+    a = ar_rmsnorm_backward_t()
+    a.dy, a.dy_stride = _matrix(i, dy, st.get("dy"), n, f, e, "dy")
+    a.h, a.h_stride = _matrix(i, h, st.get("h"), n, f, e, "h")
+    a.gain = _vector(i, gain, f, i.gain, "gain")
+    a.rstd = _vector(i, rstd, n, 4, "rstd")
+    a.dx, a.dx_stride = _matrix(i, dx, st.get("dx"), n, f, e, "dx")
+    a.dgain = _vector(i, dgain, f, i.grad, "dgain")
+    if dh is not None:
+        a.dh, a.dh_stride = _matrix(i, dh, st.get("dh"), n, f, e, "dh")
+    a.accumulate = 1 if accumulate else 0
+    if _lib.ar_rmsnorm_backward(plan, ctypes.byref(a), n, _stream(stream)) != AR_OK:
+        _raise()
+
+
+def ar_rmsnorm_destroy(plan):
+    _rms_info.pop(plan, None)
+    lib().ar_rmsnorm_destroy(plan)
+
+
+# ----------------------------------- products grouped by expert, in 8 bits
+
+class _QExpertsInfo:
+    __slots__ = ("plan", "nexperts", "inf", "outf", "elem", "arena", "scales", "device")
+
+    def __init__(self, plan):
+        s = lib().ar_qexperts_stats(plan)
+        self.plan = plan
+        self.nexperts, self.inf, self.outf = s.nexperts, s.in_features, s.out_features
+        self.elem, self.arena, self.scales = s.elem_bytes, s.arena_count, s.scale_count
+        self.device = None
+
+    def find_device(self):
+        return _device(self, lib().ar_qexperts_stats)
+
+
+_qexperts_info = {}
+
+
+def ar_qexperts_create(nexperts, in_features, out_features, dtype, weight_offsets=None):
+    """dtype (of y and dx): "bf16" or "fp32"; weight_offsets: first element of each expert's [out_features,
+    in_features] matrix in its arena (None: back to back)."""
+    if weight_offsets is not None and len(weight_offsets) != nexperts:
+        raise ValueError(f"{len(weight_offsets)} weight offsets for {nexperts} experts")
+    p = lib().ar_qexperts_create(nexperts, in_features, out_features, _code(DTYPES, dtype),
+                                 None if weight_offsets is None else _sizes(weight_offsets))
+    if not p:
+        _raise()
+    return p
+
+
+def ar_qexperts_prepare(plan):
+    _check(lib().ar_qexperts_prepare(plan))
+
+
+def ar_qexperts_stats(plan):
+    s = lib().ar_qexperts_stats(plan)
+    return {k: getattr(s, k) for k, _ in s._fields_}
+
+
+def ar_qexperts_launch_shape(plan, product, ntokens, aligned=True):
+    """dict(tile_rows, tile_cols) of a product ("forward" or "input_grad") of ntokens rows."""
+    v = [ctypes.c_int32() for _ in range(2)]
+    _check(lib().ar_qexperts_launch_shape(plan, _code(EXPERT_PRODUCTS, product), int(ntokens), 1 if aligned else 0,
+                                          *[ctypes.byref(x) for x in v]))
+    return dict(zip(("tile_rows", "tile_cols"), [x.value for x in v]))
+
+
+def ar_qexperts_quantize(plan, weights, codes, scales, stream=None, dtype=None):
+    """codes, scales = every expert's matrix of the arena in 8 bits (weights: a tensor, or an address with its
+    dtype); scales: [nexperts, ceil(out / 128), ceil(in / 128)] bytes."""
+    i = _info_of(_qexperts_info, _QExpertsInfo, lib().ar_qexperts_prepare, plan)
+    if hasattr(weights, "data_ptr"):
+        if dtype is not None:
+            raise ValueError("weights: a tensor brings its own type")
+        d = AR_BFLOAT16 if weights.element_size() == 2 else AR_FLOAT32
+    elif dtype is None:
+        raise ValueError("weights is an address: dtype is needed")
+    else:
+        d = _code(DTYPES, dtype)
+    w = _vector(i, weights, i.arena, 2 if d == AR_BFLOAT16 else 4, "weights")
+    if _lib.ar_qexperts_quantize(plan, w, d, _vector(i, codes, i.arena, "codes", "codes"),
+                                 _vector(i, scales, i.scales, "scales", "scales"), _stream(stream)) != AR_OK:
+        _raise()
+
+
+def ar_qexperts_forward(plan, x, x_scales, weights, weight_scales, y, ends, stream=None, ntokens=None, x_stride=None,
+                        x_scales_stride=None, y_stride=None):
+    """y[t] = W_e x[t] for the rows t of expert e.  x [tokens, in] codes with x_scales [tokens, ceil(in / 128)], y
+    [tokens, out]: tensors with contiguous rows, or addresses (then ntokens, and the strides if rows are not dense);
+    weights and weight_scales as ar_qexperts_quantize makes them; ends: int32 on the device."""
+    i = _info_of(_qexperts_info, _QExpertsInfo, lib().ar_qexperts_prepare, plan)
+    n = _tokens(x, ntokens, "x")
+    xp, xs = _matrix(i, x, x_stride, n, i.inf, "codes", "x")
+    sp, ss = _matrix(i, x_scales, x_scales_stride, n, _blocks(i.inf), "scales", "x_scales")
+    yp, ys = _matrix(i, y, y_stride, n, i.outf, i.elem, "y")
+    if _lib.ar_qexperts_forward(plan, xp, xs, sp, ss, _vector(i, weights, i.arena, "codes", "weights"),
+                                _vector(i, weight_scales, i.scales, "scales", "weight_scales"), yp, ys, _ends(i, ends),
+                                n, _stream(stream)) != AR_OK:
+        _raise()
+
+
+def ar_qexperts_input_grad(plan, dy, dy_scales, weights, weight_scales, dx, ends, stream=None, ntokens=None,
+                           dy_stride=None, dy_scales_stride=None, dx_stride=None):
+    """dx[t] = W_e^T dy[t] for the rows t of expert e (arguments as ar_qexperts_forward's; dy_scales [tokens, ceil(out
+    / 128)])."""
+    i = _info_of(_qexperts_info, _QExpertsInfo, lib().ar_qexperts_prepare, plan)
+    n = _tokens(dy, ntokens, "dy")
+    dp, ds = _matrix(i, dy, dy_stride, n, i.outf, "codes", "dy")
+    sp, ss = _matrix(i, dy_scales, dy_scales_stride, n, _blocks(i.outf), "scales", "dy_scales")
+    xp, xs = _matrix(i, dx, dx_stride, n, i.inf, i.elem, "dx")
+    if _lib.ar_qexperts_input_grad(plan, dp, ds, sp, ss, _vector(i, weights, i.arena, "codes", "weights"),
+                                   _vector(i, weight_scales, i.scales, "scales", "weight_scales"), xp, xs,
+                                   _ends(i, ends), n, _stream(stream)) != AR_OK:
+        _raise()
+
+
+def ar_qexperts_destroy(plan):
+    _qexperts_info.pop(plan, None)
+    lib().ar_qexperts_destroy(plan)

@@ -6,6 +6,7 @@
 
 #include <cstdint>
 #include <cstring>
+#include <new>
 #include <string>
 #include <vector>
 
@@ -54,5 +55,46 @@ hipError_t upload(void *dst, const void *src, size_t bytes);
 hipError_t device_table(void **dst, const void *src, size_t bytes);
 // AR_ERR_INVALID_ARG while the caller captures s: a plan cannot be prepared then.
 ar_status_t refuse_capture(hipStream_t s);
+
+// Runs f, turning a failed host allocation into a status.
+template <class F>
+ar_status_t guarded(F f) {
+  try {
+    return f();
+  } catch (const std::bad_alloc &) {
+    return fail(AR_ERR_OOM, "host allocation failed");
+  }
+}
+
+inline bool float_type(int32_t d) { return d == AR_FLOAT32 || d == AR_BFLOAT16; }
+
+// [p, p + n) and [q, q + m) share a byte.
+inline bool overlap(const void *p, int64_t n, const void *q, int64_t m) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return n > 0 && m > 0 && a < b + static_cast<uint64_t>(m) && b < a + static_cast<uint64_t>(n);
+}
+
+inline bool on(const void *p, uintptr_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
+
+constexpr int64_t kMaxStride = 1 << 22;
+
+// A matrix of `rows` rows of `features` elements, `stride` apart.
+struct RowsArg {
+  const void *p;
+  size_t stride;
+  int64_t features;
+  const char *name;
+};
+
+inline ar_status_t check_rows(const RowsArg &r, int64_t rows, int64_t elem, int64_t *bytes) {
+  *bytes = 0;
+  if (r.stride < static_cast<size_t>(r.features) || r.stride > static_cast<size_t>(kMaxStride))
+    return fail(AR_ERR_INVALID_ARG, std::string(r.name) + ": row stride must be from its features to 2^22");
+  if (rows == 0) return AR_OK;
+  if (!r.p) return fail(AR_ERR_INVALID_ARG, std::string(r.name) + " is NULL");
+  if (!on(r.p, elem)) return fail(AR_ERR_INVALID_ARG, std::string(r.name) + " is not aligned to its elements");
+  *bytes = ((rows - 1) * static_cast<int64_t>(r.stride) + r.features) * elem;
+  return AR_OK;
+}
 
 }  // namespace ar_host

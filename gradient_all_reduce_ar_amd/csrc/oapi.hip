@@ -14,9 +14,15 @@
 #include "kernels.hpp"
 #include "operators.hpp"
 
+using ar_host::check_rows;
 using ar_host::fail;
+using ar_host::float_type;
+using ar_host::guarded;
 using ar_host::hip_fail;
+using ar_host::on;
+using ar_host::overlap;
 using ar_host::raw_enum;
+using ar_host::RowsArg;
 
 namespace ar_host {
 
@@ -122,17 +128,9 @@ struct ar_experts {
 
 namespace {
 
-constexpr int64_t kMaxFeatures = 1 << 22, kMaxStride = 1 << 22;
+constexpr int64_t kMaxFeatures = 1 << 22;
 // rows are counted in int32, rounded up to whole tiles and parts
 constexpr size_t kMaxTokens = (size_t{1} << 31) - 65536;
-
-// [p, p + n) and [q, q + m) share a byte.
-bool overlap(const void *p, int64_t n, const void *q, int64_t m) {
-  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-  return n > 0 && m > 0 && a < b + static_cast<uint64_t>(m) && b < a + static_cast<uint64_t>(n);
-}
-
-bool on(const void *p, uintptr_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
 
 ar_status_t prepare(ar_experts *ex) {
   int dev = 0;
@@ -149,25 +147,6 @@ ar_status_t prepare(ar_experts *ex) {
     return e == hipErrorOutOfMemory ? fail(AR_ERR_OOM, "expert workspace allocation") : hip_fail(e, "expert tables");
   }
   ex->device = dev;
-  return AR_OK;
-}
-
-// A matrix of `rows` rows of `features` elements, `stride` apart.
-struct RowsArg {
-  const void *p;
-  size_t stride;
-  int64_t features;
-  const char *name;
-};
-
-ar_status_t check_rows(const RowsArg &r, int64_t rows, int64_t elem, int64_t *bytes) {
-  *bytes = 0;
-  if (r.stride < static_cast<size_t>(r.features) || r.stride > static_cast<size_t>(kMaxStride))
-    return fail(AR_ERR_INVALID_ARG, std::string(r.name) + ": row stride must be from its features to 2^22");
-  if (rows == 0) return AR_OK;
-  if (!r.p) return fail(AR_ERR_INVALID_ARG, std::string(r.name) + " is NULL");
-  if (!on(r.p, elem)) return fail(AR_ERR_INVALID_ARG, std::string(r.name) + " is not aligned to its elements");
-  *bytes = ((rows - 1) * static_cast<int64_t>(r.stride) + r.features) * elem;
   return AR_OK;
 }
 
@@ -253,18 +232,6 @@ ar_status_t run(ar_experts *ex, ExpertProduct which, const RowsArg &r1, const Ro
     return fail(AR_ERR_UNSUPPORTED, "expert product larger than one launch grid");
   return e == hipSuccess ? AR_OK : hip_fail(e, "kernel launch");
 }
-
-// Runs f, turning a failed host allocation into a status.
-template <class F>
-ar_status_t guarded(F f) {
-  try {
-    return f();
-  } catch (const std::bad_alloc &) {
-    return fail(AR_ERR_OOM, "host allocation failed");
-  }
-}
-
-bool float_type(int32_t d) { return d == AR_FLOAT32 || d == AR_BFLOAT16; }
 
 }  // namespace
 

@@ -1,5 +1,6 @@
 // operators.hpp -- interface between the C ABI and the kernels of the expert
-// products and of the Muon update.
+// products (in their own types and in 8 bits), of the RMS norm, of gradient
+// clipping and of the Muon update.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -140,5 +141,97 @@ hipError_t muon_begin(const MuonArgs &a, const MuonSteps &k, hipStream_t s);
 hipError_t muon_gram(const MuonArgs &a, const MuonStep &k, hipStream_t s);
 hipError_t muon_poly(const MuonArgs &a, const MuonStep &k, hipStream_t s);
 hipError_t muon_apply(const MuonArgs &a, const MuonStep &k, hipStream_t s);
+
+// ---- The global gradient norm and clipping (clip.hip)
+
+// A run of one tensor's elements, which one wave works on.
+struct NormChunk {
+  int64_t at;
+  int32_t count, tensor;
+};
+constexpr int kNormWaves = 8;  // chunks, a wave each, of a workgroup
+
+struct NormArgs {
+  const void *g;
+  void *out;
+  const NormChunk *chunks;
+  const int32_t *first;   // [tensors + 1] first chunk of each tensor
+  double *chunk_sums;     // [chunks] sums of squares
+  double *group_sums;     // [workgroups]
+  uint32_t *arrived;      // workgroups that are done; zero between calls
+  float *norm;
+  float *tensor_norms;    // or NULL
+  double scale, max_norm;
+  int32_t nchunks, ntensors;
+  bool bf16;
+};
+hipError_t grad_norm(const NormArgs &a, hipStream_t s);
+hipError_t grad_clip(const NormArgs &a, hipStream_t s);
+
+// ---- 8-bit rows and the RMS norm (rmsnorm.hip)
+
+constexpr int kQBlock8 = 128;  // elements of a scale
+
+struct QuantArgs {
+  const void *x;
+  uint8_t *codes, *scales;
+  int64_t features, tokens, xs, cs, ss;  // strides of x, codes and scales
+  bool bf16;
+};
+hipError_t quantize_rows(const QuantArgs &a, hipStream_t s);
+
+struct RmsForward {
+  const void *x, *r, *gain;
+  void *h, *y;
+  uint8_t *codes, *scales;
+  float *rstd;
+  int64_t xs, rs, hs, ys, cs, ss, tokens;
+  int32_t features;
+  double eps;
+  bool bf16, gain_bf16;
+};
+hipError_t rmsnorm_forward(const RmsForward &a, hipStream_t s);
+
+struct RmsBackward {
+  const void *dy, *h, *dh, *gain;
+  const float *rstd;
+  void *dx, *dgain;
+  float *parts;  // [parts][features] sums of dgain
+  int64_t dys, hs, dhs, dxs, tokens;
+  int32_t features;
+  int32_t max_parts;
+  bool bf16, gain_bf16, grad_bf16, accumulate;
+};
+hipError_t rmsnorm_backward(const RmsBackward &a, hipStream_t s);
+// Parts that a plan of such rows has room for.
+int32_t rmsnorm_parts(int64_t features);
+
+// ---- 8-bit products grouped by expert (qexperts.hip)
+
+struct QExpertArgs {
+  const uint8_t *x, *w;         // codes: rows, weights
+  const uint8_t *x_scales, *w_scales;
+  void *out;
+  const int64_t *offsets;       // [experts] first element of expert e's matrix
+  const int32_t *ends;          // [experts]
+  int64_t tokens, in, outf;
+  int64_t xs, xss, outs;        // elements between rows of x, of its scales, of out
+  int32_t experts;
+  bool bf16;                    // element type of out
+  bool aligned;                 // every row and matrix of codes starts on 16 bytes
+};
+hipError_t qexperts_forward(const QExpertArgs &a, hipStream_t s);
+hipError_t qexperts_input_grad(const QExpertArgs &a, hipStream_t s);
+ExpertShape qexperts_shape(const QExpertArgs &a, ExpertProduct product);
+
+struct QWeightArgs {
+  const void *w;
+  uint8_t *codes, *scales;
+  const int64_t *offsets;
+  int64_t in, outf;
+  int32_t experts;
+  bool bf16;
+};
+hipError_t qexperts_quantize(const QWeightArgs &a, hipStream_t s);
 
 }  // namespace ar_dev

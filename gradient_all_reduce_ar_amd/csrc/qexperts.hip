@@ -1,0 +1,550 @@
+// qexperts.hip -- matrix products grouped by expert on 8-bit rows and weights
+// with a power of two for each block of 128 (gfx950): forward and input
+// gradient of a mixture of experts' linear layers, and the quantisation of the
+// weights.
+//
+//   forward      y[t, o]  = sum over blocks b of 2^(sx[t,b] + sw[o/128,b] - 254) sum_{i in b} qx[t,i] qw[o,i]
+//   input grad   dx[t, i] = the same over o, with sw[b,i/128]
+//
+// A stage of the contraction is one block of 128: one matrix instruction
+// (16x16x128) of two fragments, which takes each lane's scale byte of either
+// operand with it, so the scales cost no arithmetic.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <type_traits>
+
+#include "grouped.hpp"
+#include "kernels.hpp"
+#include "operators.hpp"
+#include "rows.hpp"
+#include "tiles.hpp"
+
+namespace ar_dev {
+namespace {
+
+// 32 codes of one row or column: contraction elements 16 g .. and 64 + 16 g ..
+// (g: the lane's group of 16), in this order in both operands.
+struct Frag8 {
+  ux4 v[2];
+};
+
+// Sums of 128 products and c.  The 8-bit instruction lines its products up
+// with the largest and keeps about 17 bits below it: 1.5e-5 of the result on
+// normal inputs, where rounding to bf16 takes 1.7e-3; it runs at twice the
+// rate of the 16-bit ones.
+__device__ __forceinline__ fx4 mfma8(const Frag8 &a, const Frag8 &b, fx4 c, int sa, int sb) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(__builtin_bit_cast(ix8, a), __builtin_bit_cast(ix8, b), c, 0,
+                                                          0, 0, sa, 0, sb);
+}
+
+// fp32 results: the codes as bf16, which holds them exactly, so that the
+// products are exact and their sums fp32; a block's sum takes its scales then.
+struct Wide8 {
+  s16x8 v[4];
+};
+__device__ __forceinline__ Wide8 widen8(const Frag8 &f) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  Wide8 w;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t u[4];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const uint32_t q = f.v[i >> 1][(i & 1) * 2 + j];
+      u[2 * j] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q, 1.0f, false));
+      u[2 * j + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q, 1.0f, true));
+    }
+    __builtin_memcpy(&w.v[i], u, 16);
+  }
+  return w;
+}
+__device__ __forceinline__ fx4 mfma_wide(const Wide8 &a, const Wide8 &b, fx4 c, int sa, int sb) {
+  fx4 z = {0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) z = mfma16<kBF16>(a.v[i], b.v[i], z);
+  const bool nan = sa == 255 || sb == 255;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) c[i] += nan ? __builtin_nanf("") : __builtin_ldexpf(z[i], sa + sb - 254);
+  return c;
+}
+
+// A matrix of scales: byte (row, block) at base + row * by_row + block * by_block.
+struct Scales {
+  const uint8_t *base;
+  int64_t by_row, by_block;
+  int rows;    // that exist (those beyond take the last one's)
+  int blocks;  // of the contraction
+};
+
+// The tile product of 8-bit operands: Operand's stages, in one loop (of the
+// loops that TileProduct has, those of smaller tiles), with the scales of 32
+// blocks at a time beside them in the LDS.
+template <bool EXACT, class S, Major BMJ, bool ALIGNED>
+struct TileProduct8 {
+  using Sh = S;
+  using OpA = Operand<kF8, kMajorK, S::BM, S::kThreads, ALIGNED>;
+  using OpB = Operand<kF8, BMJ, S::BN, S::kThreads, ALIGNED>;
+  static constexpr int kStep = 128;
+  static constexpr int kStage = OpA::kBytes + OpB::kBytes;
+  static constexpr int kStages = ALIGNED ? S::kStages : 2;
+  // Scales: rows of 32 bytes, 36 apart, so that 16 rows' bytes lie in
+  // different banks; the tile's rows, then its blocks of columns.
+  static constexpr int kChunk = 32, kPitch = 36, kColBlocks = (S::BN + 127) / 128;
+  static constexpr int kScales = (S::BM + kColBlocks) * kPitch;
+  static constexpr int kLds = kStages * kStage + (kScales + 15) / 16 * 16;
+  fx4 acc[S::FM][S::FN];
+  OpA oa;
+  OpB ob;
+  int k, at, per;  // stage `at` of `per` is loaded next
+
+  __device__ __forceinline__ void next() {
+    if (++at < per) {
+      oa.advance();
+      ob.advance();
+    }
+  }
+  __device__ __forceinline__ void load(uint32_t stage) {
+    const int n = k - at * kStep;
+    if (n < kStep) {
+      oa.cut(n);
+      ob.cut(n);
+    }
+    oa.load(stage);
+    ob.load(stage + OpA::kBytes);
+    next();
+  }
+  __device__ __forceinline__ void fetch(int set) {
+    oa.fetch(set, k - at * kStep);
+    ob.fetch(set, k - at * kStep);
+    next();
+  }
+  __device__ __forceinline__ void land(int set, char *stage) {
+    oa.land(set, stage);
+    ob.land(set, stage + OpA::kBytes);
+  }
+
+  // Scales of blocks b0 .. b0 + 31 to the LDS (those that exist).
+  static __device__ __forceinline__ void scales_to_lds(char *lds, const Scales &sa, const Scales &sb, int b0) {
+    constexpr int kUnits = S::BM * (kChunk / 4);
+    const int n = min(kChunk, sa.blocks - b0);
+#pragma unroll
+    for (int u0 = 0; u0 < kUnits; u0 += S::kThreads) {
+      const int u = u0 + static_cast<int>(threadIdx.x), row = u / (kChunk / 4), b = u % (kChunk / 4) * 4;
+      if (b >= n || row >= S::BM) continue;
+      const uint8_t *p = sa.base + min(row, sa.rows - 1) * sa.by_row + b0 + b;
+      uint32_t v = 0;
+      if (b + 4 <= n) {
+        __builtin_memcpy(&v, p, 4);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+          if (b + i < n) v |= static_cast<uint32_t>(p[i]) << (8 * i);
+      }
+      *reinterpret_cast<uint32_t *>(lds + row * kPitch + b) = v;
+    }
+    const int c = threadIdx.x / kChunk, b = threadIdx.x % kChunk;
+    if (c < kColBlocks && b < n)
+      lds[(S::BM + c) * kPitch + b] = static_cast<char>(sb.base[min(c, sb.rows - 1) * sb.by_row + (b0 + b) * sb.by_block]);
+  }
+
+  // The products of the stage at sa, block b of the chunk.
+  __device__ __forceinline__ void multiply(const char *sa, const char *scales, int b, int rm, int rn) {
+    const char *sb = sa + OpA::kBytes;
+    const int lane = threadIdx.x & 63;
+    const int colscale = static_cast<uint8_t>(scales[(S::BM + rn / 128) * kPitch + b]);
+    auto a_of = [&](int i) { return Frag8{{OpA::fragment(sa, rm + i * 16, 0), OpA::fragment(sa, rm + i * 16, 1)}}; };
+    auto scale_of = [&](int i) { return static_cast<int>(static_cast<uint8_t>(scales[(rm + i * 16 + (lane & 15)) * kPitch + b])); };
+    if constexpr (EXACT) {
+      Wide8 fb[S::FN];
+#pragma unroll
+      for (int j = 0; j < S::FN; ++j)
+        fb[j] = widen8(Frag8{{OpB::fragment(sb, rn + j * 16, 0), OpB::fragment(sb, rn + j * 16, 1)}});
+#pragma unroll
+      for (int i = 0; i < S::FM; ++i) {
+        const Wide8 fa = widen8(a_of(i));
+        const int s = scale_of(i);
+#pragma unroll
+        for (int j = 0; j < S::FN; ++j) acc[i][j] = mfma_wide(fb[j], fa, acc[i][j], colscale, s);
+      }
+    } else {
+      Frag8 fa[S::FM], fb[S::FN];
+      int s[S::FM];
+#pragma unroll
+      for (int j = 0; j < S::FN; ++j) fb[j] = Frag8{{OpB::fragment(sb, rn + j * 16, 0), OpB::fragment(sb, rn + j * 16, 1)}};
+#pragma unroll
+      for (int i = 0; i < S::FM; ++i) {
+        fa[i] = a_of(i);
+        s[i] = scale_of(i);
+      }
+#pragma unroll
+      for (int i = 0; i < S::FM; ++i)
+#pragma unroll
+        for (int j = 0; j < S::FN; ++j) acc[i][j] = mfma8(fb[j], fa[i], acc[i][j], colscale, s[i]);
+    }
+  }
+
+  __device__ __forceinline__ void run(char *lds, const uint8_t *a, const uint8_t *b, int64_t lda, int64_t ldb, int validm,
+                                      int validn, int length, const Scales &sa, const Scales &sb) {
+#pragma unroll
+    for (int i = 0; i < S::FM; ++i)
+#pragma unroll
+      for (int j = 0; j < S::FN; ++j) acc[i][j] = fx4{0, 0, 0, 0};
+    k = length;
+    at = 0;
+    per = (k + kStep - 1) / kStep;
+    oa.init(a, lda, validm);
+    ob.init(b, ldb, validn);
+    if constexpr (ALIGNED) direct(lds, per, sa, sb);
+    else through_registers(lds, per, sa, sb);
+  }
+
+  __device__ __forceinline__ void direct(char *lds, int steps, const Scales &sa, const Scales &sb) {
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int rm = wave / S::WN * (S::BM / S::WM), rn = wave % S::WN * (S::BN / S::WN);
+    const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_offset(lds));
+    char *scales = lds + kStages * kStage;
+    constexpr int kAhead = kStages - 1;  // stages in flight when a step begins
+    constexpr int kLoads = OpA::kPer + OpB::kPer;
+    for (int i = 0; i < kAhead && i < steps; ++i) load(lds0 + i * kStage);
+    scales_to_lds(scales, sa, sb, 0);
+    int buf = 0, to = kAhead;  // stage read, stage loaded
+    for (int t = 0; t < steps; ++t) {
+      if (kAhead > 1 && t + kAhead <= steps) {  // all but the newest kAhead - 1 stages have landed
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((kAhead - 1) * kLoads) : "memory");
+      } else {
+        loads_done_and_meet();
+      }
+      if (t + kAhead < steps) load(lds0 + to * kStage);
+      if (t > 0 && t % kChunk == 0) {
+        scales_to_lds(scales, sa, sb, t);
+        __syncthreads();
+      }
+      multiply(lds + buf * kStage, scales, t % kChunk, rm, rn);
+      buf = buf + 1 == kStages ? 0 : buf + 1;
+      to = to + 1 == kStages ? 0 : to + 1;
+    }
+    __syncthreads();
+  }
+
+  // Operands that are not aligned: as TileProduct's.
+  __device__ __forceinline__ void through_registers(char *lds, int steps, const Scales &sa, const Scales &sb) {
+    constexpr int kSets = OpA::kSets < OpB::kSets ? OpA::kSets : OpB::kSets;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int rm = wave / S::WN * (S::BM / S::WM), rn = wave % S::WN * (S::BN / S::WN);
+    char *scales = lds + kStages * kStage;
+#pragma unroll
+    for (int i = 0; i < kSets; ++i)
+      if (i < steps) fetch(i);
+    scales_to_lds(scales, sa, sb, 0);
+    land(0, lds);
+    auto step = [&](int t, auto set) {
+      constexpr int cur = decltype(set)::value, nxt = (cur + 1) % kSets;
+      __syncthreads();
+      if (t > 0 && t % kChunk == 0) {
+        scales_to_lds(scales, sa, sb, t);
+        __syncthreads();
+      }
+      if (t + kSets < steps) fetch(cur);
+      multiply(lds + (t & 1) * kStage, scales, t % kChunk, rm, rn);
+      if (t + 1 < steps) land(nxt, lds + (t + 1 & 1) * kStage);
+    };
+    for (int t = 0; t < steps; t += kSets) {
+      step(t, std::integral_constant<int, 0>{});
+      if constexpr (kSets == 3) {
+        if (t + 1 < steps) step(t + 1, std::integral_constant<int, 1>{});
+        if (t + 2 < steps) step(t + 2, std::integral_constant<int, 2>{});
+      }
+    }
+    __syncthreads();
+  }
+};
+
+__device__ __forceinline__ int64_t blocks_of(int64_t n) { return (n + kQBlock8 - 1) / kQBlock8; }
+
+// Forward (GRAD false: W_e as [n][k]) and input gradient (GRAD true: as [k][n]).
+template <class P, bool GRAD, bool BF>
+__global__ __launch_bounds__(P::Sh::kThreads) void qexperts_rows(QExpertArgs a) {
+  using S = typename P::Sh;
+  extern __shared__ __align__(16) char lds[];
+  const int64_t n = GRAD ? a.in : a.outf, k = GRAD ? a.outf : a.in;
+  const int nt = static_cast<int>((n + S::BN - 1) / S::BN);
+  RowTile t;
+  if (!find_row_tile<S::BM>(a, nt, t)) return;
+  const int64_t n0 = static_cast<int64_t>(t.tile_n) * S::BN, in_blocks = blocks_of(a.in);
+  const int validn = static_cast<int>(min(static_cast<int64_t>(S::BN), n - n0));
+  const uint8_t *w = a.w + table_entry(a.offsets + t.e) + (GRAD ? n0 : n0 * a.in);
+  const int64_t first = n0 / kQBlock8;  // block of columns
+  const uint8_t *ws = a.w_scales + t.e * (blocks_of(a.outf) * in_blocks) + (GRAD ? first : first * in_blocks);
+  const int kb = static_cast<int>(blocks_of(k));
+  P p;
+  p.run(lds, a.x + t.row * a.xs, w, a.xs, a.in, t.rows, validn, static_cast<int>(k),
+        Scales{a.x_scales + t.row * a.xss, a.xss, 1, t.rows, kb},
+        Scales{ws, GRAD ? 1 : in_blocks, GRAD ? in_blocks : 1, static_cast<int>(blocks_of(n) - first), kb});
+  using Out = TileOut<S, P::kLds>;
+  Out::all(lds, p.acc, [&](int pass, int tid) {
+    Out::rows(lds, pass, tid, [&](int m, int c, fx4 v) {
+      if (m < t.rows && c < validn) store4<BF>(a.out, (t.row + m) * a.outs + n0 + c, v, validn - c);
+    });
+  });
+}
+
+// Forward for few rows per expert (decoding): the time is that of reading each
+// active expert's weights once.  A workgroup takes 16 columns of one expert and
+// up to 32 of its rows; its 8 waves take turns at blocks of the contraction,
+// so that the workgroup reads 1 KiB of each of the 16 weight rows at a time,
+// straight into the registers that feed the matrix instructions (lane l holds
+// 32 bytes of row l % 16), and the waves' sums are added in LDS in a fixed
+// order.
+constexpr int kFewWaves8 = 8, kFewRows8 = 32, kFewCols8 = 16;
+
+// The lane's 32 codes at p, of which the first n exist.
+template <bool WHOLE>
+__device__ __forceinline__ Frag8 load_codes(const uint8_t *p, int64_t n) {
+  Frag8 f;
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    f.v[c] = ux4{0, 0, 0, 0};
+    if (WHOLE || n >= (c + 1) * 16) {
+      __builtin_memcpy(&f.v[c], p + c * 16, 16);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (c * 16 + i < n) f.v[c][i >> 2] |= static_cast<uint32_t>(p[c * 16 + i]) << (8 * (i & 3));
+    }
+  }
+  return f;
+}
+
+template <bool EXACT>
+__device__ __forceinline__ fx4 add_block(const Frag8 &w, const Frag8 &x, fx4 c, int sw, int sx) {
+  if constexpr (EXACT) return mfma_wide(widen8(w), widen8(x), c, sw, sx);
+  else return mfma8(w, x, c, sw, sx);
+}
+
+template <bool EXACT>
+__global__ __launch_bounds__(64 * kFewWaves8) void qexperts_few(QExpertArgs a) {
+  __shared__ fx4 part[kFewWaves8][kFewRows8 / 16][64];
+  RowTile t;
+  if (!find_row_tile<kFewRows8>(a, static_cast<int>((a.outf + kFewCols8 - 1) / kFewCols8), t)) return;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, r = lane & 15;
+  const int64_t n0 = static_cast<int64_t>(t.tile_n) * kFewCols8, own = (lane >> 4) * 32;
+  const int64_t blocks = blocks_of(a.in);
+  // rows and columns that do not exist repeat the last one; not stored
+  const uint8_t *w = a.w + table_entry(a.offsets + t.e) + min(n0 + r, a.outf - 1) * a.in + own;
+  const uint8_t *ws = a.w_scales + (t.e * blocks_of(a.outf) + n0 / kQBlock8) * blocks;
+  const int64_t row0 = t.row + min(r, t.rows - 1), row1 = t.row + min(r + 16, t.rows - 1);
+  const uint8_t *x0 = a.x + row0 * a.xs + own, *x1 = a.x + row1 * a.xs + own;
+  const uint8_t *s0 = a.x_scales + row0 * a.xss, *s1 = a.x_scales + row1 * a.xss;
+  const bool two = t.rows > 16;
+  fx4 acc[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+  const int64_t whole = a.in / kQBlock8;
+  constexpr int kBatch = 4;  // blocks in flight per wave
+  int64_t b = wave;
+  auto work = [&](auto n) {
+    constexpr int N = decltype(n)::value;
+    Frag8 fw[N], f0[N], f1[N];
+    int sw[N], sx0[N], sx1[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int64_t at = b + i * kFewWaves8;
+      fw[i] = load_codes<true>(w + at * kQBlock8, 0);
+      sw[i] = ws[at];
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int64_t at = b + i * kFewWaves8;
+      f0[i] = load_codes<true>(x0 + at * kQBlock8, 0);
+      sx0[i] = s0[at];
+    }
+    if (two) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int64_t at = b + i * kFewWaves8;
+        f1[i] = load_codes<true>(x1 + at * kQBlock8, 0);
+        sx1[i] = s1[at];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) acc[0] = add_block<EXACT>(fw[i], f0[i], acc[0], sw[i], sx0[i]);
+    if (two) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) acc[1] = add_block<EXACT>(fw[i], f1[i], acc[1], sw[i], sx1[i]);
+    }
+    b += N * kFewWaves8;
+  };
+  while (b + (kBatch - 1) * kFewWaves8 < whole) work(std::integral_constant<int, kBatch>{});
+  while (b < whole) work(std::integral_constant<int, 1>{});
+  if (b == whole && whole < blocks) {  // the block that the rows end in
+    const int64_t at = whole * kQBlock8, left = a.in - at - own;
+    const Frag8 fw = load_codes<false>(w + at, left);
+    acc[0] = add_block<EXACT>(fw, load_codes<false>(x0 + at, left), acc[0], ws[whole], s0[whole]);
+    if (two) acc[1] = add_block<EXACT>(fw, load_codes<false>(x1 + at, left), acc[1], ws[whole], s1[whole]);
+  }
+  part[wave][0][lane] = acc[0];
+  part[wave][1][lane] = acc[1];
+  __syncthreads();
+  if (wave > 1) return;
+  fx4 v = part[0][wave][lane];
+#pragma unroll
+  for (int i = 1; i < kFewWaves8; ++i) {
+    const fx4 u = part[i][wave][lane];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] += u[e];
+  }
+  const int m = wave * 16 + r, left = static_cast<int>(min(static_cast<int64_t>(4), a.outf - n0 - (lane >> 4) * 4));
+  if (m < t.rows && left > 0) store4<!EXACT>(a.out, (t.row + m) * a.outs + n0 + (lane >> 4) * 4, v, left);
+}
+
+// A workgroup takes one 128 x 128 block at a time: 16 lanes to a row, 16 rows
+// to a pass, all of it in registers between its maximum and its codes.
+constexpr int kQuantThreads8 = 256, kPasses8 = kQBlock8 / (kQuantThreads8 / 16);
+template <bool BF>
+__global__ __launch_bounds__(kQuantThreads8) void quantize_weights(QWeightArgs a) {
+  __shared__ uint32_t tops[2][kQuantThreads8 / 64];
+  const int64_t ib = blocks_of(a.in), per = ib * blocks_of(a.outf), total = per * a.experts;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int c = (threadIdx.x & 15) * kLane, r0 = threadIdx.x >> 4;
+  int parity = 0;
+  for (int64_t id = blockIdx.x; id < total; id += gridDim.x, parity ^= 1) {
+    const int64_t e = id / per, bo = (id - e * per) / ib, bi = id - e * per - bo * ib;
+    const int64_t start = table_entry(a.offsets + e) + bo * kQBlock8 * a.in + bi * kQBlock8 + c;
+    const int n = static_cast<int>(min(static_cast<int64_t>(kQBlock8), a.in - bi * kQBlock8)) - c;
+    const int rows = static_cast<int>(min(static_cast<int64_t>(kQBlock8), a.outf - bo * kQBlock8));
+    Raw8<BF> x[kPasses8];
+#pragma unroll
+    for (int p = 0; p < kPasses8; ++p) {
+      const int r = p * (kQuantThreads8 / 16) + r0;
+      x[p] = load8<BF>(a.w, start + r * a.in, r < rows ? n : 0);
+    }
+    uint32_t top = 0;
+#pragma unroll
+    for (int p = 0; p < kPasses8; ++p) {
+      float v[kLane];
+#pragma unroll
+      for (int i = 0; i < kLane; ++i) v[i] = x[p][i];
+      top = max(top, top_of(v));
+    }
+    top = row16_max(top);
+    top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 16)));
+    top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 32)));
+    if (lane == 0) tops[parity][wave] = top;
+    __syncthreads();  // (two blocks in a row use different slots)
+#pragma unroll
+    for (int i = 0; i < kQuantThreads8 / 64; ++i) top = max(top, tops[parity][i]);
+    const uint32_t byte = scale_byte(top);
+    if (threadIdx.x == 0) a.scales[id] = static_cast<uint8_t>(byte);
+#pragma unroll
+    for (int p = 0; p < kPasses8; ++p) {
+      const int r = p * (kQuantThreads8 / 16) + r0;
+      float v[kLane];
+#pragma unroll
+      for (int i = 0; i < kLane; ++i) v[i] = x[p][i];
+      if (r < rows && n > 0) store_codes(a.codes + start + r * a.in, codes8(v, byte), n);
+    }
+  }
+}
+
+// Tiles.
+using Big = Shape<256, 256, 2, 4>;
+using Square = Shape<128, 128, 2, 2>;
+using Half = Shape<64, 128, 2, 2>;
+using Small = Shape<32, 64, 1, 4, 4>;
+
+template <class S, bool GRAD>
+int64_t row_tiles(const QExpertArgs &a) {
+  const int64_t n = GRAD ? a.in : a.outf;
+  return (a.tokens / S::BM + std::min<int64_t>(a.experts, a.tokens)) * ((n + S::BN - 1) / S::BN);
+}
+
+template <bool EXACT, class S, bool GRAD, bool ALIGNED>
+hipError_t launch_rows(const QExpertArgs &a, hipStream_t s) {
+  using P = TileProduct8<EXACT, S, GRAD ? kMajorMN : kMajorK, ALIGNED>;
+  return launch(qexperts_rows<P, GRAD, !EXACT>, row_tiles<S, GRAD>(a), 1, S::kThreads, P::kLds, s, a);
+}
+
+template <class S, bool GRAD>
+hipError_t launch_rows(const QExpertArgs &a, hipStream_t s) {
+  if constexpr (S::BM >= 256) {  // aligned, 16-bit results alone
+    return launch_rows<false, S, GRAD, true>(a, s);
+  } else {
+    if (a.aligned) return a.bf16 ? launch_rows<false, S, GRAD, true>(a, s) : launch_rows<true, S, GRAD, true>(a, s);
+    return a.bf16 ? launch_rows<false, S, GRAD, false>(a, s) : launch_rows<true, S, GRAD, false>(a, s);
+  }
+}
+
+struct TileCost {
+  double slots, alone, full, rest;
+};
+constexpr TileCost kBF16Cost[4] = {{256, 1.3, 1.45, 12}, {512, 0.65, 1.05, 5}, {768, 0.55, 0.98, 4}, {768, 0.4, 0.45, 3.5}};
+constexpr TileCost kF32Cost[4] = {{}, {512, 2.5, 3.0, 5}, {768, 1.6, 2.5, 4}, {768, 0.9, 1.2, 3.5}};
+
+template <class S, bool GRAD>
+double rows_time(const QExpertArgs &a, const TileCost &c) {
+  const double n = static_cast<double>(GRAD ? a.in : a.outf), steps = static_cast<double>(GRAD ? a.outf : a.in) / 128;
+  const double e = static_cast<double>(std::min<int64_t>(a.experts, a.tokens)), t = static_cast<double>(a.tokens);
+  // every expert ends inside a tile, half of it unused on average
+  const double tiles = std::max(e, t / S::BM + e / 2) * std::ceil(n / S::BN);
+  double rounds = tiles / c.slots;
+  rounds = rounds < 2 || c.slots <= 256 ? std::ceil(rounds) : rounds + 0.5;
+  return rounds * (std::ceil(steps) * (tiles <= 256 ? c.alone : c.full) + c.rest);
+}
+
+enum Choice { kBig, kSquare, kHalf, kSmall, kFew };
+
+template <bool GRAD>
+Choice rows_choice(const QExpertArgs &a) {
+  if constexpr (!GRAD) {
+    const int64_t e = a.experts, bytes = std::min(e, a.tokens) * a.in * a.outf;
+    if (a.tokens <= 16 * e && bytes <= 16 << 20) return kFew;
+  }
+  const TileCost *c = a.bf16 ? kBF16Cost : kF32Cost;
+  const double big = a.aligned && a.bf16 ? rows_time<Big, GRAD>(a, c[0]) : 1e300;
+  const double square = rows_time<Square, GRAD>(a, c[1]), half = rows_time<Half, GRAD>(a, c[2]);
+  const double small = rows_time<Small, GRAD>(a, c[3]);
+  if (big <= std::min({square, half, small})) return kBig;
+  if (square <= std::min(half, small)) return kSquare;
+  return half <= small ? kHalf : kSmall;
+}
+
+template <bool GRAD>
+hipError_t rows(const QExpertArgs &a, hipStream_t s) {
+  switch (rows_choice<GRAD>(a)) {
+    case kBig: return launch_rows<Big, GRAD>(a, s);
+    case kSquare: return launch_rows<Square, GRAD>(a, s);
+    case kHalf: return launch_rows<Half, GRAD>(a, s);
+    case kSmall: return launch_rows<Small, GRAD>(a, s);
+    case kFew: break;
+  }
+  if constexpr (GRAD) return hipErrorInvalidValue;  // not chosen
+  const int64_t grid = (a.tokens / kFewRows8 + std::min<int64_t>(a.experts, a.tokens)) * ((a.outf + kFewCols8 - 1) / kFewCols8);
+  return a.bf16 ? launch(qexperts_few<false>, grid, 1, 64 * kFewWaves8, 0, s, a)
+                : launch(qexperts_few<true>, grid, 1, 64 * kFewWaves8, 0, s, a);
+}
+
+}  // namespace
+
+hipError_t qexperts_forward(const QExpertArgs &a, hipStream_t s) { return rows<false>(a, s); }
+hipError_t qexperts_input_grad(const QExpertArgs &a, hipStream_t s) { return rows<true>(a, s); }
+
+ExpertShape qexperts_shape(const QExpertArgs &a, ExpertProduct product) {
+  switch (product == kExpertsForward ? rows_choice<false>(a) : rows_choice<true>(a)) {
+    case kBig: return {Big::BM, Big::BN, 1};
+    case kSquare: return {Square::BM, Square::BN, 1};
+    case kHalf: return {Half::BM, Half::BN, 1};
+    case kSmall: return {Small::BM, Small::BN, 1};
+    case kFew: break;
+  }
+  return {kFewRows8, kFewCols8, 1};
+}
+
+hipError_t qexperts_quantize(const QWeightArgs &a, hipStream_t s) {
+  const int64_t blocks = ((a.in + kQBlock8 - 1) / kQBlock8) * ((a.outf + kQBlock8 - 1) / kQBlock8) * a.experts;
+  const int64_t grid = std::min<int64_t>(blocks, 1 << 22);
+  return a.bf16 ? launch(quantize_weights<true>, grid, 1, kQuantThreads8, 0, s, a)
+                : launch(quantize_weights<false>, grid, 1, kQuantThreads8, 0, s, a);
+}
+
+}  // namespace ar_dev

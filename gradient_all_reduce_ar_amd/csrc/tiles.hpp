@@ -2,7 +2,9 @@
 // Newton-Schulz products share (gfx950, device code).
 //
 // One workgroup computes a BM x BN tile of C = A B over a contraction of
-// length k, both operands bf16, fp16 or fp32, sums in fp32.  Each operand lies
+// length k, both operands bf16, fp16 or fp32, sums in fp32 (operands of 8 bits,
+// whose products qexperts.hip forms, are staged in the same way: 128 elements
+// to a stage, which transposing reads of 8 x 16 bytes take across).  Each operand lies
 // in memory in one of two orders:
 //   kMajorK   row r of the tile is contiguous along the contraction
 //             (A[r][k]; for B: B given as its transpose, [n][k])
@@ -49,14 +51,16 @@ typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef float fx4 __attribute__((ext_vector_type(4)));
 typedef uint32_t ux4 __attribute__((ext_vector_type(4)));
 typedef uint32_t ux2 __attribute__((ext_vector_type(2)));
+typedef int32_t ix2 __attribute__((ext_vector_type(2)));
+typedef int32_t ix8 __attribute__((ext_vector_type(8)));
 
-enum Elem { kBF16, kF16, kF32 };
+enum Elem { kBF16, kF16, kF32, kF8 };
 enum Major { kMajorK, kMajorMN };
 template <Elem E>
-using ElemOf = std::conditional_t<E == kF32, float, uint16_t>;
+using ElemOf = std::conditional_t<E == kF32, float, std::conditional_t<E == kF8, uint8_t, uint16_t>>;
 // 16 bytes of contraction elements.
 template <Elem E>
-using Frag = std::conditional_t<E == kF32, fx4, s16x8>;
+using Frag = std::conditional_t<E == kF32, fx4, std::conditional_t<E == kF8, ux4, s16x8>>;
 constexpr int kStepK = 64;  // contraction elements of a stage, 16 bits
 
 __device__ __forceinline__ uint32_t lds_offset(const void *p) {
@@ -121,6 +125,15 @@ __device__ __forceinline__ constexpr int mn_swizzle(int k) {
   return W >= 128 ? ((k & 3) | ((k >> 3) & 1) << 2) : (((k >> 1) & 1) | ((k >> 3) & 1) << 1);
 }
 
+// The same for bytes, in 16-byte columns: half a wave reads one column of rows
+// k .. k + 7 and k + 16 .. k + 23, which lie in 16 different columns (or, rows
+// of 64 or 128 bytes going round the banks faster, as many as there are).
+template <int W>
+__device__ __forceinline__ constexpr int mn_swizzle8(int k) {
+  const int far = (k >> 4) & 1;
+  return W >= 256 ? ((k & 7) | far << 3) : W >= 128 ? (((k >> 1) & 3) | far << 2) : (((k >> 2) & 1) | far << 1);
+}
+
 template <Elem E>
 __device__ __forceinline__ fx4 mfma16(Frag<E> a, Frag<E> b, fx4 c) {
   if constexpr (E == kBF16) {
@@ -181,6 +194,7 @@ struct Operand {
       row = c / kRow;
       const int p = c % kRow;
       if constexpr (E == kF32) col = p ^ (row & 4);
+      else if constexpr (E == kF8) col = p ^ mn_swizzle8<W>(row);
       else col = (((p >> 1) ^ mn_swizzle<W>(row)) << 1) | (p & 1);
     }
   }
@@ -282,6 +296,18 @@ struct Operand {
       fx4 v;
 #pragma unroll
       for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const float *>(p + j * (W * 4));
+      return v;
+    } else if constexpr (E == kF8) {
+      ux4 v;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {  // 8 contraction elements each: a block of 8 x 16 bytes per 16 lanes
+        const int k = ks * 64 + (lane >> 4) * 16 + 8 * i + ((lane & 15) >> 1);
+        const char *p = stage + k * W + (((r >> 4) ^ mn_swizzle8<W>(k)) << 4) + (lane & 1) * 8;
+        const ux2 h = __builtin_bit_cast(
+            ux2, __builtin_amdgcn_ds_read_tr8_b64_v2i32((__attribute__((address_space(3))) ix2 *)const_cast<char *>(p)));
+        v[2 * i] = h[0];
+        v[2 * i + 1] = h[1];
+      }
       return v;
     } else {
       const int k = ks * 32 + (lane >> 4) * 8 + ((lane & 15) >> 2);
