@@ -45,6 +45,7 @@ __device__ __forceinline__ int wave_sum_to(int v) {  // inclusive prefix sum
 
 struct RowTile {
   int e, row, rows, tile_n;  // expert, first row, rows of the tile, column tile
+  int tile_m;                // row tile, of the expert's
 };
 
 // Workgroups go round the 8 XCDs (each with an L2 of its own) in turn, so
@@ -64,10 +65,11 @@ __device__ __forceinline__ void band_tile(int l, int mt, int nt, int &m, int &n)
   n = r / in;
 }
 
-// This workgroup's tile: of `nt` column tiles times the row tiles of all
-// experts, in runs of neighbours per XCD.
+// The tile of place `at`: of `nt` column tiles times the row tiles of all
+// experts, in runs of neighbours per XCD.  A workgroup's own place is its
+// number.
 template <int BM, class A>
-__device__ __forceinline__ bool find_row_tile(const A &a, int nt, RowTile &t) {
+__device__ __forceinline__ bool find_row_tile(const A &a, int nt, RowTile &t, int64_t at = blockIdx.x) {
   int carry = 0, lo, hi, total = 0;
   // the tiles up to and of this lane's expert, of the experts from e0 on
   auto scan = [&](int e0, int &mt, int &upto) {
@@ -79,8 +81,8 @@ __device__ __forceinline__ bool find_row_tile(const A &a, int nt, RowTile &t) {
   int mt, upto, batch = 0;
   for (int e0 = 0; e0 < a.experts; e0 += 64) total += batch = scan(e0, mt, upto);
   const int64_t tiles = static_cast<int64_t>(total) * nt;
-  if (blockIdx.x >= tiles) return false;
-  int64_t want = xcd_run(blockIdx.x, tiles);
+  if (at >= tiles) return false;
+  int64_t want = xcd_run(at, tiles);
   const bool again = a.experts > 64;  // the scan's registers hold the only batch otherwise
   carry = 0;
   for (int e0 = 0; e0 < a.experts; e0 += 64) {
@@ -99,6 +101,7 @@ __device__ __forceinline__ bool find_row_tile(const A &a, int nt, RowTile &t) {
     t.row = __builtin_amdgcn_readfirstlane(first);
     t.rows = __builtin_amdgcn_readfirstlane(min(BM, __shfl(hi, l) - first));
     t.tile_n = __builtin_amdgcn_readfirstlane(n);
+    t.tile_m = __builtin_amdgcn_readfirstlane(m);
     return true;
   }
   return false;

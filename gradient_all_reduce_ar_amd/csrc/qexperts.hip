@@ -46,7 +46,6 @@ struct Wide8 {
   s16x8 v[4];
 };
 __device__ __forceinline__ Wide8 widen8(const Frag8 &f) {
-  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
   Wide8 w;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -79,6 +78,39 @@ struct Scales {
   int blocks;  // of the contraction
 };
 
+// The scales of 32 blocks of a tile, in the LDS: rows of 32 bytes, 36 apart, so
+// that 16 rows' bytes lie in different banks; the tile's rows, then its blocks
+// of columns.
+constexpr int kScaleChunk = 32, kScalePitch = 36;
+template <int BM, int BN, int NT>
+struct ScaleChunk {
+  static constexpr int kColBlocks = (BN + 127) / 128, kUnits = BM * (kScaleChunk / 4);
+  static constexpr int kBytes = ((BM + kColBlocks) * kScalePitch + 15) / 16 * 16;
+
+  // Those of blocks b0 .. b0 + 31 that exist.
+  static __device__ __forceinline__ void move(char *lds, const Scales &sa, const Scales &sb, int b0) {
+    const int n = min(kScaleChunk, sa.blocks - b0);
+#pragma unroll
+    for (int u0 = 0; u0 < kUnits; u0 += NT) {
+      const int u = u0 + static_cast<int>(threadIdx.x), row = u / (kScaleChunk / 4), b = u % (kScaleChunk / 4) * 4;
+      if (b >= n || row >= BM) continue;
+      const uint8_t *p = sa.base + min(row, sa.rows - 1) * sa.by_row + b0 + b;
+      uint32_t v = 0;
+      if (b + 4 <= n) {
+        __builtin_memcpy(&v, p, 4);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+          if (b + i < n) v |= static_cast<uint32_t>(p[i]) << (8 * i);
+      }
+      *reinterpret_cast<uint32_t *>(lds + row * kScalePitch + b) = v;
+    }
+    const int c = threadIdx.x / kScaleChunk, b = threadIdx.x % kScaleChunk;
+    if (c < kColBlocks && b < n)
+      lds[(BM + c) * kScalePitch + b] = static_cast<char>(sb.base[min(c, sb.rows - 1) * sb.by_row + (b0 + b) * sb.by_block]);
+  }
+};
+
 // The tile product of 8-bit operands: Operand's stages, in one loop (of the
 // loops that TileProduct has, those of smaller tiles), with the scales of 32
 // blocks at a time beside them in the LDS.
@@ -90,17 +122,15 @@ struct TileProduct8 {
   static constexpr int kStep = 128;
   static constexpr int kStage = OpA::kBytes + OpB::kBytes;
   static constexpr int kStages = ALIGNED ? S::kStages : 2;
-  // Scales: rows of 32 bytes, 36 apart, so that 16 rows' bytes lie in
-  // different banks; the tile's rows, then its blocks of columns.
-  static constexpr int kChunk = 32, kPitch = 36, kColBlocks = (S::BN + 127) / 128;
-  static constexpr int kScales = (S::BM + kColBlocks) * kPitch;
-  static constexpr int kLds = kStages * kStage + (kScales + 15) / 16 * 16;
+  using Chunk = ScaleChunk<S::BM, S::BN, S::kThreads>;
+  static constexpr int kChunk = kScaleChunk, kPitch = kScalePitch, kScales = Chunk::kBytes;
+  static constexpr int kLds = kStages * kStage + kScales;
   fx4 acc[S::FM][S::FN];
   OpA oa;
   OpB ob;
   int k, at, per;  // stage `at` of `per` is loaded next
 
-  __device__ __forceinline__ void next() {
+  __device__ __forceinline__ void next_stage() {
     if (++at < per) {
       oa.advance();
       ob.advance();
@@ -114,40 +144,16 @@ struct TileProduct8 {
     }
     oa.load(stage);
     ob.load(stage + OpA::kBytes);
-    next();
+    next_stage();
   }
   __device__ __forceinline__ void fetch(int set) {
     oa.fetch(set, k - at * kStep);
     ob.fetch(set, k - at * kStep);
-    next();
+    next_stage();
   }
   __device__ __forceinline__ void land(int set, char *stage) {
     oa.land(set, stage);
     ob.land(set, stage + OpA::kBytes);
-  }
-
-  // Scales of blocks b0 .. b0 + 31 to the LDS (those that exist).
-  static __device__ __forceinline__ void scales_to_lds(char *lds, const Scales &sa, const Scales &sb, int b0) {
-    constexpr int kUnits = S::BM * (kChunk / 4);
-    const int n = min(kChunk, sa.blocks - b0);
-#pragma unroll
-    for (int u0 = 0; u0 < kUnits; u0 += S::kThreads) {
-      const int u = u0 + static_cast<int>(threadIdx.x), row = u / (kChunk / 4), b = u % (kChunk / 4) * 4;
-      if (b >= n || row >= S::BM) continue;
-      const uint8_t *p = sa.base + min(row, sa.rows - 1) * sa.by_row + b0 + b;
-      uint32_t v = 0;
-      if (b + 4 <= n) {
-        __builtin_memcpy(&v, p, 4);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 3; ++i)
-          if (b + i < n) v |= static_cast<uint32_t>(p[i]) << (8 * i);
-      }
-      *reinterpret_cast<uint32_t *>(lds + row * kPitch + b) = v;
-    }
-    const int c = threadIdx.x / kChunk, b = threadIdx.x % kChunk;
-    if (c < kColBlocks && b < n)
-      lds[(S::BM + c) * kPitch + b] = static_cast<char>(sb.base[min(c, sb.rows - 1) * sb.by_row + (b0 + b) * sb.by_block]);
   }
 
   // The products of the stage at sa, block b of the chunk.
@@ -186,17 +192,22 @@ struct TileProduct8 {
     }
   }
 
-  __device__ __forceinline__ void run(char *lds, const uint8_t *a, const uint8_t *b, int64_t lda, int64_t ldb, int validm,
-                                      int validn, int length, const Scales &sa, const Scales &sb) {
+  __device__ __forceinline__ void clear() {
 #pragma unroll
     for (int i = 0; i < S::FM; ++i)
 #pragma unroll
       for (int j = 0; j < S::FN; ++j) acc[i][j] = fx4{0, 0, 0, 0};
+  }
+  __device__ __forceinline__ void init(const uint8_t *a, const uint8_t *b, int64_t lda, int64_t ldb, int validm, int validn,
+                                       int length) {
     k = length;
     at = 0;
     per = (k + kStep - 1) / kStep;
     oa.init(a, lda, validm);
     ob.init(b, ldb, validn);
+  }
+  __device__ __forceinline__ void run(char *lds, const Scales &sa, const Scales &sb) {
+    clear();
     if constexpr (ALIGNED) direct(lds, per, sa, sb);
     else through_registers(lds, per, sa, sb);
   }
@@ -209,7 +220,7 @@ struct TileProduct8 {
     constexpr int kAhead = kStages - 1;  // stages in flight when a step begins
     constexpr int kLoads = OpA::kPer + OpB::kPer;
     for (int i = 0; i < kAhead && i < steps; ++i) load(lds0 + i * kStage);
-    scales_to_lds(scales, sa, sb, 0);
+    Chunk::move(scales, sa, sb, 0);
     int buf = 0, to = kAhead;  // stage read, stage loaded
     for (int t = 0; t < steps; ++t) {
       if (kAhead > 1 && t + kAhead <= steps) {  // all but the newest kAhead - 1 stages have landed
@@ -219,7 +230,7 @@ struct TileProduct8 {
       }
       if (t + kAhead < steps) load(lds0 + to * kStage);
       if (t > 0 && t % kChunk == 0) {
-        scales_to_lds(scales, sa, sb, t);
+        Chunk::move(scales, sa, sb, t);
         __syncthreads();
       }
       multiply(lds + buf * kStage, scales, t % kChunk, rm, rn);
@@ -238,13 +249,13 @@ struct TileProduct8 {
 #pragma unroll
     for (int i = 0; i < kSets; ++i)
       if (i < steps) fetch(i);
-    scales_to_lds(scales, sa, sb, 0);
+    Chunk::move(scales, sa, sb, 0);
     land(0, lds);
     auto step = [&](int t, auto set) {
       constexpr int cur = decltype(set)::value, nxt = (cur + 1) % kSets;
       __syncthreads();
       if (t > 0 && t % kChunk == 0) {
-        scales_to_lds(scales, sa, sb, t);
+        Chunk::move(scales, sa, sb, t);
         __syncthreads();
       }
       if (t + kSets < steps) fetch(cur);
@@ -264,31 +275,343 @@ struct TileProduct8 {
 
 __device__ __forceinline__ int64_t blocks_of(int64_t n) { return (n + kQBlock8 - 1) / kQBlock8; }
 
+// The way out of a tile of bf16 results: as TileOut's, but rounded before they
+// pass through the LDS, and 16 bytes to a lane.  16-byte chunk c of row r is
+// kept at c ^ (r & 15) (fewer where a row has fewer): 16 rows' writes of one
+// column lie in different banks.
+template <class S, int LDS>
+struct TileOut16 {
+  static constexpr int kRowBytes = S::BN * 2, kChunks = kRowBytes / 16, kMask = kChunks < 16 ? kChunks - 1 : 15;
+  static constexpr int fit(int ip) { return ip * 16 * S::WM * kRowBytes <= LDS ? ip : fit(ip / 2); }
+  static constexpr int IP = fit(S::FM), kPasses = S::FM / IP, kRows = IP * 16 * S::WM;
+
+  // f(m, n, v): v holds C[m][n .. n + 7] of the tile.
+  template <class F>
+  static __device__ __forceinline__ void all(char *lds, const fx4 (&acc)[S::FM][S::FN], F f) {
+    int tid = threadIdx.x;
+    asm volatile("" : "+v"(tid));  // (see TileOut)
+    const int wave = tid >> 6, lane = tid & 63;
+    const int row0 = wave / S::WN * (IP * 16) + (lane & 15), col0 = wave % S::WN * (S::BN / S::WN) * 2 + (lane >> 4) * 8;
+#pragma unroll
+    for (int pass = 0; pass < kPasses; ++pass) {
+      if (pass > 0) __syncthreads();
+#pragma unroll
+      for (int i = 0; i < IP; ++i)
+#pragma unroll
+        for (int j = 0; j < S::FN; ++j) {
+          const fx4 v = acc[pass * IP + i][j];
+          const int row = row0 + i * 16, col = col0 + j * 32;
+          *reinterpret_cast<ux2 *>(lds + row * kRowBytes + (((col >> 4) ^ (row & kMask)) << 4) + (col & 8)) =
+              ux2{bf16_bits(v[0]) | bf16_bits(v[1]) << 16, bf16_bits(v[2]) | bf16_bits(v[3]) << 16};
+        }
+      __syncthreads();
+      constexpr int kAll = kRows * kChunks;
+      static_assert(kAll % S::kThreads == 0, "whole rounds");
+#pragma unroll 4
+      for (int r = 0; r < kAll / S::kThreads; ++r) {
+        const int c = r * S::kThreads + tid, row = c / kChunks, chunk = c % kChunks;
+        const ux4 v = *reinterpret_cast<const ux4 *>(lds + row * kRowBytes + ((chunk ^ (row & kMask)) << 4));
+        f(row / (IP * 16) * (S::BM / S::WM) + pass * IP * 16 + row % (IP * 16), chunk * 8, v);
+      }
+    }
+    __syncthreads();
+  }
+};
+
+// Stores v to out[0 .. n) (n in 1 .. 8).
+__device__ __forceinline__ void store8_bf16(uint16_t *out, const ux4 &v, int n) {
+  Raw8<true> r;
+  r.v[0] = v;
+  store8<true>(out, 0, r, n);
+}
+
+// A tile's operands and scales.
+template <class S, bool GRAD>
+struct QTile {
+  RowTile t;
+  int64_t n0;
+  int validn, k;
+  const uint8_t *x, *w;
+  Scales sa, sb;
+
+  __device__ __forceinline__ QTile(const QExpertArgs &a, const RowTile &tile) : t(tile) {
+    const int64_t n = GRAD ? a.in : a.outf, in_blocks = blocks_of(a.in);
+    n0 = static_cast<int64_t>(t.tile_n) * S::BN;
+    k = static_cast<int>(GRAD ? a.outf : a.in);
+    validn = static_cast<int>(min(static_cast<int64_t>(S::BN), n - n0));
+    x = a.x + t.row * a.xs;
+    w = a.w + table_entry(a.offsets + t.e) + (GRAD ? n0 : n0 * a.in);
+    const int64_t first = n0 / kQBlock8;  // block of columns
+    const uint8_t *ws = a.w_scales + t.e * (blocks_of(a.outf) * in_blocks) + (GRAD ? first : first * in_blocks);
+    const int kb = static_cast<int>(blocks_of(k));
+    sa = Scales{a.x_scales + t.row * a.xss, a.xss, 1, t.rows, kb};
+    sb = Scales{ws, GRAD ? 1 : in_blocks, GRAD ? in_blocks : 1, static_cast<int>(blocks_of(n) - first), kb};
+  }
+  template <class P, bool BF, int LDS>
+  __device__ __forceinline__ void store(const QExpertArgs &a, const P &p, char *lds) const {
+    if constexpr (BF) {
+      TileOut16<S, LDS>::all(lds, p.acc, [&](int m, int c, const ux4 &v) {
+        if (m < t.rows && c < validn) store8_bf16(static_cast<uint16_t *>(a.out) + (t.row + m) * a.outs + n0 + c, v, validn - c);
+      });
+    } else {
+      using Out = TileOut<S, LDS>;
+      Out::all(lds, p.acc, [&](int pass, int tid) {
+        Out::rows(lds, pass, tid, [&](int m, int c, fx4 v) {
+          if (m < t.rows && c < validn) store4<false>(a.out, (t.row + m) * a.outs + n0 + c, v, validn - c);
+        });
+      });
+    }
+  }
+};
+
+__device__ __forceinline__ int column_tiles(int64_t n, int bn) { return static_cast<int>((n + bn - 1) / bn); }
+
 // Forward (GRAD false: W_e as [n][k]) and input gradient (GRAD true: as [k][n]).
 template <class P, bool GRAD, bool BF>
 __global__ __launch_bounds__(P::Sh::kThreads) void qexperts_rows(QExpertArgs a) {
   using S = typename P::Sh;
   extern __shared__ __align__(16) char lds[];
-  const int64_t n = GRAD ? a.in : a.outf, k = GRAD ? a.outf : a.in;
-  const int nt = static_cast<int>((n + S::BN - 1) / S::BN);
   RowTile t;
-  if (!find_row_tile<S::BM>(a, nt, t)) return;
-  const int64_t n0 = static_cast<int64_t>(t.tile_n) * S::BN, in_blocks = blocks_of(a.in);
-  const int validn = static_cast<int>(min(static_cast<int64_t>(S::BN), n - n0));
-  const uint8_t *w = a.w + table_entry(a.offsets + t.e) + (GRAD ? n0 : n0 * a.in);
-  const int64_t first = n0 / kQBlock8;  // block of columns
-  const uint8_t *ws = a.w_scales + t.e * (blocks_of(a.outf) * in_blocks) + (GRAD ? first : first * in_blocks);
-  const int kb = static_cast<int>(blocks_of(k));
+  if (!find_row_tile<S::BM>(a, column_tiles(GRAD ? a.in : a.outf, S::BN), t)) return;
+  const QTile<S, GRAD> q(a, t);
   P p;
-  p.run(lds, a.x + t.row * a.xs, w, a.xs, a.in, t.rows, validn, static_cast<int>(k),
-        Scales{a.x_scales + t.row * a.xss, a.xss, 1, t.rows, kb},
-        Scales{ws, GRAD ? 1 : in_blocks, GRAD ? in_blocks : 1, static_cast<int>(blocks_of(n) - first), kb});
-  using Out = TileOut<S, P::kLds>;
-  Out::all(lds, p.acc, [&](int pass, int tid) {
-    Out::rows(lds, pass, tid, [&](int m, int c, fx4 v) {
-      if (m < t.rows && c < validn) store4<BF>(a.out, (t.row + m) * a.outs + n0 + c, v, validn - c);
-    });
-  });
+  p.init(q.x, q.w, a.xs, a.in, q.t.rows, q.validn, q.k);
+  p.run(lds, q.sa, q.sb);
+  q.template store<P, BF, P::kLds>(a, p, lds);
+}
+
+using Big = Shape<256, 256, 2, 2>;
+
+// Tiles of 256 x 256 for long products (aligned, 16-bit results).  The LDS holds
+// two stages; fragments are read half a stage ahead of their instructions, and
+// between a stage's halves the workgroup meets: the next stage has landed, and
+// this one's LDS is free for the loads of the next but one.
+template <bool GRAD>
+struct Long8 {
+  static constexpr int kThreads = Big::kThreads, kStep = 128;
+  static constexpr int NJ = Big::BN / Big::WN / 32, kSlots = 2 * NJ;
+  using OpA = Operand<kF8, kMajorK, Big::BM, kThreads, true>;
+  using OpB = Operand<kF8, GRAD ? kMajorMN : kMajorK, Big::BN, kThreads, true>;
+  using Chunk = ScaleChunk<Big::BM, Big::BN, kThreads>;
+  static constexpr int kStage = OpA::kBytes + OpB::kBytes;
+  static constexpr int kLds = 2 * kStage + 2 * Chunk::kBytes + 4 * kThreads;
+  typedef float fx16 __attribute__((ext_vector_type(16)));
+
+  fx16 acc[4][NJ];
+  Frag8 fa[2][2][2], fb[NJ][2];  // [rows 64 s ..][32 rows][half], [32 columns][half]
+  int sa[2][2], sb;
+  OpA oa;
+  OpB ob;
+  Chunk chunk;
+  char *lds;
+  uint32_t lds0;
+  int rm, rn;  // the wave's first row and column
+
+  // What the L2 is told to fetch one stage before the LDS is: one 128-byte line
+  // to a lane, by loads of 4 bytes to a place in the LDS that nobody reads.  The tiles that an XCD
+  // works on at once are mostly 8 row tiles by 4 column tiles, so a workgroup
+  // asks for a quarter of its rows' lines and an eighth of its columns'.
+  const uint8_t *soon_a, *soon_b;
+  int64_t by_stage;          // bytes from a stage's columns to the next one's
+  uint32_t line_a, line_b;   // bytes from there; kOutOfRange: nothing
+  uint32_t unread;           // LDS, 256 bytes to a wave
+
+  __device__ __forceinline__ void aim_ahead(const QTile<Big, GRAD> &q, int64_t lda, int64_t ldb, int last) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    constexpr int kWaves = kThreads / 64, kA = 64 / kWaves, kB = 32 / kWaves;
+    const int row = (wave * kA + lane) * 4 + (q.t.tile_n & 3), line = (wave * kB + lane) * 8 + (q.t.tile_m & 7);
+    soon_a = q.x;
+    soon_b = q.w;
+    by_stage = GRAD ? kStep * ldb : kStep;
+    line_a = lane < kA ? static_cast<uint32_t>(min(row, q.t.rows - 1)) * static_cast<uint32_t>(lda) : kOutOfRange;
+    // columns: 256 rows of a line, or 128 contraction steps (of the last stage `last`) of two lines
+    const uint32_t at = GRAD ? static_cast<uint32_t>(min(line >> 1, last - 1)) * static_cast<uint32_t>(ldb) +
+                                   min((line & 1) * 128, (q.validn - 1) & ~15)
+                             : static_cast<uint32_t>(min(line, q.validn - 1)) * static_cast<uint32_t>(ldb);
+    line_b = lane < kB ? at : kOutOfRange;
+    unread = lds0 + 2 * kStage + 2 * Chunk::kBytes + uniform(static_cast<int32_t>(wave)) * 256;
+  }
+  __device__ __forceinline__ void touch(const uint8_t *base, uint32_t off) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(unread), "v"(off),
+                 "s"(resource(base))
+                 : "memory", "m0");
+  }
+
+  // The 32 bytes of half h of the stage (contraction elements 64 h + 32 (lane / 32) ..) of row/column r + lane % 32.
+  static __device__ __forceinline__ Frag8 rows32(const char *stage, int r, int h) {
+    const int lane = threadIdx.x & 63, row = r + (lane & 31), c = h * 4 + (lane >> 5) * 2;
+    Frag8 f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) f.v[i] = *reinterpret_cast<const ux4 *>(stage + row * 128 + (((c + i) ^ k_swizzle<kF8, 256>(row)) << 4));
+    return f;
+  }
+  static __device__ __forceinline__ Frag8 columns32(const char *stage, int r, int h) {
+    const int lane = threadIdx.x & 63;
+    Frag8 f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {  // 8 contraction elements each: a block of 8 x 16 bytes per 16 lanes
+      const int k = h * 64 + (lane >> 5) * 32 + 8 * i + ((lane & 15) >> 1);
+      const char *p = stage + k * Big::BN + ((((r >> 4) + ((lane >> 4) & 1)) ^ mn_swizzle8<Big::BN>(k)) << 4) + (lane & 1) * 8;
+      const ux2 v = __builtin_bit_cast(
+          ux2, __builtin_amdgcn_ds_read_tr8_b64_v2i32((__attribute__((address_space(3))) ix2 *)const_cast<char *>(p)));
+      f.v[i >> 1][2 * (i & 1)] = v[0];
+      f.v[i >> 1][2 * (i & 1) + 1] = v[1];
+    }
+    return f;
+  }
+  __device__ __forceinline__ void read_a(int set, int i, int h, const char *stage) {
+    fa[set][i][h] = rows32(stage, rm + set * 64 + i * 32, h);
+  }
+  __device__ __forceinline__ void read_b(int j, int h, const char *stage) {
+    const char *p = stage + OpA::kBytes;
+    fb[j][h] = GRAD ? columns32(p, rn + j * 32, h) : rows32(p, rn + j * 32, h);
+  }
+  __device__ __forceinline__ const uint8_t *scales(int at) const {  // at: chunk's buffer and block
+    return reinterpret_cast<const uint8_t *>(lds) + 2 * kStage + at;
+  }
+  __device__ __forceinline__ void read_row_scales(int set, int at) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) sa[set][i] = scales(at)[(rm + set * 64 + i * 32 + (threadIdx.x & 31)) * kScalePitch];
+  }
+  __device__ __forceinline__ int col_scale(int at) const { return scales(at)[(Big::BM + rn / 128) * kScalePitch]; }
+  static __device__ __forceinline__ fx16 mfma(const Frag8 &a, const Frag8 &b, fx16 c, int s, int t) {
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(__builtin_bit_cast(ix8, a), __builtin_bit_cast(ix8, b), c, 0,
+                                                           0, 0, s, 0, t);
+  }
+
+  // One stage, the one in buffer `buf`; now, next: where its scales and the next stage's are.  The code is free of
+  // branches: behind one, the compiler would gather all products of the stage.
+  __device__ __forceinline__ void step(int buf, int now, int next, int ahead) {
+    const char *mine = lds + buf * kStage, *other = lds + (buf ^ 1) * kStage;
+    const uint32_t to = lds0 + buf * kStage;
+    read_row_scales(1, now);
+    touch(soon_a + static_cast<int64_t>(ahead) * kStep, line_a);
+    touch(soon_b + ahead * by_stage, line_b);
+#pragma unroll
+    for (int n = 0; n < kSlots; ++n) {
+      const int h = n / NJ, j = n % NJ;
+      if (n < 4) read_a(1, n & 1, n >> 1, mine);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) acc[i][j] = mfma(fb[j][h], fa[0][i][h], acc[i][j], sb, sa[0][i]);
+      __builtin_amdgcn_sched_barrier(0);  // keeps the reads spread among the products
+    }
+    // all loads to the LDS have landed: only the two above, the youngest, may be under way
+    asm volatile("s_waitcnt vmcnt(2) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    const int next_sb = col_scale(next);
+    read_row_scales(0, next);
+#pragma unroll
+    for (int n = 0; n < kSlots; ++n) {
+      const int h = n / NJ, j = n % NJ;
+      static_assert(OpA::kPer == kSlots && OpB::kPer == kSlots, "one load of each operand");
+      oa.load_one(n, to);
+      ob.load_one(n, to + OpA::kBytes);
+      if (n < 4) read_a(0, n & 1, n >> 1, other);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) acc[2 + i][j] = mfma(fb[j][h], fa[1][i][h], acc[2 + i][j], sb, sa[1][i]);
+      read_b(j, h, other);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    sb = next_sb;
+    oa.advance();
+    ob.advance();
+  }
+
+  __device__ __forceinline__ void run(char *l, const QTile<Big, GRAD> &q, int64_t lda, int64_t ldb) {
+    const int wave = uniform(static_cast<int32_t>(threadIdx.x >> 6));
+    const int per = (q.k + kStep - 1) / kStep;
+    lds = l;
+    lds0 = uniform(static_cast<int32_t>(lds_offset(l)));
+    rm = wave / Big::WN * (Big::BM / Big::WM);
+    rn = wave % Big::WN * (Big::BN / Big::WN);
+    oa.init(q.x, lda, q.t.rows);
+    ob.init(q.w, ldb, q.validn);
+    int left = q.k;  // contraction elements from the stage on that is loaded next
+    const auto aim = [&] {  // the last stage may be short; behind it, zeros
+      if (left < kStep) {
+        oa.cut(max(left, 0));
+        ob.cut(max(left, 0));
+      }
+      left -= kStep;
+    };
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      aim();
+      oa.load(lds0 + i * kStage);
+      ob.load(lds0 + i * kStage + OpA::kBytes);
+      oa.advance();
+      ob.advance();
+    }
+    aim_ahead(q, lda, ldb, q.k - (per - 1) * kStep);
+    char *chunks = lds + 2 * kStage;
+    Chunk::move(chunks, q.sa, q.sb, 0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) acc[i][j] = fx16{};
+    loads_done_and_meet();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) read_a(0, i, h, lds);
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) read_b(j, h, lds);
+    }
+    read_row_scales(0, 0);
+    sb = col_scale(0);
+    int now = 0, then = Chunk::kBytes;  // the chunks' places
+    for (int t = 0; t < per;) {
+      if (t + kScaleChunk < per) Chunk::move(chunks + then, q.sa, q.sb, t + kScaleChunk);
+      const int end = min(per, t + kScaleChunk), last = end - 1 - t;
+      for (int b = 0; t < end; ++t, ++b) {
+        aim();
+        step(t & 1, now + b, b < last ? now + b + 1 : then, min(t + 3, per - 1));
+      }
+      const int s = now;
+      now = then;
+      then = s;
+    }
+    loads_done_and_meet();
+  }
+
+  // A lane has, of each 32 columns, 8 q + 4 (lane / 32) .. + 3 of row lane % 32.  Rounded, they pass through the LDS,
+  // all of the tile at once, and leave in whole lines: 16-byte chunk c of row r is kept at c ^ (r & 31).
+  __device__ __forceinline__ void store(const QExpertArgs &a, const QTile<Big, GRAD> &q) const {
+    int tid = threadIdx.x;
+    asm volatile("" : "+v"(tid));  // (see TileOut)
+    const int lane = tid & 63;
+    constexpr int kRowBytes = Big::BN * 2, kChunks = kRowBytes / 16;
+    static_assert(Big::BM * kRowBytes <= 2 * kStage, "the tile fits");
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = rm + i * 32 + (lane & 31);
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          *reinterpret_cast<ux2 *>(lds + row * kRowBytes + (((rn / 8 + j * 4 + c) ^ (row & 31)) << 4) + (lane >> 5) * 8) =
+              ux2{bf16_bits(acc[i][j][4 * c]) | bf16_bits(acc[i][j][4 * c + 1]) << 16,
+                  bf16_bits(acc[i][j][4 * c + 2]) | bf16_bits(acc[i][j][4 * c + 3]) << 16};
+    }
+    __syncthreads();
+    const int chunk = tid % kChunks, c = chunk * 8;
+    uint16_t *out = static_cast<uint16_t *>(a.out) + q.t.row * a.outs + q.n0 + c;
+    if (c >= q.validn) return;  // (whole vectors: the columns are a multiple of 16)
+#pragma unroll 8
+    for (int row = tid / kChunks; row < q.t.rows; row += kThreads / kChunks)
+      *reinterpret_cast<ux4_at2 *>(out + row * a.outs) =
+          *reinterpret_cast<const ux4 *>(lds + row * kRowBytes + ((chunk ^ (row & 31)) << 4));
+  }
+};
+
+template <bool GRAD>
+__global__ __launch_bounds__(Big::kThreads) void qexperts_long(QExpertArgs a) {
+  extern __shared__ __align__(16) char lds[];
+  RowTile t;
+  if (!find_row_tile<Big::BM>(a, column_tiles(GRAD ? a.in : a.outf, Big::BN), t)) return;
+  const QTile<Big, GRAD> q(a, t);
+  Long8<GRAD> p;
+  p.run(lds, q, a.xs, a.in);
+  p.store(a, q);
 }
 
 // Forward for few rows per expert (decoding): the time is that of reading each
@@ -447,8 +770,7 @@ __global__ __launch_bounds__(kQuantThreads8) void quantize_weights(QWeightArgs a
   }
 }
 
-// Tiles.
-using Big = Shape<256, 256, 2, 4>;
+// Tiles.  Big (aligned, 16-bit results) is qexperts_long's.
 using Square = Shape<128, 128, 2, 2>;
 using Half = Shape<64, 128, 2, 2>;
 using Small = Shape<32, 64, 1, 4, 4>;
@@ -467,19 +789,15 @@ hipError_t launch_rows(const QExpertArgs &a, hipStream_t s) {
 
 template <class S, bool GRAD>
 hipError_t launch_rows(const QExpertArgs &a, hipStream_t s) {
-  if constexpr (S::BM >= 256) {  // aligned, 16-bit results alone
-    return launch_rows<false, S, GRAD, true>(a, s);
-  } else {
-    if (a.aligned) return a.bf16 ? launch_rows<false, S, GRAD, true>(a, s) : launch_rows<true, S, GRAD, true>(a, s);
-    return a.bf16 ? launch_rows<false, S, GRAD, false>(a, s) : launch_rows<true, S, GRAD, false>(a, s);
-  }
+  if (a.aligned) return a.bf16 ? launch_rows<false, S, GRAD, true>(a, s) : launch_rows<true, S, GRAD, true>(a, s);
+  return a.bf16 ? launch_rows<false, S, GRAD, false>(a, s) : launch_rows<true, S, GRAD, false>(a, s);
 }
 
 struct TileCost {
   double slots, alone, full, rest;
 };
-constexpr TileCost kBF16Cost[4] = {{256, 1.3, 1.45, 12}, {512, 0.65, 1.05, 5}, {768, 0.55, 0.98, 4}, {768, 0.4, 0.45, 3.5}};
-constexpr TileCost kF32Cost[4] = {{}, {512, 2.5, 3.0, 5}, {768, 1.6, 2.5, 4}, {768, 0.9, 1.2, 3.5}};
+constexpr TileCost kBF16Cost[4] = {{256, 1.2, 1.33, 12}, {512, 0.95, 1.06, 5}, {768, 0.75, 0.95, 3.5}, {768, 0.36, 0.36, 3.5}};
+constexpr TileCost kF32Cost[4] = {{}, {512, 3.0, 3.2, 5}, {768, 2.1, 2.1, 4}, {768, 0.6, 0.71, 3.5}};
 
 template <class S, bool GRAD>
 double rows_time(const QExpertArgs &a, const TileCost &c) {
@@ -512,7 +830,8 @@ Choice rows_choice(const QExpertArgs &a) {
 template <bool GRAD>
 hipError_t rows(const QExpertArgs &a, hipStream_t s) {
   switch (rows_choice<GRAD>(a)) {
-    case kBig: return launch_rows<Big, GRAD>(a, s);
+    case kBig:
+      return launch(qexperts_long<GRAD>, row_tiles<Big, GRAD>(a), 1, Big::kThreads, Long8<GRAD>::kLds, s, a);
     case kSquare: return launch_rows<Square, GRAD>(a, s);
     case kHalf: return launch_rows<Half, GRAD>(a, s);
     case kSmall: return launch_rows<Small, GRAD>(a, s);

@@ -125,13 +125,24 @@ __device__ __forceinline__ constexpr int mn_swizzle(int k) {
   return W >= 128 ? ((k & 3) | ((k >> 3) & 1) << 2) : (((k >> 1) & 1) | ((k >> 3) & 1) << 1);
 }
 
-// The same for bytes, in 16-byte columns: half a wave reads one column of rows
-// k .. k + 7 and k + 16 .. k + 23, which lie in 16 different columns (or, rows
-// of 64 or 128 bytes going round the banks faster, as many as there are).
+// Where a kMajorK row keeps its 16-byte column c: at c ^ k_swizzle(row).  A read
+// of 16 bytes takes the wave in quarters, lanes l .. l + 7 with l + 16 .. l + 23:
+// these are eight rows of two columns where 16 rows make a fragment, and rows r
+// .. r + 7 and r + 16 .. r + 23 of one column where 32 do (of 8 bits, 256 rows:
+// half of the LDS's cycles were conflicts with r & 7).
+template <Elem E, int W>
+__device__ __forceinline__ constexpr int k_swizzle(int row) {
+  return E == kF8 && W >= 256 ? (row & 6) | ((row >> 4) & 1) : row & 7;
+}
+
+// mn_swizzle for bytes, in 16-byte columns.  Half a wave reads one column of rows
+// k .. k + 7 and k + 16 .. k + 23 (rows of 64 and 128 bytes go round the banks
+// faster, so fewer columns have to differ), or, of 256 columns, two
+// neighbouring columns of rows k .. k + 7.
 template <int W>
 __device__ __forceinline__ constexpr int mn_swizzle8(int k) {
   const int far = (k >> 4) & 1;
-  return W >= 256 ? ((k & 7) | far << 3) : W >= 128 ? (((k >> 1) & 3) | far << 2) : (((k >> 2) & 1) | far << 1);
+  return W >= 256 ? (k & 7) << 1 : W >= 128 ? (((k >> 1) & 3) | far << 2) : (((k >> 2) & 1) | far << 1);
 }
 
 template <Elem E>
@@ -189,7 +200,7 @@ struct Operand {
     const int c = ALIGNED ? (threadIdx.x >> 6) * (64 * kPer) + j * 64 + (threadIdx.x & 63) : j * NT + threadIdx.x;
     if constexpr (MJ == kMajorK) {
       row = c >> 3;
-      col = (c & 7) ^ (row & 7);
+      col = (c & 7) ^ k_swizzle<E, W>(row);
     } else {
       row = c / kRow;
       const int p = c % kRow;
@@ -289,7 +300,7 @@ struct Operand {
     const int lane = threadIdx.x & 63;
     if constexpr (MJ == kMajorK) {
       const int row = r + (lane & 15), c = ks * 4 + (lane >> 4);
-      return *reinterpret_cast<const Frag<E> *>(stage + row * 128 + ((c ^ (row & 7)) << 4));
+      return *reinterpret_cast<const Frag<E> *>(stage + row * 128 + ((c ^ k_swizzle<E, W>(row)) << 4));
     } else if constexpr (E == kF32) {
       const int i = r + (lane & 15);
       const char *p = stage + (ks * 16 + (lane >> 4) * 4) * (W * 4) + (((i >> 2) ^ (lane >> 2 & 4)) << 4) + (i & 3) * 4;
