@@ -789,25 +789,45 @@ hipError_t launch_rows(const QExpertArgs &a, hipStream_t s) {
 
 template <class S, bool GRAD>
 hipError_t launch_rows(const QExpertArgs &a, hipStream_t s) {
-  if (a.aligned) return a.bf16 ? launch_rows<false, S, GRAD, true>(a, s) : launch_rows<true, S, GRAD, true>(a, s);
-  return a.bf16 ? launch_rows<false, S, GRAD, false>(a, s) : launch_rows<true, S, GRAD, false>(a, s);
+  if (a.bf16) return a.aligned ? launch_rows<false, S, GRAD, true>(a, s) : launch_rows<false, S, GRAD, false>(a, s);
+  if constexpr (S::BM < 128) {  // fp32 results take the smaller tiles
+    return a.aligned ? launch_rows<true, S, GRAD, true>(a, s) : launch_rows<true, S, GRAD, false>(a, s);
+  } else {
+    return hipErrorInvalidValue;  // not chosen
+  }
 }
 
+// Which tile: the least of modelled times.  A tile's time is that of its blocks
+// of the contraction and a rest; `slots` tiles run at once, one workgroup on a
+// CU or several, whose rounds overlap.  `alone`: launches of up to 256 tiles.
+// The model against measured times, bf16 results, rows spread over the experts
+// as a router does (rows, experts, in x out: Big / Square / Half / Small,
+// microseconds):
+//   16384, 8, 4096 x 12288:  723 / 983 / 1172 / 2111   measured 833 / 945 / 1132 / 2258
+//   16384, 4, 2048 x 2048:   104 / 100 / 115 / 217               94 / 85 / 91 / 202
+//   8192, 32, 2048 x 2048:    70 / 66 / 68 / 117                 70 / 66 / 76 / 122
+//   2048, 8, 4096 x 4096:     59 / 68 / 71 / 101                 65 / 77 / 76 / 111
+//   4096, 8, 1024 x 1024:     25 / 14 / 14 / 22                  20 / 14 / 13 / 20
+//   300, 2, 3968 x 3968:      57 / 34 / 27 / 21                  44 / 27 / 21 / 18
+// (28 such calls of both products take 2% more than with the best tile for
+// each.)  fp32 results (Square only lost, 920 and 37 in these):
+//   16384, 8, 4096 x 4096:      - / - / 831 / 1173   measured 807 / 1131
+//   3001, 8, 1024 x 1536:       - / - / 27 / 34                26 / 30
 struct TileCost {
   double slots, alone, full, rest;
 };
-constexpr TileCost kBF16Cost[4] = {{256, 1.2, 1.33, 12}, {512, 0.95, 1.06, 5}, {768, 0.75, 0.95, 3.5}, {768, 0.36, 0.36, 3.5}};
-constexpr TileCost kF32Cost[4] = {{}, {512, 3.0, 3.2, 5}, {768, 2.1, 2.1, 4}, {768, 0.6, 0.71, 3.5}};
+constexpr TileCost kBF16Cost[4] = {{256, 1.4, 1.3, 14}, {512, 0.95, 1.06, 5}, {768, 0.75, 1.0, 3.5}, {768, 0.36, 0.4, 3.5}};
+constexpr TileCost kF32Cost[4] = {{}, {}, {768, 2.1, 2.1, 4}, {768, 0.6, 0.71, 3.5}};
 
 template <class S, bool GRAD>
 double rows_time(const QExpertArgs &a, const TileCost &c) {
   const double n = static_cast<double>(GRAD ? a.in : a.outf), steps = static_cast<double>(GRAD ? a.outf : a.in) / 128;
   const double e = static_cast<double>(std::min<int64_t>(a.experts, a.tokens)), t = static_cast<double>(a.tokens);
-  // every expert ends inside a tile, half of it unused on average
-  const double tiles = std::max(e, t / S::BM + e / 2) * std::ceil(n / S::BN);
-  double rounds = tiles / c.slots;
-  rounds = rounds < 2 || c.slots <= 256 ? std::ceil(rounds) : rounds + 0.5;
-  return rounds * (std::ceil(steps) * (tiles <= 256 ? c.alone : c.full) + c.rest);
+  // one of several experts ends inside a tile, half of it unused on average
+  const double tiles = (e > 1 ? std::max(e, t / S::BM + e / 2) : std::ceil(t / S::BM)) * std::ceil(n / S::BN);
+  const double rounds = tiles / c.slots;
+  return (c.slots <= 256 ? std::ceil(rounds) : std::max(1.0, rounds + 0.5)) *
+         (std::ceil(steps) * (tiles <= 256 ? c.alone : c.full) + c.rest);
 }
 
 enum Choice { kBig, kSquare, kHalf, kSmall, kFew };
@@ -815,12 +835,24 @@ enum Choice { kBig, kSquare, kHalf, kSmall, kFew };
 template <bool GRAD>
 Choice rows_choice(const QExpertArgs &a) {
   if constexpr (!GRAD) {
-    const int64_t e = a.experts, bytes = std::min(e, a.tokens) * a.in * a.outf;
-    if (a.tokens <= 16 * e && bytes <= 16 << 20) return kFew;
+    // Short decoding calls, where latency counts: up to 512 workgroups of
+    // qexperts_few, two to a CU.  Microseconds with it / Small, weights from
+    // memory (rows, active of experts, in x out):
+    //   2, 2 of 8, 1024 x 512         7.4 /  7.1
+    //   1, 1 of 1, 4096 x 4096        7.3 / 13.4
+    //   4, 4 of 8, 2048 x 1024        6.9 /  8.5
+    //   2, 2 of 8, 4096 x 4096       11.0 / 13.9
+    //   16, 8 of 8, 2048 x 1024       8.4 /  8.6
+    //   8, 8 of 8, 2048 x 2048       14.5 /  9.6
+    //   1, 1 of 1, 4096 x 12288      15.6 / 14.2
+    //   32, 20 of 32, 4096 x 1536    43.9 / 30.4
+    const int64_t e = a.experts;
+    if (a.tokens <= 16 * e && std::min(e, a.tokens) * ((a.outf + kFewCols8 - 1) / kFewCols8) <= 512) return kFew;
   }
   const TileCost *c = a.bf16 ? kBF16Cost : kF32Cost;
   const double big = a.aligned && a.bf16 ? rows_time<Big, GRAD>(a, c[0]) : 1e300;
-  const double square = rows_time<Square, GRAD>(a, c[1]), half = rows_time<Half, GRAD>(a, c[2]);
+  const double square = a.bf16 ? rows_time<Square, GRAD>(a, c[1]) : 1e300;
+  const double half = rows_time<Half, GRAD>(a, c[2]);
   const double small = rows_time<Small, GRAD>(a, c[3]);
   if (big <= std::min({square, half, small})) return kBig;
   if (square <= std::min(half, small)) return kSquare;

@@ -247,19 +247,20 @@ def test_ends_of_any_contents(ends):
 def test_every_tile(product, dtype):
     """Every tile that a call can launch is run: calls whose tiles are checked to be all there are."""
     seen = set()
-    for inf, outf, counts in ((64, 64, [1]), (512, 512, [40, 30]), (512, 1024, [300] * 4), (1024, 1024, [4096]),
+    for inf, outf, counts in ((64, 64, [1]), (63, 65, [1]), (512, 512, [40, 30]), (512, 1024, [300] * 4), (1024, 1024, [4096]),
                               (2048, 4096, [4096]), (2048, 2048, [900, 3000]), (1000, 1001, [3000]), (333, 777, [200]),
-                              (2048, 4096, [16384]), (4096, 4096, [4000] * 4)):
+                              (2047, 2047, [1000] * 8), (2048, 4096, [16384]), (4096, 4096, [4000] * 4), (1472, 704, [25] * 40)):
         c = Case(inf, outf, counts, dtype)
         aligned = inf % 16 == 0 and outf % 16 == 0
         s = B.ar_qexperts_launch_shape(c.plan, product, c.t, aligned)
-        seen.add((s["tile_rows"], s["tile_cols"]))
+        seen.add((s["tile_rows"], s["tile_cols"], aligned))
         got = c.forward() if product == "forward" else c.input_grad()
         torch.cuda.synchronize()
         c.check(got, product == "input_grad")
         B.ar_qexperts_destroy(c.plan)
-    want = {(32, 64), (64, 128), (128, 128)} | ({(256, 256)} if dtype == "bf16" else set()) | ({(32, 16)} if product == "forward" else set())
-    assert want <= seen, seen
+    tiles = [(32, 64), (64, 128)] + ([(128, 128)] if dtype == "bf16" else []) + ([(32, 16)] if product == "forward" else [])
+    want = {t + (aligned,) for t in tiles for aligned in (True, False)} | ({(256, 256, True)} if dtype == "bf16" else set())
+    assert seen == want, seen ^ want
 
 
 @pytest.mark.gpu
