@@ -158,7 +158,6 @@ struct NormArgs {
   const int32_t *first;   // [tensors + 1] first chunk of each tensor
   double *chunk_sums;     // [chunks] sums of squares
   double *group_sums;     // [workgroups]
-  uint32_t *arrived;      // workgroups that are done; zero between calls
   float *norm;
   float *tensor_norms;    // or NULL
   double scale, max_norm;

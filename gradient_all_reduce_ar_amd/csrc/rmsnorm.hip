@@ -81,6 +81,7 @@ __global__ __launch_bounds__(kRowThreads<T>) void rms_forward(RmsForward a) {
 #pragma unroll
       for (int i = 0; i < kLane; ++i) v[i] = h[j][i] + r[i];
       h[j] = rounded8<BF>(v);
+      if constexpr (K >= 8) __builtin_amdgcn_sched_barrier(0);  // one piece of the residual at a time in registers
     }
   }
   if (a.h) {
@@ -118,6 +119,7 @@ __global__ __launch_bounds__(kRowThreads<T>) void rms_forward(RmsForward a) {
         if ((t & 15) == 0) a.scales[row * a.ss + e / kQBlock8] = static_cast<uint8_t>(byte);
       }
     }
+    if constexpr (K >= 8) __builtin_amdgcn_sched_barrier(0);
   }
 }
 
@@ -145,7 +147,7 @@ __global__ __launch_bounds__(kRowThreads<T>) void rms_backward(RmsBackward a) {
   const int t = threadIdx.x % T, team = threadIdx.x / T;
   const int64_t step = static_cast<int64_t>(gridDim.x) * kTeams<T>;
   struct Row {
-    Raw8<BF> dy[KH], h[KH];
+    Raw8<BF> dy[KH], h[KH], dh[KH];
     float rstd;
   };
   auto load = [&](const void *p, int64_t start, int j) {
@@ -159,6 +161,7 @@ __global__ __launch_bounds__(kRowThreads<T>) void rms_backward(RmsBackward a) {
       for (int j = 0; j < K; ++j) {
         r.dy[j] = load(a.dy, row * a.dys, j);
         r.h[j] = load(a.h, row * a.hs, j);
+        if (a.dh) r.dh[j] = load(a.dh, row * a.dhs, j);
       }
     }
   };
@@ -189,6 +192,7 @@ __global__ __launch_bounds__(kRowThreads<T>) void rms_backward(RmsBackward a) {
         acc[j][i] += dy[i] * xhat;
         dot += dy[i] * g[i] * xhat;
       }
+      if constexpr (!kHold) __builtin_amdgcn_sched_barrier(0);
     }
     const float mean = team_sum<T>(dot, slots[parity]) / static_cast<float>(a.features);
 #pragma unroll
@@ -200,11 +204,14 @@ __global__ __launch_bounds__(kRowThreads<T>) void rms_backward(RmsBackward a) {
 #pragma unroll
       for (int i = 0; i < kLane; ++i) v[i] = (dy[i] * g[i] - (h[i] * now.rstd) * mean) * now.rstd;
       if (a.dh) {
-        const Raw8<BF> dh = load(a.dh, row * a.dhs, j);
+        Raw8<BF> dh;
+        if constexpr (kHold) dh = now.dh[j];
+        else dh = load(a.dh, row * a.dhs, j);
 #pragma unroll
         for (int i = 0; i < kLane; ++i) v[i] += dh[i];
       }
       if (n > 0) store8<BF>(a.dx, row * a.dxs + e, rounded8<BF>(v), n);
+      if constexpr (!kHold) __builtin_amdgcn_sched_barrier(0);
     }
     now = next;
   }
@@ -237,15 +244,15 @@ __global__ __launch_bounds__(kRowThreads<T>) void rms_backward(RmsBackward a) {
   }
 }
 
-// dgain of columns 64 b .. 64 b + 63: 16 lanes of four columns, 64 ranges of
-// the parts, each added in order, then the ranges in order.
-constexpr int kGainCols = 64, kGainRanges = 64, kGainThreads = kGainCols / 4 * kGainRanges;
+// dgain of columns 32 b .. 32 b + 31: 8 lanes of four columns, 64 ranges of the
+// parts, each added in order, then the ranges in order.
+constexpr int kGainCols = 32, kGainRanges = 64, kGainThreads = kGainCols / 4 * kGainRanges;
 __global__ __launch_bounds__(kGainThreads) void rms_gain(RmsBackward a, int parts) {
   __shared__ float sums[kGainRanges][kGainCols];
   const int range = threadIdx.x / (kGainCols / 4), c = threadIdx.x % (kGainCols / 4) * 4;
   const int col = blockIdx.x * kGainCols + c, n = a.features - col;
   fx4 s = {0, 0, 0, 0};
-#pragma unroll 4
+#pragma unroll 8
   for (int p = range; p < parts; p += kGainRanges) {
     const fx4 v = n > 0 ? load4<false>(a.parts, static_cast<int64_t>(p) * a.features + col, n) : fx4{0, 0, 0, 0};
 #pragma unroll
@@ -301,20 +308,22 @@ hipError_t forward(const RmsForward &a, hipStream_t s) {
   return launch(rms_forward<BF, T, K>, (a.tokens + kTeams<T> - 1) / kTeams<T>, 1, kRowThreads<T>, 0, s, a);
 }
 
+// Teams and pieces: few pieces to a thread, so that many rows are under way.
+// Microseconds, bf16, residual, h, y and codes (rows x features):
+//   32768 x 512:   64 threads, 1 piece  33.3;  64, 2  35.5;  256, 1  60.8
+//   16384 x 1024:  64, 2  33.9;  64, 4  36.7;  256, 1  39.4
+//   16384 x 2048:  256, 1  57.2;  64, 4  62.0;  256, 2  61.3;  512, 1  71.6
+//   16384 x 4096:  512, 1  107.6;  256, 2  110.7;  64, 8  124.9;  1024, 1  130.5
+//   8192 x 8192:   512, 2  110.4;  256, 4  116.0;  1024, 1  112.3
+// (5.6 TB/s; one row of 4096 takes 3.7 in the kernel with any of them.)
 template <bool BF>
 hipError_t forward_of(const RmsForward &a, hipStream_t s) {
   const int64_t c = (a.features + kLane - 1) / kLane;  // lanes of a row
-  const bool few = a.tokens < 1024;
-  if (few) {
-    if (c <= 64) return forward<BF, 64, 1>(a, s);
-    if (c <= 256) return forward<BF, 256, 1>(a, s);
-    if (c <= 1024) return forward<BF, 1024, 1>(a, s);
-  }
   if (c <= 64) return forward<BF, 64, 1>(a, s);
   if (c <= 128) return forward<BF, 64, 2>(a, s);
-  if (c <= 256) return forward<BF, 64, 4>(a, s);
-  if (c <= 512) return forward<BF, 256, 2>(a, s);
-  if (c <= 1024) return forward<BF, 256, 4>(a, s);
+  if (c <= 256) return forward<BF, 256, 1>(a, s);
+  if (c <= 512) return forward<BF, 512, 1>(a, s);
+  if (c <= 1024) return forward<BF, 512, 2>(a, s);
   if (c <= 2048) return forward<BF, 1024, 2>(a, s);
   if (c <= 4096) return forward<BF, 1024, 4>(a, s);
   return forward<BF, 1024, 8>(a, s);
@@ -322,11 +331,13 @@ hipError_t forward_of(const RmsForward &a, hipStream_t s) {
 
 constexpr int32_t kMostParts = 1024;
 
-template <bool BF, int T, int K>
+// PARTS: workgroups at most, about those that run at once; each takes two rows
+// at least (512 rows of 4096: 256 workgroups 13.0 us, 512 of them 14.8).
+template <bool BF, int T, int K, int PARTS>
 hipError_t backward(const RmsBackward &a, hipStream_t s) {
-  const int64_t teams = (a.tokens + kTeams<T> - 1) / kTeams<T>;
-  const int64_t most = std::min<int64_t>(a.max_parts, T >= 1024 ? 256 : kMostParts);
-  const int64_t grid = std::min(teams, most);
+  static_assert(PARTS <= kMostParts, "the workspace has room");
+  const int64_t rows = 2 * kTeams<T>, teams = (a.tokens + rows - 1) / rows;
+  const int64_t grid = std::min<int64_t>({teams, PARTS, a.max_parts});
   const LaunchEvents ev = t_launch_events;  // the call's mark goes on its last kernel
   if (grid > 1) t_launch_events = LaunchEvents{};
   const hipError_t e = launch(rms_backward<BF, T, K>, grid, 1, kRowThreads<T>, 0, s, a);
@@ -335,17 +346,24 @@ hipError_t backward(const RmsBackward &a, hipStream_t s) {
   return launch(rms_gain, (a.features + kGainCols - 1) / kGainCols, 1, kGainThreads, 0, s, a, static_cast<int>(grid));
 }
 
+// Teams, pieces and workgroups, by microseconds (bf16, with dh):
+//   32768 x 512:   64 threads, 1 piece, 1024 workgroups  35.6;  64, 2, 1536  46.7
+//   16384 x 1024:  64, 2, 512  40.1;  64, 2, 1024  43.6;  256, 1, 1024  47.5
+//   16384 x 2048:  256, 1, 1024  61.9;  256, 1, 512  75.4;  512, 1, 512  74.6
+//   16384 x 4096:  512, 1, 512  108.6;  256, 2, 768  113.9;  1024, 1, 256  163.9
+//   8192 x 8192:   512, 2, 256  121.4;  256, 4, 512  123.2
+//   fp32, 16384 x 2048:  256, 1, 512  100.9;  256, 1, 1024  107.6
 template <bool BF>
 hipError_t backward_of(const RmsBackward &a, hipStream_t s) {
   const int64_t c = (a.features + kLane - 1) / kLane;
-  if (c <= 64) return backward<BF, 64, 1>(a, s);
-  if (c <= 128) return backward<BF, 64, 2>(a, s);
-  if (c <= 256) return backward<BF, 256, 1>(a, s);
-  if (c <= 512) return backward<BF, 256, 2>(a, s);
-  if (c <= 1024) return backward<BF, 256, 4>(a, s);
-  if (c <= 2048) return backward<BF, 1024, 2>(a, s);
-  if (c <= 4096) return backward<BF, 1024, 4>(a, s);
-  return backward<BF, 1024, 8>(a, s);
+  if (c <= 64) return backward<BF, 64, 1, 1024>(a, s);
+  if (c <= 128) return backward<BF, 64, 2, 512>(a, s);
+  if (c <= 256) return backward<BF, 256, 1, BF ? 1024 : 512>(a, s);
+  if (c <= 512) return backward<BF, 512, 1, 512>(a, s);
+  if (c <= 1024) return backward<BF, 512, 2, 256>(a, s);
+  if (c <= 2048) return backward<BF, 1024, 2, 256>(a, s);
+  if (c <= 4096) return backward<BF, 1024, 4, 256>(a, s);
+  return backward<BF, 1024, 8, 256>(a, s);
 }
 
 }  // namespace

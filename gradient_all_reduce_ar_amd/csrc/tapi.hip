@@ -130,14 +130,13 @@ struct ar_norm_plan {
   int64_t groups() const {
     return std::max<int64_t>(1, (static_cast<int64_t>(chunks.size()) + ar_dev::kNormWaves - 1) / ar_dev::kNormWaves);
   }
-  // the arrivals (on 256 bytes of their own), the workgroups' sums, the chunks'
-  size_t sum_bytes() const { return 256 + 8 * (static_cast<size_t>(groups()) + chunks.size()); }
+  // the workgroups' sums, the chunks'
+  size_t sum_bytes() const { return 8 * (static_cast<size_t>(groups()) + chunks.size()); }
   size_t table_bytes() const { return chunks.size() * sizeof(ar_dev::NormChunk) + first.size() * 4; }
 
   ar_status_t prepare() {
     return prepare_on(this, "norm", [&] {
-      const std::vector<char> zeros(sum_bytes(), 0);
-      hipError_t e = ar_host::device_table(&d_sums, zeros.data(), zeros.size());
+      hipError_t e = ar_host::device_table(&d_sums, nullptr, sum_bytes());
       if (e == hipSuccess && !chunks.empty())
         e = ar_host::device_table(&d_chunks, chunks.data(), chunks.size() * sizeof(ar_dev::NormChunk));
       if (e == hipSuccess) e = ar_host::device_table(&d_first, first.data(), first.size() * 4);
@@ -153,22 +152,24 @@ struct ar_norm_plan {
 
 namespace {
 
-// Elements of a chunk: enough chunks to fill the device, and not more than
-// that of a few KiB each; whole 64 x 16 bytes, so that chunks of an aligned
-// tensor stay aligned.
+// Elements of a chunk: whole 64 x 16 bytes, so that chunks of an aligned tensor
+// stay aligned; few gradients in one workgroup, which saves a launch, more of
+// them in enough chunks to fill the device, of 16 KiB at most (174 M bf16
+// gradients: norm 59 us and scaling 124; with 32 KiB 60 and 130, with 8 KiB 59
+// and 118, but 184 M fp32 ones then take 267 instead of 248 to scale).
 int64_t chunk_elements(int64_t count, bool bf16) {
   const int64_t piece = bf16 ? 512 : 256;
+  if (count <= ar_dev::kNormWaves * 8 * piece)
+    return std::max(piece, (count / ar_dev::kNormWaves + piece - 1) / piece * piece);
   const int64_t even = (count / (256 * 16) + piece - 1) / piece * piece;
-  return std::clamp<int64_t>(even, piece, 32 * piece);
+  return std::clamp<int64_t>(even, piece, 16 * piece);
 }
 
 ar_dev::NormArgs norm_args(const ar_norm_plan *p) {
   ar_dev::NormArgs a{};
-  char *sums = static_cast<char *>(p->d_sums);
   a.chunks = static_cast<const ar_dev::NormChunk *>(p->d_chunks);
   a.first = static_cast<const int32_t *>(p->d_first);
-  a.arrived = reinterpret_cast<uint32_t *>(sums);
-  a.group_sums = reinterpret_cast<double *>(sums + 256);
+  a.group_sums = static_cast<double *>(p->d_sums);
   a.chunk_sums = a.group_sums + p->groups();
   a.nchunks = static_cast<int32_t>(p->chunks.size());
   a.ntensors = p->ntensors;
