@@ -13,6 +13,26 @@
 namespace ar_dev {
 namespace {
 
+// The value of another lane by a data-parallel primitive, `none` where there is
+// no such lane or the masks leave it out.
+template <int CTRL, int ROWS = 0xf>
+__device__ __forceinline__ int lane_moved(int none, int v) {
+  return __builtin_amdgcn_update_dpp(none, v, CTRL, ROWS, 0xf, false);
+}
+// Inclusive scan over the wave: rows of 16 lanes by shifts of 1, 2, 4 and 8,
+// then the last lane of a row to the next row, and of the first half to the
+// second.  f(identity, v) = v.  (Twelve lane permutations through the LDS instead
+// take about a microsecond of every workgroup's start.)
+template <class F>
+__device__ __forceinline__ int wave_scan(int v, int identity, F f) {
+  v = f(lane_moved<0x111>(identity, v), v);
+  v = f(lane_moved<0x112>(identity, v), v);
+  v = f(lane_moved<0x114>(identity, v), v);
+  v = f(lane_moved<0x118>(identity, v), v);
+  v = f(lane_moved<0x142, 0xa>(identity, v), v);
+  return f(lane_moved<0x143, 0xc>(identity, v), v);
+}
+
 // Running maximum of the ends, 64 experts at a time: one call gives lane l
 // the first and one-past-last row of expert e0 + l (an empty range from the
 // last expert on).  carry: the end before expert e0; updated.
@@ -21,26 +41,14 @@ __device__ __forceinline__ void scan_ends(const A &a, int e0, int &carry, int &l
   const int lane = threadIdx.x & 63, e = e0 + lane;
   int v = e < a.experts ? a.ends[e] : 0;
   v = max(0, min(v, static_cast<int>(a.tokens)));
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int u = __shfl_up(v, d);
-    if (lane >= d) v = max(v, u);
-  }
-  v = max(v, carry);
-  const int prev = __shfl_up(v, 1);
-  lo = lane == 0 ? carry : prev;
+  v = max(wave_scan(v, 0, [](int p, int q) { return max(p, q); }), carry);
+  lo = lane_moved<0x138>(carry, v);  // the lane before
   hi = v;
-  carry = __shfl(v, 63);
+  carry = __builtin_amdgcn_readlane(v, 63);
 }
 
 __device__ __forceinline__ int wave_sum_to(int v) {  // inclusive prefix sum
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int u = __shfl_up(v, d);
-    if (lane >= d) v += u;
-  }
-  return v;
+  return wave_scan(v, 0, [](int p, int q) { return p + q; });
 }
 
 struct RowTile {
@@ -65,24 +73,23 @@ __device__ __forceinline__ void band_tile(int l, int mt, int nt, int &m, int &n)
   n = r / in;
 }
 
-// The tile of place `at`: of `nt` column tiles times the row tiles of all
-// experts, in runs of neighbours per XCD.  A workgroup's own place is its
-// number.
+// This workgroup's tile: of `nt` column tiles times the row tiles of all
+// experts, in runs of neighbours per XCD.
 template <int BM, class A>
-__device__ __forceinline__ bool find_row_tile(const A &a, int nt, RowTile &t, int64_t at = blockIdx.x) {
+__device__ __forceinline__ bool find_row_tile(const A &a, int nt, RowTile &t) {
   int carry = 0, lo, hi, total = 0;
   // the tiles up to and of this lane's expert, of the experts from e0 on
   auto scan = [&](int e0, int &mt, int &upto) {
     scan_ends(a, e0, carry, lo, hi);
     mt = (hi - lo + BM - 1) / BM;
     upto = wave_sum_to(mt);
-    return __shfl(upto, 63);
+    return __builtin_amdgcn_readlane(upto, 63);
   };
   int mt, upto, batch = 0;
   for (int e0 = 0; e0 < a.experts; e0 += 64) total += batch = scan(e0, mt, upto);
   const int64_t tiles = static_cast<int64_t>(total) * nt;
-  if (at >= tiles) return false;
-  int64_t want = xcd_run(at, tiles);
+  if (blockIdx.x >= tiles) return false;
+  int64_t want = xcd_run(blockIdx.x, tiles);
   const bool again = a.experts > 64;  // the scan's registers hold the only batch otherwise
   carry = 0;
   for (int e0 = 0; e0 < a.experts; e0 += 64) {
@@ -92,14 +99,14 @@ __device__ __forceinline__ bool find_row_tile(const A &a, int nt, RowTile &t, in
       continue;
     }
     const int l = __builtin_ctzll(__ballot(static_cast<int64_t>(upto) * nt > want));
-    const int mte = __shfl(mt, l);
-    want -= static_cast<int64_t>(__shfl(upto, l) - mte) * nt;
+    const int mte = __builtin_amdgcn_readlane(mt, l);
+    want -= static_cast<int64_t>(__builtin_amdgcn_readlane(upto, l) - mte) * nt;
     int m, n;
     band_tile(static_cast<int>(want), mte, nt, m, n);
-    const int first = __shfl(lo, l) + m * BM;
+    const int first = __builtin_amdgcn_readlane(lo, l) + m * BM;
     t.e = __builtin_amdgcn_readfirstlane(e0 + l);
     t.row = __builtin_amdgcn_readfirstlane(first);
-    t.rows = __builtin_amdgcn_readfirstlane(min(BM, __shfl(hi, l) - first));
+    t.rows = __builtin_amdgcn_readfirstlane(min(BM, __builtin_amdgcn_readlane(hi, l) - first));
     t.tile_n = __builtin_amdgcn_readfirstlane(n);
     t.tile_m = __builtin_amdgcn_readfirstlane(m);
     return true;
