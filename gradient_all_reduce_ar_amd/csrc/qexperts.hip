@@ -302,7 +302,7 @@ struct TileOut16 {
           const fx4 v = acc[pass * IP + i][j];
           const int row = row0 + i * 16, col = col0 + j * 32;
           *reinterpret_cast<ux2 *>(lds + row * kRowBytes + (((col >> 4) ^ (row & kMask)) << 4) + (col & 8)) =
-              ux2{bf16_bits(v[0]) | bf16_bits(v[1]) << 16, bf16_bits(v[2]) | bf16_bits(v[3]) << 16};
+              ux2{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
         }
       __syncthreads();
       constexpr int kAll = kRows * kChunks;
@@ -543,11 +543,11 @@ struct Long8 {
     }
     aim_ahead(q, lda, ldb, q.k - (per - 1) * kStep);
     char *chunks = lds + 2 * kStage;
-    Chunk::move(chunks, q.sa, q.sb, 0);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int j = 0; j < NJ; ++j) acc[i][j] = fx16{};
+    Chunk::move(chunks, q.sa, q.sb, 0);
     loads_done_and_meet();
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -589,8 +589,7 @@ struct Long8 {
 #pragma unroll
         for (int c = 0; c < 4; ++c)
           *reinterpret_cast<ux2 *>(lds + row * kRowBytes + (((rn / 8 + j * 4 + c) ^ (row & 31)) << 4) + (lane >> 5) * 8) =
-              ux2{bf16_bits(acc[i][j][4 * c]) | bf16_bits(acc[i][j][4 * c + 1]) << 16,
-                  bf16_bits(acc[i][j][4 * c + 2]) | bf16_bits(acc[i][j][4 * c + 3]) << 16};
+              ux2{bf16_pair(acc[i][j][4 * c], acc[i][j][4 * c + 1]), bf16_pair(acc[i][j][4 * c + 2], acc[i][j][4 * c + 3])};
     }
     __syncthreads();
     const int chunk = tid % kChunks, c = chunk * 8;
