@@ -10,6 +10,7 @@ with a ``cuda_stream`` attribute (torch streams).
 """
 import ctypes
 import os
+import struct
 import sys
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -213,8 +214,8 @@ def _declare(L):
         "ar_rmsnorm_create": ([sz, ctypes.c_int, ctypes.c_int, ctypes.c_int, dbl], P),
         "ar_rmsnorm_prepare": ([P], ctypes.c_int),
         "ar_rmsnorm_stats": ([P], ar_rmsnorm_stats_t),
-        "ar_rmsnorm_forward": ([P, ctypes.POINTER(ar_rmsnorm_forward_t), sz, P], ctypes.c_int),
-        "ar_rmsnorm_backward": ([P, ctypes.POINTER(ar_rmsnorm_backward_t), sz, P], ctypes.c_int),
+        "ar_rmsnorm_forward": ([P, P, sz, P], ctypes.c_int),
+        "ar_rmsnorm_backward": ([P, P, sz, P], ctypes.c_int),
         "ar_rmsnorm_destroy": ([P], None),
         "ar_qexperts_create": ([ctypes.c_int, sz, sz, ctypes.c_int, psz], P),
         "ar_qexperts_prepare": ([P], ctypes.c_int),
@@ -1120,9 +1121,9 @@ _kinds = {}
 
 def _matrix(info, t, stride, rows, cols, kind, what):
     """(pointer, row stride in elements) of a [rows, cols] argument: a device tensor whose rows are contiguous, or
-    an address (dense without a stride); (None, cols) without one."""
+    an address (dense without a stride); (0, cols) without one."""
     if t is None:
-        return None, cols
+        return 0, cols
     if not hasattr(t, "data_ptr"):
         return int(t), cols if stride is None else int(stride)
     if stride is not None:
@@ -1147,9 +1148,9 @@ def _matrix(info, t, stride, rows, cols, kind, what):
 
 
 def _vector(info, t, count, kind, what):
-    """Pointer of at least count contiguous elements: a device tensor or an address; None without one."""
+    """Pointer of at least count contiguous elements: a device tensor or an address; 0 without one."""
     if t is None:
-        return None
+        return 0
     if not hasattr(t, "data_ptr"):
         return int(t)
     d = t.get_device()
@@ -1211,6 +1212,10 @@ def ar_quantize_rows(x, codes, scales, stream=None, dtype=None, features=None, n
         _raise()
 
 
+# ar_rmsnorm_forward_t and ar_rmsnorm_backward_t, packed at once: setting fields one by one takes longer than the rest
+_FORWARD, _BACKWARD = struct.Struct("8N6N"), struct.Struct("7N4Ni4x")
+
+
 class _RmsInfo:
     __slots__ = ("plan", "features", "elem", "gain", "grad", "device")
 
@@ -1252,23 +1257,16 @@ def ar_rmsnorm_forward(plan, x, gain, residual=None, h=None, y=None, codes=None,
     [tokens, features] with contiguous rows, or addresses (x one: then ntokens; strides: {"x": elements between
     rows, ...} of those that are not dense)."""
     i = _info_of(_rms_info, _RmsInfo, lib().ar_rmsnorm_prepare, plan)
-    n, f, e, st = _tokens(x, ntokens, "x"), i.features, i.elem, strides or {}
-    a = ar_rmsnorm_forward_t()
-    a.x, a.x_stride = _matrix(i, x, st.get("x"), n, f, e, "x")
-    a.gain = _vector(i, gain, f, i.gain, "gain")
-    if residual is not None:
-        a.residual, a.residual_stride = _matrix(i, residual, st.get("residual"), n, f, e, "residual")
-    if h is not None:
-        a.h, a.h_stride = _matrix(i, h, st.get("h"), n, f, e, "h")
-    if y is not None:
-        a.y, a.y_stride = _matrix(i, y, st.get("y"), n, f, e, "y")
-    if codes is not None:
-        a.codes, a.codes_stride = _matrix(i, codes, st.get("codes"), n, f, "codes", "codes")
-    if scales is not None:
-        a.scales, a.scales_stride = _matrix(i, scales, st.get("scales"), n, _blocks(f), "scales", "scales")
-    if rstd is not None:
-        a.rstd = _vector(i, rstd, n, 4, "rstd")
-    if _lib.ar_rmsnorm_forward(plan, ctypes.byref(a), n, _stream(stream)) != AR_OK:
+    n, f, e, st, b = _tokens(x, ntokens, "x"), i.features, i.elem, strides or {}, _blocks(i.features)
+    xp, xs = _matrix(i, x, st.get("x"), n, f, e, "x")
+    rp, rs = _matrix(i, residual, st.get("residual"), n, f, e, "residual")
+    hp, hs = _matrix(i, h, st.get("h"), n, f, e, "h")
+    yp, ys = _matrix(i, y, st.get("y"), n, f, e, "y")
+    cp, cs = _matrix(i, codes, st.get("codes"), n, f, "codes", "codes")
+    sp, ss = _matrix(i, scales, st.get("scales"), n, b, "scales", "scales")
+    a = _FORWARD.pack(xp, rp, _vector(i, gain, f, i.gain, "gain"), hp, yp, cp, sp, _vector(i, rstd, n, 4, "rstd"), xs, rs,
+                      hs, ys, cs, ss)
+    if _lib.ar_rmsnorm_forward(plan, a, n, _stream(stream)) != AR_OK:
         _raise()
 
 
@@ -1278,17 +1276,13 @@ def ar_rmsnorm_backward(plan, dy, h, gain, rstd, dx, dgain, dh=None, accumulate=
     gain's.  Arguments as ar_rmsnorm_forward's; rstd is the forward pass's."""
     i = _info_of(_rms_info, _RmsInfo, lib().ar_rmsnorm_prepare, plan)
     n, f, e, st = _tokens(dy, ntokens, "dy"), i.features, i.elem, strides or {}
-    a = ar_rmsnorm_backward_t()
-    a.dy, a.dy_stride = _matrix(i, dy, st.get("dy"), n, f, e, "dy")
-    a.h, a.h_stride = _matrix(i, h, st.get("h"), n, f, e, "h")
-    a.gain = _vector(i, gain, f, i.gain, "gain")
-    a.rstd = _vector(i, rstd, n, 4, "rstd")
-    a.dx, a.dx_stride = _matrix(i, dx, st.get("dx"), n, f, e, "dx")
-    a.dgain = _vector(i, dgain, f, i.grad, "dgain")
-    if dh is not None:
-        a.dh, a.dh_stride = _matrix(i, dh, st.get("dh"), n, f, e, "dh")
-    a.accumulate = 1 if accumulate else 0
-    if _lib.ar_rmsnorm_backward(plan, ctypes.byref(a), n, _stream(stream)) != AR_OK:
+    dp, ds = _matrix(i, dy, st.get("dy"), n, f, e, "dy")
+    hp, hs = _matrix(i, h, st.get("h"), n, f, e, "h")
+    rp, rs = _matrix(i, dh, st.get("dh"), n, f, e, "dh")
+    xp, xs = _matrix(i, dx, st.get("dx"), n, f, e, "dx")
+    a = _BACKWARD.pack(dp, hp, rp, _vector(i, gain, f, i.gain, "gain"), _vector(i, rstd, n, 4, "rstd"), xp,
+                       _vector(i, dgain, f, i.grad, "dgain"), ds, hs, rs, xs, 1 if accumulate else 0)
+    if _lib.ar_rmsnorm_backward(plan, a, n, _stream(stream)) != AR_OK:
         _raise()
 
 

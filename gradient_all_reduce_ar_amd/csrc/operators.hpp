@@ -198,12 +198,11 @@ struct RmsBackward {
   float *parts;  // [parts][features] sums of dgain
   int64_t dys, hs, dhs, dxs, tokens;
   int32_t features;
-  int32_t max_parts;
   bool bf16, gain_bf16, grad_bf16, accumulate;
 };
 hipError_t rmsnorm_backward(const RmsBackward &a, hipStream_t s);
-// Parts that a plan of such rows has room for.
-int32_t rmsnorm_parts(int64_t features);
+// Parts that such rows are summed in at most.
+int32_t rmsnorm_parts(int64_t features, bool bf16);
 
 // ---- 8-bit products grouped by expert (qexperts.hip)
 

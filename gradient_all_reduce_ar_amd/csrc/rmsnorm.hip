@@ -329,15 +329,20 @@ hipError_t forward_of(const RmsForward &a, hipStream_t s) {
   return forward<BF, 1024, 8>(a, s);
 }
 
-constexpr int32_t kMostParts = 1024;
+// Workgroups of the backward pass at most, about those that run at once; each
+// takes two rows at least (512 rows of 4096: 256 workgroups 13.0 us, 512 of them
+// 14.8).
+int32_t most_parts(int64_t features, bool bf16) {
+  if (features <= 64 * kLane) return 1024;
+  if (features <= 128 * kLane) return 512;
+  if (features <= 256 * kLane) return bf16 ? 1024 : 512;
+  return features <= 512 * kLane ? 512 : 256;
+}
 
-// PARTS: workgroups at most, about those that run at once; each takes two rows
-// at least (512 rows of 4096: 256 workgroups 13.0 us, 512 of them 14.8).
-template <bool BF, int T, int K, int PARTS>
+template <bool BF, int T, int K>
 hipError_t backward(const RmsBackward &a, hipStream_t s) {
-  static_assert(PARTS <= kMostParts, "the workspace has room");
   const int64_t rows = 2 * kTeams<T>, teams = (a.tokens + rows - 1) / rows;
-  const int64_t grid = std::min<int64_t>({teams, PARTS, a.max_parts});
+  const int64_t grid = std::min<int64_t>(teams, most_parts(a.features, BF));
   const LaunchEvents ev = t_launch_events;  // the call's mark goes on its last kernel
   if (grid > 1) t_launch_events = LaunchEvents{};
   const hipError_t e = launch(rms_backward<BF, T, K>, grid, 1, kRowThreads<T>, 0, s, a);
@@ -356,14 +361,14 @@ hipError_t backward(const RmsBackward &a, hipStream_t s) {
 template <bool BF>
 hipError_t backward_of(const RmsBackward &a, hipStream_t s) {
   const int64_t c = (a.features + kLane - 1) / kLane;
-  if (c <= 64) return backward<BF, 64, 1, 1024>(a, s);
-  if (c <= 128) return backward<BF, 64, 2, 512>(a, s);
-  if (c <= 256) return backward<BF, 256, 1, BF ? 1024 : 512>(a, s);
-  if (c <= 512) return backward<BF, 512, 1, 512>(a, s);
-  if (c <= 1024) return backward<BF, 512, 2, 256>(a, s);
-  if (c <= 2048) return backward<BF, 1024, 2, 256>(a, s);
-  if (c <= 4096) return backward<BF, 1024, 4, 256>(a, s);
-  return backward<BF, 1024, 8, 256>(a, s);
+  if (c <= 64) return backward<BF, 64, 1>(a, s);
+  if (c <= 128) return backward<BF, 64, 2>(a, s);
+  if (c <= 256) return backward<BF, 256, 1>(a, s);
+  if (c <= 512) return backward<BF, 512, 1>(a, s);
+  if (c <= 1024) return backward<BF, 512, 2>(a, s);
+  if (c <= 2048) return backward<BF, 1024, 2>(a, s);
+  if (c <= 4096) return backward<BF, 1024, 4>(a, s);
+  return backward<BF, 1024, 8>(a, s);
 }
 
 }  // namespace
@@ -385,8 +390,6 @@ hipError_t rmsnorm_backward(const RmsBackward &a, hipStream_t s) {
   return a.bf16 ? backward_of<true>(a, s) : backward_of<false>(a, s);
 }
 
-int32_t rmsnorm_parts(int64_t features) {
-  return static_cast<int32_t>(std::clamp<int64_t>((int64_t{64} << 20) / (4 * features), 1, kMostParts));
-}
+int32_t rmsnorm_parts(int64_t features, bool bf16) { return most_parts(features, bf16); }
 
 }  // namespace ar_dev

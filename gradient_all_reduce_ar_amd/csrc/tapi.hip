@@ -298,7 +298,6 @@ ar_status_t backward(ar_rmsnorm *p, const ar_rmsnorm_backward_t &q, size_t ntoke
   a.dxs = static_cast<int64_t>(q.dx_stride);
   a.tokens = t;
   a.features = static_cast<int32_t>(f);
-  a.max_parts = p->parts;
   a.bf16 = p->bf16;
   a.gain_bf16 = p->gain_bf16;
   a.grad_bf16 = p->grad_bf16;
@@ -561,7 +560,7 @@ ar_rmsnorm_t *ar_rmsnorm_create(size_t features, ar_dtype_t dtype, ar_dtype_t ga
     p->gain_bf16 = w == AR_BFLOAT16;
     p->grad_bf16 = g == AR_BFLOAT16;
     p->eps = eps;
-    p->parts = ar_dev::rmsnorm_parts(p->features);
+    p->parts = ar_dev::rmsnorm_parts(p->features, p->bf16);
     return AR_OK;
   });
   return st == AR_OK ? p : nullptr;

@@ -274,3 +274,8 @@ def test_structs_are_as_the_header_has_them(tmp_path):
     subprocess.run(["gcc", "-std=c99", "-I", os.path.join(root, "include"), str(src), "-o", str(tmp_path / "s")], check=True)
     sizes = [int(v) for v in subprocess.run([str(tmp_path / "s")], capture_output=True, text=True, check=True).stdout.split()]
     assert sizes == [ctypes.sizeof(getattr(B, n)) for n in names]
+    for packed, fields in ((B._FORWARD, B.ar_rmsnorm_forward_t), (B._BACKWARD, B.ar_rmsnorm_backward_t)):
+        values = list(range(1, len(fields._fields_) + 1))
+        assert packed.size == ctypes.sizeof(fields)
+        made = fields.from_buffer_copy(packed.pack(*values))
+        assert [getattr(made, k) for k, _ in fields._fields_] == values
