@@ -2,6 +2,8 @@
 import os
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -28,14 +30,7 @@ HIPCC_FLAGS = [
 ]
 
 
-def build(out=LIB, defines=(), verbose=False, sanitize=False):
-    hipcc = os.path.join(os.environ.get("ROCM_PATH", "/opt/rocm"), "bin", "hipcc")
-    objs = []
-    tmpdir = os.path.join(HERE, "_build")
-    os.makedirs(tmpdir, exist_ok=True)
-    defs = [f"-D{d}" for d in defines]
-    san = SANITIZE_FLAGS if sanitize else []
-    cmd = [hipcc, *HIPCC_FLAGS, *san, *defs, "-o", out] + [os.path.join(CSRC, s) for s in SOURCES]
+def _run(cmd, verbose):
     if verbose:
         print(" ".join(cmd))
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -47,7 +42,22 @@ def build(out=LIB, defines=(), verbose=False, sanitize=False):
     for line in (r.stdout + r.stderr).splitlines():
         if noise not in line and line.strip() and verbose:
             print(line)
-    del objs
+
+
+def build(out=LIB, defines=(), verbose=False, sanitize=False):
+    """Compiles every source, several at a time, and links them."""
+    hipcc = os.path.join(os.environ.get("ROCM_PATH", "/opt/rocm"), "bin", "hipcc")
+    os.makedirs(os.path.join(HERE, "_build"), exist_ok=True)
+    flags = [*HIPCC_FLAGS, *(SANITIZE_FLAGS if sanitize else []), *[f"-D{d}" for d in defines]]
+    with tempfile.TemporaryDirectory(dir=os.path.join(HERE, "_build")) as tmp:
+        def compiled(source):
+            obj = os.path.join(tmp, source + ".o")
+            _run([hipcc, *[f for f in flags if f != "-shared"], "-c", "-o", obj, os.path.join(CSRC, source)], verbose)
+            return obj
+
+        with ThreadPoolExecutor(min(8, int(os.environ.get("MAX_JOBS", 8)))) as pool:
+            objs = list(pool.map(compiled, SOURCES))
+        _run([hipcc, *flags, "-o", out, *objs], verbose)
     return out
 
 
