@@ -1230,6 +1230,14 @@ class _RmsInfo:
 
 
 _rms_info = {}
+_FORWARD_ROWS, _BACKWARD_ROWS = ({k[:-7] for k, _ in t._fields_ if k.endswith("_stride")}
+                                 for t in (ar_rmsnorm_forward_t, ar_rmsnorm_backward_t))
+
+
+def _strides(given, names):
+    if given and not names.issuperset(given):
+        raise ValueError(f"strides of {sorted(set(given) - names)}: rows are {sorted(names)}")
+    return given or {}
 
 
 def ar_rmsnorm_create(features, dtype, gain_dtype=None, grad_dtype=None, eps=1e-6):
@@ -1257,7 +1265,8 @@ def ar_rmsnorm_forward(plan, x, gain, residual=None, h=None, y=None, codes=None,
     [tokens, features] with contiguous rows, or addresses (x one: then ntokens; strides: {"x": elements between
     rows, ...} of those that are not dense)."""
     i = _info_of(_rms_info, _RmsInfo, lib().ar_rmsnorm_prepare, plan)
-    n, f, e, st, b = _tokens(x, ntokens, "x"), i.features, i.elem, strides or {}, _blocks(i.features)
+    n, f, e, b = _tokens(x, ntokens, "x"), i.features, i.elem, _blocks(i.features)
+    st = _strides(strides, _FORWARD_ROWS)
     xp, xs = _matrix(i, x, st.get("x"), n, f, e, "x")
     rp, rs = _matrix(i, residual, st.get("residual"), n, f, e, "residual")
     hp, hs = _matrix(i, h, st.get("h"), n, f, e, "h")
@@ -1275,7 +1284,7 @@ def ar_rmsnorm_backward(plan, dy, h, gain, rstd, dx, dgain, dh=None, accumulate=
     """dx = the gradient of x (and of residual) for the gradients dy of y and dh of h; dgain = (the old dgain +) the
     gain's.  Arguments as ar_rmsnorm_forward's; rstd is the forward pass's."""
     i = _info_of(_rms_info, _RmsInfo, lib().ar_rmsnorm_prepare, plan)
-    n, f, e, st = _tokens(dy, ntokens, "dy"), i.features, i.elem, strides or {}
+    n, f, e, st = _tokens(dy, ntokens, "dy"), i.features, i.elem, _strides(strides, _BACKWARD_ROWS)
     dp, ds = _matrix(i, dy, st.get("dy"), n, f, e, "dy")
     hp, hs = _matrix(i, h, st.get("h"), n, f, e, "h")
     rp, rs = _matrix(i, dh, st.get("dh"), n, f, e, "dh")

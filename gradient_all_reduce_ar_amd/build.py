@@ -55,7 +55,7 @@ def build(out=LIB, defines=(), verbose=False, sanitize=False):
             _run([hipcc, *[f for f in flags if f != "-shared"], "-c", "-o", obj, os.path.join(CSRC, source)], verbose)
             return obj
 
-        with ThreadPoolExecutor(min(8, int(os.environ.get("MAX_JOBS", 8)))) as pool:
+        with ThreadPoolExecutor(max(1, min(8, int(os.environ.get("MAX_JOBS") or 8)))) as pool:
             objs = list(pool.map(compiled, SOURCES))
         _run([hipcc, *flags, "-o", out, *objs], verbose)
     return out

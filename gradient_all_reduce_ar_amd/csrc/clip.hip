@@ -8,7 +8,10 @@
 // are not touched.  Bound by memory: the norm reads every gradient, and the
 // scaling, which needs the whole norm first, reads it again and writes it.  The
 // squares in fp64 cost nothing beside that (fp32 ones take the same time).
-// Loads and stores are non-temporal: neither pass finds what the other read.
+// The norm's loads are ordinary ones, and the scaling finds part of what they
+// left; its own loads and its stores are non-temporal (norm and scaling of 174 M
+// bf16 gradients to another arena 167 us; with non-temporal loads in the norm too
+// 183, with ordinary stores 206; going backwards over the chunks 170).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -94,11 +97,11 @@ __device__ __forceinline__ double chunk_squares(const NormArgs &a, const NormChu
   for (; i + 64 * (kBatch - 1) < pieces; i += 64 * kBatch) {
     ux4 u[kBatch];
 #pragma unroll
-    for (int j = 0; j < kBatch; ++j) u[j] = __builtin_nontemporal_load(v + i + 64 * j);
+    for (int j = 0; j < kBatch; ++j) u[j] = v[i + 64 * j];
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) add(u[j]);
   }
-  for (; i < pieces; i += 64) add(__builtin_nontemporal_load(v + i));
+  for (; i < pieces; i += 64) add(v[i]);
   return wave_total(s[0] + s[1]);
 }
 

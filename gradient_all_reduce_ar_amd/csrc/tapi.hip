@@ -65,6 +65,12 @@ ar_status_t check_pointer(const void *p, uintptr_t elem, const char *name) {
   return AR_OK;
 }
 
+ar_status_t launched(hipError_t e, const char *what) {
+  if (e == hipErrorInvalidConfiguration)
+    return fail(AR_ERR_UNSUPPORTED, std::string(what) + " larger than one launch grid");
+  return e == hipSuccess ? AR_OK : hip_fail(e, "kernel launch");
+}
+
 // Launches f on s and marks the call's end.
 template <class F>
 ar_status_t run_marked(ar_host::CallMarks &marks, hipStream_t s, const char *what, F f) {
@@ -74,9 +80,7 @@ ar_status_t run_marked(ar_host::CallMarks &marks, hipStream_t s, const char *wha
   ar_dev::t_launch_events = ar_dev::LaunchEvents{nullptr, mark};
   const hipError_t e = f();
   ar_dev::t_launch_events = ar_dev::LaunchEvents{};
-  if (e == hipErrorInvalidConfiguration)
-    return fail(AR_ERR_UNSUPPORTED, std::string(what) + " larger than one launch grid");
-  return e == hipSuccess ? AR_OK : hip_fail(e, "kernel launch");
+  return launched(e, what);
 }
 
 // Allocates a plan's device memory with f on the current device, once.
@@ -154,9 +158,9 @@ namespace {
 
 // Elements of a chunk: whole 64 x 16 bytes, so that chunks of an aligned tensor
 // stay aligned; few gradients in one workgroup, which saves a launch, more of
-// them in enough chunks to fill the device, of 16 KiB at most (174 M bf16
-// gradients: norm 59 us and scaling 124; with 32 KiB 60 and 130, with 8 KiB 59
-// and 118, but 184 M fp32 ones then take 267 instead of 248 to scale).
+// them in enough chunks to fill the device, of 16 KiB at most (norm and
+// scaling of 174 M bf16 gradients 167 us; with 32 KiB 171, with 8 KiB 164, but 184 M
+// fp32 ones then take 371 instead of 356).
 int64_t chunk_elements(int64_t count, bool bf16) {
   const int64_t piece = bf16 ? 512 : 256;
   if (count <= ar_dev::kNormWaves * 8 * piece)
@@ -254,8 +258,8 @@ ar_status_t forward(ar_rmsnorm *p, const ar_rmsnorm_forward_t &q, size_t ntokens
   a.eps = p->eps;
   a.bf16 = p->bf16;
   a.gain_bf16 = p->gain_bf16;
-  hipStream_t s = static_cast<hipStream_t>(stream);
-  return run_marked(p->marks, s, "RMS norm", [&] { return ar_dev::rmsnorm_forward(a, s); });
+  // nothing of the plan's is read on the device, so destroying it need not wait for this: no mark
+  return launched(ar_dev::rmsnorm_forward(a, static_cast<hipStream_t>(stream)), "RMS norm");
 }
 
 ar_status_t backward(ar_rmsnorm *p, const ar_rmsnorm_backward_t &q, size_t ntokens, void *stream) {

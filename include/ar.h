@@ -1019,15 +1019,15 @@ typedef struct {
  * leaves it).  Forward calls use no workspace and may be in flight together;
  * backward calls of one plan must not overlap in time, replays of captured
  * ones included.  AR_ERR_INVALID_ARG for bad arguments or another device than
- * the plan's; AR_ERR_UNSUPPORTED for more rows than one launch grid takes (2^25
- * of up to 1024 features, 2^21 of the longest); AR_ERR_OOM / AR_ERR_HIP as
+ * the plan's; AR_ERR_UNSUPPORTED for more rows than one launch grid takes (2^25 - 4
+ * of up to 1024 features, 2^21 - 1 of the longest); AR_ERR_OOM / AR_ERR_HIP as
  * above.  The structs are read during the call (a captured graph keeps their
  * values).
  */
 ar_status_t ar_rmsnorm_forward(ar_rmsnorm_t *plan, const ar_rmsnorm_forward_t *args, size_t ntokens, void *stream);
 ar_status_t ar_rmsnorm_backward(ar_rmsnorm_t *plan, const ar_rmsnorm_backward_t *args, size_t ntokens, void *stream);
-/* Waits for the plan's calls in flight (captured ones are the caller's to
- * finish) and releases it. */
+/* Waits for the plan's backward calls in flight (captured ones are the caller's
+ * to finish) and releases it.  Forward calls use nothing of it on the device. */
 void ar_rmsnorm_destroy(ar_rmsnorm_t *plan);
 
 /* ---- Products grouped by expert, in 8 bits ----

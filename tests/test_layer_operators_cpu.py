@@ -261,6 +261,13 @@ def test_binding_checks_tensors(rms, experts, norm):
         B.ar_grad_norm(norm, torch.zeros(600, dtype=torch.bfloat16), far(1))
 
 
+def test_binding_refuses_unknown_strides(rms):
+    with pytest.raises(ValueError, match="strides of"):
+        B.ar_rmsnorm_forward(rms, far(0), far(1), y=far(2), ntokens=4, strides={"code": 300})
+    with pytest.raises(ValueError, match="strides of"):
+        B.ar_rmsnorm_backward(rms, far(0), far(1), far(2), far(3), far(4), far(5), ntokens=4, strides={"y": 300})
+
+
 def test_structs_are_as_the_header_has_them(tmp_path):
     """Sizes of the structs that cross the ABI, from a C compiler."""
     import os
