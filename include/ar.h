@@ -954,7 +954,8 @@ ar_status_t ar_quantize_rows(const void *x, ar_dtype_t dtype, size_t x_stride, v
  *   dgain = sum over the rows of dy xhat    (+ the old dgain with accumulate)
  *
  * dx is the gradient of x and of residual alike.  The mean of squares is
- * formed in fp64, the rest in fp32 with one rounding to the output's type.
+ * formed in fp64, dgain's parts are added in fp64, and the rest is fp32 with one
+ * rounding to the output's type.
  * Infinities and NaN spread as in the formulas: a row's only into the row's
  * own results, and into dgain.  Results depend on the inputs and the number
  * of rows alone (no atomics).
