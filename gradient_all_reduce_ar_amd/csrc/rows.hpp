@@ -83,12 +83,14 @@ __device__ __forceinline__ Raw8<BF> rounded8(const float (&v)[kLane]) {
   return r;
 }
 
-template <bool BF>
+// NT: non-temporal (whole pieces of 16 bits).
+template <bool BF, bool NT = false>
 __device__ __forceinline__ void store8(void *base, int64_t at, const Raw8<BF> &r, int n) {
   if constexpr (BF) {
     uint16_t *p = static_cast<uint16_t *>(base) + at;
     if (n >= kLane) {
-      *reinterpret_cast<ux4_at2 *>(p) = r.v[0];
+      if constexpr (NT) __builtin_nontemporal_store(r.v[0], reinterpret_cast<ux4_at2 *>(p));
+      else *reinterpret_cast<ux4_at2 *>(p) = r.v[0];
     } else {
 #pragma unroll
       for (int i = 0; i < kLane - 1; ++i)
@@ -151,9 +153,11 @@ __device__ __forceinline__ ux2 codes8(const float (&v)[kLane], uint32_t byte) {
   return r;
 }
 
+template <bool NT = false>
 __device__ __forceinline__ void store_codes(uint8_t *p, ux2 c, int n) {
   if (n >= kLane) {
-    *reinterpret_cast<ux2_at1 *>(p) = c;
+    if constexpr (NT) __builtin_nontemporal_store(c, reinterpret_cast<ux2_at1 *>(p));
+    else *reinterpret_cast<ux2_at1 *>(p) = c;
   } else {
 #pragma unroll
     for (int i = 0; i < kLane - 1; ++i)
