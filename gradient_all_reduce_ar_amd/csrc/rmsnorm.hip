@@ -317,7 +317,8 @@ hipError_t forward(const RmsForward &a, hipStream_t s) {
 }
 
 // Teams and pieces: few pieces to a thread, so that many rows are under way.
-// Microseconds, bf16, residual, h, y and codes (rows x features):
+// Microseconds, bf16, residual, h, y and codes, all by ordinary stores (rows x
+// features):
 //   32768 x 512:   64 threads, 1 piece  33.3;  64, 2  35.5;  256, 1  60.8
 //   16384 x 1024:  64, 2  33.9;  64, 4  36.7;  256, 1  39.4
 //   16384 x 2048:  256, 1  57.2;  64, 4  62.0;  256, 2  61.3;  512, 1  71.6
