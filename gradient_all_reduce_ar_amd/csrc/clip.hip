@@ -52,13 +52,18 @@ struct Grad {
   }
 };
 
-// A chunk's elements from its first 16-byte boundary on: [lead, lead + 16-byte
-// pieces), then the rest.  Addresses go by the arena's own alignment.
-template <class T>
-__device__ __forceinline__ int lead_of(const T *p, int n) {
-  const int past = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15);
-  return min(n, past == 0 ? 0 : (16 - past) / static_cast<int>(sizeof(T)));
+// A chunk's elements before its 16-byte pieces: those up to the next multiple of
+// kVec elements of the arena, for the norm, whose order is the plan's then, at
+// any address; for the scaling, which has none, up to a boundary of what is
+// written.
+template <bool BF>
+__device__ __forceinline__ int lead_of(uint64_t at, int n) {
+  constexpr int kVec = Grad<BF>::kVec;
+  return min(n, static_cast<int>(-at & (kVec - 1)));
 }
+
+// 16 bytes at any element's address: the hardware takes such loads.
+typedef uint32_t ux4_any __attribute__((ext_vector_type(4), aligned(2)));
 
 __device__ __forceinline__ double wave_total(double v) {
 #pragma unroll
@@ -74,7 +79,7 @@ __device__ __forceinline__ double chunk_squares(const NormArgs &a, const NormChu
   using T = typename G::T;
   const int lane = threadIdx.x & 63;
   const T *p = static_cast<const T *>(a.g) + c.at;
-  const int lead = lead_of(p, c.count), pieces = (c.count - lead) / G::kVec;
+  const int lead = lead_of<BF>(static_cast<uint64_t>(c.at), c.count), pieces = (c.count - lead) / G::kVec;
   const int tail = lead + pieces * G::kVec;
   double s[2] = {0, 0};
   if (lane < lead) {
@@ -85,7 +90,7 @@ __device__ __forceinline__ double chunk_squares(const NormArgs &a, const NormChu
     const double d = G::wide(p[tail + lane]);
     s[1] = d * d;
   }
-  const ux4 *v = reinterpret_cast<const ux4 *>(p + lead);
+  const ux4_any *v = reinterpret_cast<const ux4_any *>(p + lead);
   auto add = [&](ux4 u) {
     float f[G::kVec];
     G::split(u, f);
@@ -168,11 +173,11 @@ __global__ __launch_bounds__(kNormThreads) void clip_chunks(NormArgs a) {
   const NormChunk chunk = table_entry(a.chunks + id);
   const T *p = static_cast<const T *>(a.g) + chunk.at;
   T *q = static_cast<T *>(a.out) + chunk.at;
-  const int lead = lead_of(q, chunk.count), pieces = (chunk.count - lead) / G::kVec;  // whole 16 bytes are written
+  const int lead = lead_of<BF>(reinterpret_cast<uintptr_t>(q) / sizeof(T), chunk.count);
+  const int pieces = (chunk.count - lead) / G::kVec;
   const int tail = lead + pieces * G::kVec;
   if (lane < lead) q[lane] = G::narrow(G::wide(p[lane]) * c);
   if (tail + lane < chunk.count) q[tail + lane] = G::narrow(G::wide(p[tail + lane]) * c);
-  typedef uint32_t ux4_any __attribute__((ext_vector_type(4), aligned(2)));  // the two arenas may lie differently
   const ux4_any *v = reinterpret_cast<const ux4_any *>(p + lead);
   ux4 *w = reinterpret_cast<ux4 *>(q + lead);
   auto scaled = [&](ux4 u) {

@@ -259,3 +259,45 @@ def test_tensor_checks():
     with pytest.raises(ValueError, match="holds"):
         B.ar_grad_norm(c.plan, c.grads, c.norm, c.each[:0])
     B.ar_norm_plan_destroy(c.plan)
+
+
+def near_a_tie(dtype):
+    """Gradients whose squares add up to hardly more than the middle between two fp32 norms: a chunk's worth of small
+    ones with a large one behind them, which take the norm to the other side where they are added to it one by one.
+    (Counts so that a chunk of the plan is an eighth of them, a wave's work.)"""
+    n, lost = {"fp32": (16384, 16), "bf16": (32768, 32)}[dtype]
+    chunk, small, middle = n // 8, 2.0 ** -3, (1 << 24) + 1
+    g = torch.zeros(n, dtype=torch.float64)
+    g[:chunk - 1], g[chunk - 1] = small, 2.0 ** 24
+    rest = middle ** 2 + lost / 2 * small ** 2 - float(g.square().sum())  # in other chunks
+    at = 2 * chunk
+    while rest >= 1:
+        v = torch.tensor(math.floor(math.sqrt(rest))).to(T[dtype])
+        if float(v) ** 2 > rest:
+            v = torch.nextafter(v, torch.zeros_like(v))
+        g[at] = float(v)
+        rest, at = rest - float(v) ** 2, at + 3
+    left = int(rest / small ** 2)
+    g[3 * chunk:3 * chunk + left] = small
+    assert float(g.square().sum()) == middle ** 2 + lost / 2 * small ** 2 and torch.equal(g.to(T[dtype]).double(), g)
+    return g.to(T[dtype])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_norm_is_the_same_at_any_address(dtype):
+    """The order of the sums is the plan's: the same gradients have the same norm wherever their arena lies."""
+    g = near_a_tie(dtype)
+    n = g.numel()
+    plan = B.ar_norm_plan_create([n], dtype)
+    got = []
+    for shift in range(8):
+        arena = torch.zeros(n + 8, device=DEV, dtype=T[dtype])
+        arena[shift:shift + n] = g.to(DEV)
+        norm, each = torch.zeros(1, device=DEV), torch.zeros(1, device=DEV)
+        B.ar_grad_norm(plan, arena[shift:shift + n], norm, each)
+        torch.cuda.synchronize()
+        got.append((float(norm), float(each)))
+    assert len(set(got)) == 1, got
+    assert abs(got[0][0] - ((1 << 24) + 1)) <= 1  # either neighbour of the middle
+    B.ar_norm_plan_destroy(plan)
