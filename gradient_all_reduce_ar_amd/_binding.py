@@ -1171,12 +1171,11 @@ def _vector(info, t, count, kind, what):
 
 
 class _CurrentDevice:
-    """The checks of a call without a plan: its tensors lie on the current device."""
-
-    def __init__(self):
-        self.device = sys.modules["torch"].cuda.current_device()
+    """The checks of a call that no plan binds to a device: its tensors lie on the current one."""
+    device = None
 
     def find_device(self):
+        self.device = sys.modules["torch"].cuda.current_device()
         return self.device
 
 
@@ -1204,7 +1203,7 @@ def ar_quantize_rows(x, codes, scales, stream=None, dtype=None, features=None, n
             raise ValueError("x is an address: dtype, features and ntokens are needed")
         n, f, d = int(ntokens), int(features), _code(DTYPES, dtype)
         elem = 2 if d == AR_BFLOAT16 else 4
-    info = _CurrentDevice() if any(hasattr(t, "data_ptr") for t in (x, codes, scales)) else None
+    info = _CurrentDevice()
     xp, xs = _matrix(info, x, x_stride, n, f, elem, "x")
     cp, cs = _matrix(info, codes, codes_stride, n, f, "codes", "codes")
     sp, ss = _matrix(info, scales, scales_stride, n, _blocks(f), "scales", "scales")
@@ -1252,6 +1251,7 @@ def ar_rmsnorm_create(features, dtype, gain_dtype=None, grad_dtype=None, eps=1e-
 
 def ar_rmsnorm_prepare(plan):
     _check(lib().ar_rmsnorm_prepare(plan))
+    _info_of(_rms_info, _RmsInfo, lib().ar_rmsnorm_prepare, plan).find_device()
 
 
 def ar_rmsnorm_stats(plan):
@@ -1265,7 +1265,9 @@ def ar_rmsnorm_forward(plan, x, gain, residual=None, h=None, y=None, codes=None,
     [tokens, features] with contiguous rows, or addresses (x one: then ntokens; strides: {"x": elements between
     rows, ...} of those that are not dense)."""
     i = _info_of(_rms_info, _RmsInfo, lib().ar_rmsnorm_prepare, plan)
-    n, f, e, b = _tokens(x, ntokens, "x"), i.features, i.elem, _blocks(i.features)
+    n, f, e, b, gain_bytes = _tokens(x, ntokens, "x"), i.features, i.elem, _blocks(i.features), i.gain
+    if i.device is None:  # not prepared, which this call does not need
+        i = _CurrentDevice()
     st = _strides(strides, _FORWARD_ROWS)
     xp, xs = _matrix(i, x, st.get("x"), n, f, e, "x")
     rp, rs = _matrix(i, residual, st.get("residual"), n, f, e, "residual")
@@ -1273,7 +1275,7 @@ def ar_rmsnorm_forward(plan, x, gain, residual=None, h=None, y=None, codes=None,
     yp, ys = _matrix(i, y, st.get("y"), n, f, e, "y")
     cp, cs = _matrix(i, codes, st.get("codes"), n, f, "codes", "codes")
     sp, ss = _matrix(i, scales, st.get("scales"), n, b, "scales", "scales")
-    a = _FORWARD.pack(xp, rp, _vector(i, gain, f, i.gain, "gain"), hp, yp, cp, sp, _vector(i, rstd, n, 4, "rstd"), xs, rs,
+    a = _FORWARD.pack(xp, rp, _vector(i, gain, f, gain_bytes, "gain"), hp, yp, cp, sp, _vector(i, rstd, n, 4, "rstd"), xs, rs,
                       hs, ys, cs, ss)
     if _lib.ar_rmsnorm_forward(plan, a, n, _stream(stream)) != AR_OK:
         _raise()

@@ -83,16 +83,23 @@ ar_status_t run_marked(ar_host::CallMarks &marks, hipStream_t s, const char *wha
   return launched(e, what);
 }
 
+// Where a plan is prepared, its device has to be the current one.
+template <class P>
+ar_status_t check_device(const P *p, const char *what) {
+  if (p->device < 0) return AR_OK;
+  int dev = 0;
+  const hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return hip_fail(e, "hipGetDevice");
+  return dev == p->device ? AR_OK : fail(AR_ERR_INVALID_ARG, std::string(what) + " plan was prepared on another device");
+}
+
 // Allocates a plan's device memory with f on the current device, once.
 template <class P, class F>
 ar_status_t prepare_on(P *p, const char *what, F f) {
+  if (p->device >= 0) return check_device(p, what);
   int dev = 0;
   hipError_t e = hipGetDevice(&dev);
   if (e != hipSuccess) return hip_fail(e, "hipGetDevice");
-  if (p->device >= 0) {
-    if (dev != p->device) return fail(AR_ERR_INVALID_ARG, std::string(what) + " plan was prepared on another device");
-    return AR_OK;
-  }
   e = f();
   if (e != hipSuccess) {
     p->release();
@@ -236,7 +243,9 @@ ar_status_t forward(ar_rmsnorm *p, const ar_rmsnorm_forward_t &q, size_t ntokens
                      {{q.x, bx, "x"}, {q.residual, br, "residual"}, {q.gain, p->gain_bytes(), "gain"}}, may);
     if (st != AR_OK) return st;
   }
-  st = prepare_for(p, stream);
+  // the kernel uses nothing of the plan's: no workspace for it, which a program that only runs forward would never
+  // touch, and no mark, since destroying the plan need not wait
+  st = check_device(p, "RMS norm");
   if (st != AR_OK || t == 0) return st;
   ar_dev::RmsForward a{};
   a.x = q.x;
@@ -258,7 +267,6 @@ ar_status_t forward(ar_rmsnorm *p, const ar_rmsnorm_forward_t &q, size_t ntokens
   a.eps = p->eps;
   a.bf16 = p->bf16;
   a.gain_bf16 = p->gain_bf16;
-  // nothing of the plan's is read on the device, so destroying it need not wait for this: no mark
   return launched(ar_dev::rmsnorm_forward(a, static_cast<hipStream_t>(stream)), "RMS norm");
 }
 

@@ -979,8 +979,10 @@ typedef struct {
 ar_rmsnorm_t *ar_rmsnorm_create(size_t features, ar_dtype_t dtype, ar_dtype_t gain_dtype, ar_dtype_t grad_dtype,
                                 double eps);
 /* Allocates the plan's workspace (of the backward pass, at most 64 MiB) on the
- * current device (the first call does it otherwise; one that is captured into
- * a HIP graph before is refused with AR_ERR_INVALID_ARG). */
+ * current device (the first backward call does it otherwise; one that is
+ * captured into a HIP graph before is refused with AR_ERR_INVALID_ARG).
+ * Forward calls do not need it: they run, and are captured, on any device
+ * until the plan is prepared, and on its device from then on. */
 ar_status_t ar_rmsnorm_prepare(ar_rmsnorm_t *plan);
 ar_rmsnorm_stats_t ar_rmsnorm_stats(const ar_rmsnorm_t *plan);
 
@@ -1015,9 +1017,8 @@ typedef struct {
  * Any output of the forward pass may be left out.  h or y may be x or
  * residual itself, dx may be dy, h or dh itself (the same pointer and
  * stride); outputs overlap nothing else.  Pointers are aligned to their
- * elements.  ntokens up to 2^31 - 65536; 0: the forward pass does nothing
- * (but prepare the plan), the backward pass makes dgain zero (accumulate:
- * leaves it).  Forward calls use no workspace and may be in flight together;
+ * elements.  ntokens up to 2^31 - 65536; 0: the forward pass does nothing,
+ * the backward pass makes dgain zero (accumulate: leaves it).  Forward calls use no workspace and may be in flight together;
  * backward calls of one plan must not overlap in time, replays of captured
  * ones included.  AR_ERR_INVALID_ARG for bad arguments or another device than
  * the plan's; AR_ERR_UNSUPPORTED for more rows than one launch grid takes (2^25 - 4

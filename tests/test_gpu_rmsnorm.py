@@ -391,3 +391,33 @@ def test_tensor_checks():
     with pytest.raises(ValueError, match="wanted"):
         B.ar_quantize_rows(x, byte_rows(4, 63), byte_rows(4, 1))
     B.ar_rmsnorm_destroy(plan)
+
+
+@pytest.mark.gpu
+def test_forward_needs_no_workspace():
+    """A program that only runs forward, eager and captured, never pays for the backward pass's workspace."""
+    t, n = 70, 1000
+    x, g = rows(t, n, torch.bfloat16, seed=1), rows(1, n, torch.bfloat16, seed=2)[0]
+    y, z = torch.zeros_like(x), torch.zeros_like(x)
+    plan = B.ar_rmsnorm_create(n, "bf16")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        B.ar_rmsnorm_forward(plan, x, g, y=y, stream=torch.cuda.current_stream())
+    assert B.ar_rmsnorm_stats(plan)["device"] == -1
+    for k in range(3):
+        x.copy_(rows(t, n, torch.bfloat16, seed=3 + k))
+        graph.replay()
+        B.ar_rmsnorm_forward(plan, x, g, y=z)
+        torch.cuda.synchronize()
+        assert torch.equal(y, z) and float(y.abs().max()) > 0
+    assert B.ar_rmsnorm_stats(plan)["device"] == -1
+    r, dx, dg = torch.ones(t, device=DEV), torch.empty_like(x), torch.empty_like(g)
+    with pytest.raises(ValueError, match="prepared"):  # the backward pass has one
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            B.ar_rmsnorm_backward(plan, x, x, g, r, dx, dg, stream=torch.cuda.current_stream())
+    B.ar_rmsnorm_backward(plan, x, x, g, r, dx, dg)
+    assert B.ar_rmsnorm_stats(plan)["device"] == 0
+    B.ar_rmsnorm_forward(plan, x, g, y=y)
+    torch.cuda.synchronize()
+    assert torch.equal(y, z)
+    B.ar_rmsnorm_destroy(plan)

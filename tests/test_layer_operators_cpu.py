@@ -286,3 +286,9 @@ def test_structs_are_as_the_header_has_them(tmp_path):
         assert packed.size == ctypes.sizeof(fields)
         made = fields.from_buffer_copy(packed.pack(*values))
         assert [getattr(made, k) for k, _ in fields._fields_] == values
+
+
+def test_rmsnorm_forward_needs_no_workspace(rms):
+    """No rows: done, without a device to prepare the plan on."""
+    B.ar_rmsnorm_forward(rms, far(0), far(1), y=far(2), ntokens=0)
+    assert B.ar_rmsnorm_stats(rms)["device"] == -1
