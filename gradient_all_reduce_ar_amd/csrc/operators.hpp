@@ -147,7 +147,7 @@ hipError_t muon_apply(const MuonArgs &a, const MuonStep &k, hipStream_t s);
 // A run of one tensor's elements, which one wave works on.
 struct NormChunk {
   int64_t at;
-  int32_t count, tensor;
+  int32_t count, unused;  // (16 bytes)
 };
 constexpr int kNormWaves = 8;  // chunks, a wave each, of a workgroup
 

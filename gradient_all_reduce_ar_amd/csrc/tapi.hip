@@ -167,13 +167,14 @@ namespace {
 // stay aligned; few gradients in one workgroup, which saves a launch, more of
 // them in enough chunks to fill the device, of 16 KiB at most (norm and
 // scaling of 174 M bf16 gradients 167 us; with 32 KiB 171, with 8 KiB 164, but 184 M
-// fp32 ones then take 371 instead of 356).
+// fp32 ones then take 371 instead of 356).  Over 2^36 gradients again more: 2^24
+// chunks and two for each tensor's ends are less than one launch takes.
 int64_t chunk_elements(int64_t count, bool bf16) {
   const int64_t piece = bf16 ? 512 : 256;
   if (count <= ar_dev::kNormWaves * 8 * piece)
     return std::max(piece, (count / ar_dev::kNormWaves + piece - 1) / piece * piece);
   const int64_t even = (count / (256 * 16) + piece - 1) / piece * piece;
-  return std::clamp<int64_t>(even, piece, 16 * piece);
+  return std::max(std::clamp<int64_t>(even, piece, 16 * piece), ((count >> 24) + piece - 1) / piece * piece);
 }
 
 ar_dev::NormArgs norm_args(const ar_norm_plan *p) {
@@ -421,24 +422,29 @@ ar_norm_plan_t *ar_norm_plan_create(int ntensors, const size_t *counts, const si
       ranges.push_back({at, next});
       if (next > at) p->arena = std::max(p->arena, next);
     }
-    const int64_t size = chunk_elements(p->count, p->bf16);
-    for (int i = 0; i < ntensors; ++i) {
-      p->first.push_back(static_cast<int32_t>(p->chunks.size()));
-      // the first cut of a tensor falls where the following ones are multiples of the chunks' size in the arena
-      for (int64_t at = ranges[i].first, end = ranges[i].second; at < end;) {
-        const int64_t to = std::min(end, at / size * size + size);
-        p->chunks.push_back({at, static_cast<int32_t>(to - at), i});
-        at = to;
-      }
-    }
-    p->first.push_back(static_cast<int32_t>(p->chunks.size()));
-    std::sort(ranges.begin(), ranges.end());
+    std::vector<std::pair<int64_t, int64_t>> sorted = ranges;
+    std::sort(sorted.begin(), sorted.end());
     int64_t end = 0;
-    for (const auto &r : ranges) {
+    for (const auto &r : sorted) {
       if (r.second == r.first) continue;
       if (r.first < end) return fail(AR_ERR_INVALID_ARG, "tensors overlap");
       end = r.second;
     }
+    const int64_t size = chunk_elements(p->count, p->bf16);
+    size_t chunks = 0;
+    for (const auto &r : ranges)
+      if (r.second > r.first) chunks += static_cast<size_t>((r.second - 1) / size - r.first / size + 1);
+    p->chunks.reserve(chunks);
+    for (int i = 0; i < ntensors; ++i) {
+      p->first.push_back(static_cast<int32_t>(p->chunks.size()));
+      // the first cut of a tensor falls where the following ones are multiples of the chunks' size in the arena
+      for (int64_t at = ranges[i].first, last = ranges[i].second; at < last;) {
+        const int64_t to = std::min(last, at / size * size + size);
+        p->chunks.push_back({at, static_cast<int32_t>(to - at), 0});
+        at = to;
+      }
+    }
+    p->first.push_back(static_cast<int32_t>(p->chunks.size()));
     return AR_OK;
   });
   if (st != AR_OK) {

@@ -292,3 +292,35 @@ def test_rmsnorm_forward_needs_no_workspace(rms):
     """No rows: done, without a device to prepare the plan on."""
     B.ar_rmsnorm_forward(rms, far(0), far(1), y=far(2), ntokens=0)
     assert B.ar_rmsnorm_stats(rms)["device"] == -1
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("counts", [[1 << 40], [1 << 37, 1 << 38, 5], [(1 << 20) - 1] * (1 << 20)], ids=["one", "three", "many"])
+def test_norm_plans_fit_a_launch(counts, dtype):
+    """Every plan within the documented limits has its chunks, a wave each and 8 to a workgroup of 512 threads, in one
+    launch (less than 2^31 threads).  A chunk takes 16 bytes of the workspace, and 8 of sums, its workgroup 8 more, a
+    tensor 4."""
+    p = B.ar_norm_plan_create(counts, dtype)
+    n = B.ar_norm_plan_stats(p)["workspace_bytes"] - 4 * (len(counts) + 1)
+    B.ar_norm_plan_destroy(p)
+    assert n / 25 < (1 << 31) // 64
+
+
+def test_norm_create_refuses_before_it_builds():
+    """Overlapping tensors are refused without the memory that their chunks would take."""
+    import subprocess
+    import sys
+
+    code = """
+import resource
+from gradient_all_reduce_ar_amd import _binding as B
+B.lib()
+pages = int(open("/proc/self/statm").read().split()[0])
+resource.setrlimit(resource.RLIMIT_AS, (pages * resource.getpagesize() + (64 << 20),) * 2)
+try:
+    B.ar_norm_plan_create([1 << 39, 1 << 39], "fp32", [0, 5])
+except B.ArError as e:
+    print(e)
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=100)
+    assert "tensors overlap" in r.stdout, r.stdout + r.stderr
