@@ -190,3 +190,56 @@ def test_large_terms_that_cancel(product, dtype, k, n, counts, tile):
     got = run({8 * g + i: v for g in range(16) for i, v in ({0: (256, 256), 1: (-256, 256)} | beside).items()})
     assert got == 384 if dtype == "fp32" else abs(got - 384) <= 96 * 2.0 ** 3
     B.ar_qexperts_destroy(c.plan)
+
+
+LONG = [  # contraction, columns, rows of each expert
+    (4240, 4368, [8000, 300]),    # more than the 32 blocks of scales that are held at once; a short last stage; short edges
+    (4368, 4240, [8000, 300]),
+    (144, 4096, [4093]),          # two stages, the second of 16 elements
+    (256, 4096, [4093]),
+    (1408, 4112, [7000]),         # an odd number of stages
+    (4096, 4112, [255, 1, 0, 256, 257, 4100]),
+    (8208, 2064, [5000]),         # three chunks of scales, the last of one block
+    (2048, 4096, [270, 0, 500, 3, 256, 1000, 30] * 4),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("product", ["forward", "input_grad"])
+@pytest.mark.parametrize("k,n,counts", LONG, ids=[f"{k}x{n}-{sum(c)}" for k, n, c in LONG])
+def test_long_tile_edges(product, k, n, counts):
+    c = Tile(product, "bf16", k, n, counts, (256, 256), extra=3)
+    c.check_all(c.run())
+    B.ar_qexperts_destroy(c.plan)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("product", ["forward", "input_grad"])
+@pytest.mark.parametrize("pad,shift", [(16, 32), (48, 16)])
+@pytest.mark.parametrize("more,off", [(0, 0), (1, 0), (5, 3), (16, 8)])
+def test_long_tile_strides(product, pad, shift, more, off):
+    """Padded rows of codes, their scales at any byte, and results at any element's address; what lies between the
+    rows of the results stays."""
+    k, n, counts = 1424, 4112, [4000, 3000]
+    c = Tile(product, "bf16", k, n, counts, (256, 256), extra=2, pad=pad, shift=shift, offsets=[64, 64 + k * n + 160])
+    flat = torch.full((c.t * (n + more) + off,), 7.0, device=DEV, dtype=T["bf16"])
+    out = flat[off:].view(c.t, n + more)[:, :n]
+    c.check_all(c.run(out))
+    assert (flat[:off] == 7).all() and (flat[off:].view(c.t, n + more)[:, n:] == 7).all()
+    B.ar_qexperts_destroy(c.plan)
+
+
+@pytest.mark.gpu
+def test_long_tile_far_rows():
+    """Rows as far apart as a stride may be: the last one of a tile 2^30 bytes from its first."""
+    k, n, counts, stride = 1424, 4112, [4000, 3000], 1 << 22
+    c = Tile("forward", "bf16", k, n, counts, (256, 256))
+    want = c.run()
+    far = torch.empty(c.t * stride, device=DEV, dtype=torch.uint8).view(c.t, stride)[:, :k]
+    far.copy_(c.x)
+    out = c.out(n)
+    B.ar_qexperts_forward(c.plan, far, c.xs, c.w, c.ws, out, c.ends)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+    c.check_all(out)
+    B.ar_qexperts_destroy(c.plan)
