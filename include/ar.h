@@ -857,8 +857,8 @@ void ar_muon_plan_destroy(ar_muon_plan_t *plan);
  * fit).  Elements outside the tensors are neither read nor written.
  *
  * Squares and sums are formed in fp64, so gradients of any size that their
- * type holds have their norm, and in a fixed order: the norm depends on the
- * inputs and the plan alone.  It stays on the device; no call waits for the
+ * type holds have their norm (infinite where fp32 does not hold it), and in a
+ * fixed order: the norm depends on the inputs and the plan alone.  It stays on the device; no call waits for the
  * host.  c is formed in fp64 from the norm and rounded to fp32, and each
  * product is rounded once to the gradients' type.  An infinite norm gives c =
  * 0 and a NaN one c = NaN, as the formula says.

@@ -301,3 +301,21 @@ def test_norm_is_the_same_at_any_address(dtype):
     assert len(set(got)) == 1, got
     assert abs(got[0][0] - ((1 << 24) + 1)) <= 1  # either neighbour of the middle
     B.ar_norm_plan_destroy(plan)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_norm_beyond_fp32(dtype):
+    """Finite gradients whose norm fp32 does not hold: infinite, and so c = 0; with a scale that it holds, the norm."""
+    g = torch.full((5000,), 3e38, device=DEV).to(T[dtype])
+    plan = B.ar_norm_plan_create([4999, 1], dtype)
+    norm, each, out = torch.zeros(1, device=DEV), torch.zeros(2, device=DEV), torch.empty_like(g)
+    B.ar_grad_norm(plan, g, norm, each)
+    B.ar_grad_clip(plan, g, norm, 1.0, out)
+    torch.cuda.synchronize()
+    assert float(norm) == float("inf") and each.tolist() == [float("inf"), float(g[0])] and (out == 0).all()
+    B.ar_grad_norm(plan, g, norm, scale=2.0 ** -10)
+    torch.cuda.synchronize()
+    want = 2.0 ** -10 * math.sqrt(5000) * float(g[0])
+    assert abs(float(norm) - want) <= NORM_TOL * want
+    B.ar_norm_plan_destroy(plan)
