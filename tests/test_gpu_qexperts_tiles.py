@@ -243,3 +243,35 @@ def test_long_tile_far_rows():
     assert torch.equal(out, want)
     c.check_all(out)
     B.ar_qexperts_destroy(c.plan)
+
+
+@pytest.mark.gpu
+@TILES
+def test_captured_and_streams(product, dtype, k, n, counts, tile):
+    """In a graph, replayed on changing rows with eager calls between; calls of one plan on two streams; the same
+    bits every time."""
+    c = Tile(product, dtype, k, n, counts, tile, extra=1)
+    f = B.ar_qexperts_input_grad if c.grad else B.ar_qexperts_forward
+    codes, scales = c.rows()
+    B.ar_qexperts_prepare(c.plan)
+    graph, out = torch.cuda.CUDAGraph(), c.out(n)
+    with torch.cuda.graph(graph):
+        f(c.plan, codes, scales, c.w, c.ws, out, c.ends, torch.cuda.current_stream())
+    for i in range(3):
+        codes.copy_(c.codes(c.t, k)[0])
+        c.ends.copy_(torch.tensor([counts[0] - i, sum(counts) - i], dtype=torch.int32))
+        out.fill_(7)
+        graph.replay()
+        got = c.run()
+        assert torch.equal(out, got)
+    c.counts = [counts[0] - 2, counts[1]]
+    c.check_all(got)
+    streams, outs = [torch.cuda.Stream() for _ in range(2)], []
+    for _ in range(3):
+        for s in streams:
+            with torch.cuda.stream(s):
+                outs.append(c.out(n))
+                f(c.plan, codes, scales, c.w, c.ws, outs[-1], c.ends, s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, got) for o in outs)
+    B.ar_qexperts_destroy(c.plan)
